@@ -10,6 +10,7 @@
 #include <mutex>
 #include <utility>
 
+#include "lowp.h"
 #include "ozk_internal.h"
 
 namespace ozk {
@@ -781,9 +782,13 @@ int ozk_dgemm_host_async(int64_t M, int64_t N, int64_t K, const double* A, int64
 
 int ozk_stream_status(ozk_stream_t stream) {
   int status = 0;
-  const int rc = take_device_status(reinterpret_cast<cudaStream_t>(stream), &status);
+  int rc = take_device_status(reinterpret_cast<cudaStream_t>(stream), &status);
   if (rc) return rc;
-  return status ? OZK_ERR_TIMEOUT : OZK_OK;
+  int products = 0;
+  rc = take_product_status(&products);
+  if (rc) return rc;
+  if (status || (products & 1)) return OZK_ERR_TIMEOUT;
+  return products ? OZK_ERR_INVALID_ARG : OZK_OK;
 }
 
 int ozk_release_cached(void) {

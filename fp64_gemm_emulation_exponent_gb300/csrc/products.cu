@@ -1,0 +1,739 @@
+// Low-precision products on the tensor cores: rows grouped by expert with
+// 16-bit operands (forward and both gradients), and microscaled 4-bit
+// operands (one group or many).
+//
+// One tile is kTileRows (or, on a CTA pair, twice that) output columns by up
+// to BN output rows of one group.  The operand with few rows of its own (the
+// grouped rows) takes the N side of tcgen05.mma and the weights the M side:
+// N may be any multiple of 16, so a group of three rows costs the tensor
+// cores and the copies three rows' worth, not a tile's, and the weights,
+// which bound small calls, stream through whole.
+//   forward, 4-bit   out[t, m] = sum_k x[t, k] w[e][m, k]     both K-major
+//   gradient of x    out[t, m] = sum_k dy[t, k] w[e][k, m]    w M-major
+//   gradient of w    out[e][n, m] = sum_t dy[t, n] x[t, m]    both MN-major,
+//                    the group's rows are the reduction
+// The MN-major operands are read as they lie (tcgen05's transposed operand
+// form), nothing is transposed in memory.
+//
+// Roles of a CTA (12 warps): warp 0 issues the TMA loads, warp 1 the MMAs,
+// warp 2 (gradient of w) clears the rows past a group's end in its last
+// block, warps 4..11 the epilogue.  Every mbarrier wait is bounded; a wait
+// that runs out latches the fault, stops the CTA's roles, drains and returns.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cstring>
+#include <map>
+#include <mutex>
+
+#include "lowp.h"
+#include "tc_ptx.cuh"
+
+namespace ozk {
+namespace {
+
+constexpr int kTileRows = 128;   // M side of one CTA: TMEM lanes
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
+constexpr uint32_t kRowBytes = 128;                       // K bytes of a stage: one swizzle row
+constexpr uint32_t kABytes = kTileRows * kRowBytes;       // 16 KB
+constexpr uint32_t kScaleTile = 512;                      // 128 rows x 4 scale bytes
+constexpr int kSuper = 16;       // tile rows of the M side that run together (L2 reuse)
+
+// Formats of an instance.  k16: 16-bit operands; the 4-bit ones differ in the
+// MMA's kind and in how many blocks a step of 64 takes (4 scale bytes, or 2).
+enum Format { kNv = OZK_NVFP4, kMx = OZK_MXFP4, k16 = 2 };
+
+template <ProductOp OP, int FMT, int BN_, bool PAIR_>
+struct Config {
+  static constexpr bool PAIR = PAIR_;
+  static constexpr int BN = BN_;
+  static constexpr bool MX = OP == kMx4;
+  static constexpr bool A_MN = OP == kGradRows || OP == kGradWeights;  // M side read across K
+  static constexpr bool B_MN = OP == kGradWeights;
+  static constexpr int CTAS = PAIR ? 2 : 1;
+  static constexpr int BLOCK_K = MX ? 256 : 64;          // K elements of a stage
+  static constexpr int MMA_K = MX ? 64 : 16;             // of one MMA: 32 bytes
+  static constexpr int B_ROWS = BN / CTAS;               // N rows a CTA stages
+  static constexpr int BOX = B_MN ? 64 : (BN >= 256 ? 64 : 32);  // rows of one B copy
+  static constexpr uint32_t B_BYTES = B_ROWS * kRowBytes;
+  static constexpr uint32_t BOX_BYTES = (B_MN ? 64 : BOX) * kRowBytes;
+  static constexpr int KG = FMT == kNv ? 4 : 2;          // scale words of a stage
+  static constexpr int NB = (BN + 127) / 128;            // 128-row scale tiles of the N side
+  static constexpr uint32_t SFA_BYTES = MX ? KG * kScaleTile : 0;
+  static constexpr uint32_t SFB_BYTES = MX ? NB * KG * kScaleTile : 0;
+  static constexpr uint32_t STAGE = kABytes + B_BYTES + SFA_BYTES + SFB_BYTES;
+  static constexpr int STAGES = MX ? 5 : 6;
+  static constexpr int BUFS = BN >= 256 && MX ? 1 : 2;
+  static constexpr uint32_t SF_COLS = MX ? KG * 4 + KG * 4 * NB : 0;
+  static constexpr uint32_t SF_BASE = BUFS * BN;
+  static constexpr uint32_t TMEM = BUFS * BN + SF_COLS <= 256 ? 256 : 512;
+  static_assert(BUFS * BN + SF_COLS <= 512, "TMEM");
+  // full, empty and tail per stage; accumulator full and empty; drain
+  static constexpr int BARS = 3 * STAGES + 5;
+  static constexpr uint32_t FIXED = 1024 + STAGES * STAGE + 256;
+  static_assert(8 * BARS + 8 <= 256, "barriers");
+  static_assert(BN % 32 == 0 && B_ROWS % BOX == 0, "tile");
+};
+
+struct ProductParams {
+  int T, M, N, K;
+  int groups, tiles_m, tiles_n;  // tiles_n: of a group (gradient of w only)
+  const int32_t* offsets;
+  void* out;
+  int out_type;
+  int64_t ldo, out_group;
+  float alpha;
+  uint32_t idesc;  // types, majorness, M; N is filled in per tile
+};
+
+__device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+
+// Shared-memory matrix descriptors, 128-byte swizzle, version 1.  K-major:
+// rows of 128 bytes of K, 8-row groups 1024 bytes apart.  MN-major: slabs of
+// 64 rows-or-columns (128 bytes) by 64 of K; 8 of K are 1024 bytes (the
+// stride offset), the next 64 rows-or-columns a slab of 8 KB away (the
+// leading offset).
+template <bool MN>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+  constexpr uint64_t lead = MN ? 8192 >> 4 : 1;
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (lead << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+// Of one 512-byte scale tile: 32 rows of 16 bytes, 8-row groups 128 bytes apart, no swizzle.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (1ull << 16) | (static_cast<uint64_t>(128 >> 4) << 32) |
+         (1ull << 46);
+}
+
+// One scale tile into four TMEM columns, the same in every lane quadrant.
+// Copies and MMAs issued by one thread run in the order they were issued.
+template <bool PAIR>
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
+  if (PAIR)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+#define OZK_MMA_SCALED(GROUP, KIND)                                                                              \
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                                 \
+               "tcgen05.mma." GROUP "." KIND " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),                  \
+               "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)                                          \
+               : "memory")
+template <int FMT, bool PAIR>
+__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                           uint32_t sfb, uint32_t acc) {
+  if (FMT == kNv) {
+    if (PAIR) OZK_MMA_SCALED("cta_group::2", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+    else OZK_MMA_SCALED("cta_group::1", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+  } else {
+    if (PAIR) OZK_MMA_SCALED("cta_group::2", "kind::mxf4.block_scale.scale_vec::2X");
+    else OZK_MMA_SCALED("cta_group::1", "kind::mxf4.block_scale.scale_vec::2X");
+  }
+}
+#undef OZK_MMA_SCALED
+
+// ---------------------------------------------------------------------------
+// The schedule
+// ---------------------------------------------------------------------------
+// Group table in shared memory: first tile, first row and rows of each group.
+struct Groups {
+  int* first;  // groups + 1
+  int* row0;
+  int* rows;
+};
+
+// Fills the table (one warp).  Offsets outside [0, T] or running backwards
+// are cut to an empty or shorter group, so every access stays inside the
+// operands, and latched as a fault.
+template <typename C, ProductOp OP>
+__device__ __forceinline__ void build_groups(const ProductParams& p, const Groups& g, int lane) {
+  int carry = 0;
+  for (int b = 0; b < p.groups; b += 32) {
+    const int e = b + lane;
+    int lo = 0, hi = 0;
+    if (e < p.groups) {
+      lo = p.offsets ? p.offsets[e] : 0;
+      hi = p.offsets ? p.offsets[e + 1] : p.T;
+      if (lo < 0 || hi < lo || hi > p.T) {
+        atomicOr(&g_status, 2);
+        lo = min(max(lo, 0), p.T);
+        hi = min(max(hi, lo), p.T);
+      }
+    }
+    int tiles = 0;
+    if (e < p.groups) tiles = (OP == kGradWeights ? p.tiles_n : (hi - lo + C::BN - 1) / C::BN) * p.tiles_m;
+    int sum = tiles;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+      if (lane >= d) sum += v;
+    }
+    if (e < p.groups) {
+      g.first[e] = carry + sum - tiles;
+      g.row0[e] = lo;
+      g.rows[e] = hi - lo;
+    }
+    carry += __shfl_sync(0xFFFFFFFFu, sum, 31);
+  }
+  if (lane == 0) g.first[p.groups] = carry;
+}
+
+struct Tile {
+  int e, row0;     // group and its first row
+  int m0, n0;      // first output column; first output row within the group
+  int n;           // output rows of the tile
+  int half;        // N rows of each CTA (all of them on a single CTA), MMA N = CTAS * half
+  int k, blocks;   // terms, and stages they take
+};
+
+template <typename C, ProductOp OP>
+__device__ __forceinline__ Tile tile_at(const ProductParams& p, const Groups& g, int u, int& e) {
+  while (u >= g.first[e + 1]) ++e;  // u only grows
+  Tile t;
+  t.e = e;
+  t.row0 = g.row0[e];
+  const int in = u - g.first[e];
+  const int total_n = OP == kGradWeights ? p.N : g.rows[e];
+  const int tn = (total_n + C::BN - 1) / C::BN;
+  const int super = in / (kSuper * tn);
+  const int gm = min(kSuper, p.tiles_m - super * kSuper);
+  const int r = in - super * kSuper * tn;
+  t.m0 = (super * kSuper + r % gm) * (kTileRows * C::CTAS);
+  t.n0 = r / gm * C::BN;
+  t.n = min(C::BN, total_n - t.n0);
+  t.half = C::PAIR ? (t.n + 31) / 32 * 16 : (t.n + 15) / 16 * 16;
+  t.k = OP == kGradWeights ? g.rows[e] : p.K;
+  t.blocks = (t.k + C::BLOCK_K - 1) / C::BLOCK_K;
+  return t;
+}
+
+// The gradient of w reduces over a group's rows: where the last MMA step
+// (16 rows) reaches past the group's end, the rows after it belong to the
+// next group and must not enter the sum, whatever they hold.
+template <ProductOp OP>
+__device__ __forceinline__ bool has_tail(const Tile& t) {
+  return OP == kGradWeights && t.k % 16 != 0;
+}
+
+// ---------------------------------------------------------------------------
+// Epilogue: 32 accumulator columns (output rows n0 .. n0 + 31) of 32 TMEM
+// lanes (consecutive output columns).
+// ---------------------------------------------------------------------------
+template <typename T>
+__device__ __forceinline__ T out_of(float v) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) return __float2bfloat16_rn(v);
+  else if constexpr (std::is_same<T, __half>::value) return __float2half_rn(v);
+  else return v;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_block(T* out, int64_t ldo, int rows, bool in_m, const uint32_t (&v)[32], float alpha) {
+#pragma unroll
+  for (int c = 0; c < 32; ++c)
+    if (c < rows && in_m) out[c * ldo] = out_of<T>(__uint_as_float(v[c]) * alpha);
+}
+
+template <ProductOp OP, int FMT, int BN, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1)
+    product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+                   const ProductParams p) {
+  using C = Config<OP, FMT, BN, PAIR>;
+  grid_dependency_sync();
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  const uint32_t sA = smem_u32(smem);
+  const uint32_t sB = sA + C::STAGES * kABytes;
+  const uint32_t sSA = sB + C::STAGES * C::B_BYTES;
+  const uint32_t sSB = sSA + C::STAGES * C::SFA_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::BARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  Groups g;
+  g.first = reinterpret_cast<int*>(smem + C::STAGES * C::STAGE + 256);
+  g.row0 = g.first + p.groups + 1;
+  g.rows = g.row0 + p.groups;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_rank() : 0;
+  const bool leader = rank == 0;
+  const uint32_t full0 = smem_u32(bars);
+  const uint32_t empty0 = full0 + 8 * C::STAGES;
+  const uint32_t accf0 = empty0 + 8 * C::STAGES;
+  const uint32_t acce0 = accf0 + 16;
+  const uint32_t drain = acce0 + 16;
+  const uint32_t tail0 = drain + 8;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      // on a pair that clears tails, both CTAs say when their part is in place
+      mbar_init(full0 + 8 * s, PAIR && OP == kGradWeights ? 2 : 1);
+      mbar_init(empty0 + 8 * s, 1);
+      mbar_init(tail0 + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(accf0 + 8 * b, 1);
+      mbar_init(acce0 + 8 * b, C::CTAS * kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+  }
+  if (warp == 1) {
+    if (PAIR) {
+      tmem_alloc_pair(smem_u32(tmem_slot), C::TMEM);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(tmem_slot), C::TMEM);
+      tmem_relinquish();
+    }
+  }
+  if (warp == 2) build_groups<C, OP>(p, g, lane);
+  tc_fence_before();
+  __syncthreads();
+  if (PAIR) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  const int units = g.first[p.groups];
+  const int unit0 = static_cast<int>(blockIdx.x) / C::CTAS, unit_step = static_cast<int>(gridDim.x) / C::CTAS;
+
+  if (warp == 0) {
+    // ------------------------------ TMA producer ------------------------------
+    if (lane == 0) {
+      int stage = 0, e = 0;
+      uint32_t phase = 0;
+      int issued_parity[C::STAGES];
+      for (int s = 0; s < C::STAGES; ++s) issued_parity[s] = -1;
+      uint32_t tails = 0;  // bit s: parity of the next tail in stage s
+      int tail_stage = -1;
+      bool ok = true;
+      for (int u = unit0; u < units && ok; u += unit_step) {
+        const Tile t = tile_at<C, OP>(p, g, u, e);
+        const int m0 = t.m0 + static_cast<int>(rank) * kTileRows;
+        const int n0 = t.n0 + static_cast<int>(rank) * t.half;
+        const int boxes = (t.half + C::BOX - 1) / C::BOX;
+        const uint32_t bytes = kABytes + static_cast<uint32_t>(boxes) * C::BOX_BYTES + C::SFA_BYTES + C::SFB_BYTES;
+        for (int kb = 0; kb < t.blocks; ++kb) {
+          if (!mbar_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, kTimeoutNs)) {
+            ok = false;
+            break;
+          }
+          const bool clear = has_tail<OP>(t) && kb == t.blocks - 1;
+          uint32_t bar = full0 + 8 * stage;
+          if (clear) {  // warp 2 passes the stage on once it has cleared the rows
+            bar = tail0 + 8 * stage;
+            mbar_expect_tx(bar, bytes);
+            tails ^= 1u << stage;
+            tail_stage = stage;
+          } else if (!PAIR) {
+            mbar_expect_tx(bar, bytes);
+          } else {
+            if (leader) mbar_expect_tx(bar, 2 * bytes);
+            bar = cluster_addr(bar, 0);
+            if (OP == kGradWeights && !leader) mbar_arrive_cluster(bar);
+          }
+          auto load2 = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1) {
+            if (PAIR) tma_load_2d_pair(dst, map, c0, c1, clear ? cluster_addr(bar, rank) : bar);
+            else tma_load_2d(dst, map, c0, c1, bar);
+          };
+          auto load3 = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2) {
+            if (PAIR) tma_load_3d_pair(dst, map, c0, c1, c2, bar);
+            else tma_load_3d(dst, map, c0, c1, c2, bar);
+          };
+          const uint32_t a = sA + stage * kABytes, b = sB + stage * C::B_BYTES;
+          const int k0 = kb * C::BLOCK_K;
+          if constexpr (OP == kForward) load3(a, &tmA, k0, m0, t.e);
+          if constexpr (OP == kMx4) load3(a, &tmA, k0 / 2, m0, t.e);
+          if constexpr (OP == kGradRows) {
+            load3(a, &tmA, m0, k0, t.e);
+            load3(a + kABytes / 2, &tmA, m0 + 64, k0, t.e);
+          }
+          if constexpr (OP == kGradWeights) {
+            load2(a, &tmA, m0, t.row0 + k0);
+            load2(a + kABytes / 2, &tmA, m0 + 64, t.row0 + k0);
+          }
+          for (int j = 0; j < boxes; ++j) {
+            if constexpr (OP == kGradWeights) load2(b + j * C::BOX_BYTES, &tmB, n0 + 64 * j, t.row0 + k0);
+            else load2(b + j * C::BOX_BYTES, &tmB, C::MX ? k0 / 2 : k0, t.row0 + n0 + C::BOX * j);
+          }
+          if constexpr (C::MX) {
+            // scale tiles: of these 128 weight rows, and of the tile's rows (both CTAs: all of them)
+            const int64_t wrow = static_cast<int64_t>(t.e) * p.M;
+            load3(sSA + stage * C::SFA_BYTES, &tmSA, 0, kb * C::KG, static_cast<int>(wrow / 128) + t.e + m0 / 128);
+            load3(sSB + stage * C::SFB_BYTES, &tmSB, 0, kb * C::KG, t.row0 / 128 + t.e + t.n0 / 128);
+          }
+          if (!clear) issued_parity[stage] = static_cast<int>(phase);
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {  // let copies still in flight land before the CTA exits
+        if (leader)
+          for (int s = 0; s < C::STAGES; ++s)
+            if (issued_parity[s] >= 0) mbar_wait_drain(full0 + 8 * s, static_cast<uint32_t>(issued_parity[s]));
+        if (tail_stage >= 0) mbar_wait_drain(tail0 + 8 * tail_stage, ((tails >> tail_stage) & 1u) ^ 1u);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1 && leader) {
+    // ------------------------------ MMA issuer ------------------------------
+    if (lane == 0) {
+      int stage = 0, e = 0, ab = 0;
+      uint32_t phase = 0, aphase = 0;
+      bool ok = true;
+      for (int u = unit0; u < units && ok; u += unit_step) {
+        const Tile t = tile_at<C, OP>(p, g, u, e);
+        if (t.blocks == 0) continue;
+        if (!mbar_wait(acce0 + 8 * ab, aphase ^ 1u, abort_flag, kTimeoutNs)) break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + static_cast<uint32_t>(ab * BN);
+        const uint32_t idesc = p.idesc | (static_cast<uint32_t>(t.half * C::CTAS >> 3) << 17);
+        for (int kb = 0; kb < t.blocks; ++kb) {
+          if (!mbar_wait(full0 + 8 * stage, phase, abort_flag, kTimeoutNs)) {
+            ok = false;
+            break;
+          }
+          if (PAIR && OP == kGradWeights) mbar_test_cluster(full0 + 8 * stage, phase);  // acquire the peer's clearing
+          tc_fence_after();
+          const uint64_t da = operand_desc<C::A_MN>(sA + stage * kABytes);
+          const uint64_t db = operand_desc<C::B_MN>(sB + stage * C::B_BYTES);
+          const int steps = min(4, (t.k - kb * C::BLOCK_K + C::MMA_K - 1) / C::MMA_K);
+          if constexpr (C::MX) {
+            const uint32_t sfa = tmem_base + C::SF_BASE, sfb = sfa + 4 * C::KG;
+#pragma unroll
+            for (int i = 0; i < C::KG; ++i) {
+              copy_scales<PAIR>(sfa + 4 * i, scale_desc(sSA + stage * C::SFA_BYTES + i * kScaleTile));
+#pragma unroll
+              for (int r = 0; r < C::NB; ++r)
+                copy_scales<PAIR>(sfb + 4 * (C::NB * i + r),
+                                  scale_desc(sSB + stage * C::SFB_BYTES + (r * C::KG + i) * kScaleTile));
+            }
+            for (int s = 0; s < steps; ++s) {
+              const int word = FMT == kNv ? s : s / 2;                       // scale word of the step
+              const uint32_t id = FMT == kNv ? 0u : 2u * (s & 1);            // its first byte
+              mma_scaled<FMT, PAIR>(d, da + 2ull * s, db + 2ull * s, idesc | (id << 4) | (id << 29), sfa + 4 * word,
+                                    sfb + 4 * C::NB * word, (kb > 0 || s > 0) ? 1u : 0u);
+            }
+          } else {
+            // 32 bytes of K, or 16 rows of 128 bytes
+            constexpr uint64_t step_a = C::A_MN ? (16 * kRowBytes) >> 4 : 2, step_b = C::B_MN ? (16 * kRowBytes) >> 4 : 2;
+            for (int s = 0; s < steps; ++s) {
+              const uint32_t acc = (kb > 0 || s > 0) ? 1u : 0u;
+              if (PAIR) mma_f16_pair(d, da + step_a * s, db + step_b * s, idesc, acc);
+              else mma_f16(d, da + step_a * s, db + step_b * s, idesc, acc);
+            }
+          }
+          if (PAIR) mma_commit_both(empty0 + 8 * stage);
+          else mma_commit(empty0 + 8 * stage);
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if (PAIR) mma_commit_both(accf0 + 8 * ab);
+        else mma_commit(accf0 + 8 * ab);
+        if (++ab == C::BUFS) {
+          ab = 0;
+          aphase ^= 1u;
+        }
+      }
+      if (PAIR) mma_commit_local(drain);
+      else mma_commit(drain);
+      mbar_wait_drain(drain, 0);
+    }
+    __syncwarp();
+  } else if (warp == 2 && OP == kGradWeights) {
+    // ------------------------------ tails ------------------------------
+    int e = 0;
+    unsigned pos = 0;  // stages the producer has filled before this tile
+    uint32_t tails = 0;
+    for (int u = unit0; u < units; u += unit_step) {
+      const Tile t = tile_at<C, OP>(p, g, u, e);
+      if (t.blocks > 0 && has_tail<OP>(t)) {
+        const int stage = static_cast<int>((pos + t.blocks - 1) % C::STAGES);
+        if (!warp_wait(tail0 + 8 * stage, (tails >> stage) & 1u, abort_flag, kTimeoutNs)) break;
+        tails ^= 1u << stage;
+        const int r0 = t.k % 64;                 // first row past the group's end; the MMAs stop at the next 16
+        const int r1 = (r0 + 15) / 16 * 16;
+        const int slabs_b = (t.half + 63) / 64;
+        const int chunks = (r1 - r0) * 8;        // 16-byte pieces of one slab
+        for (int i = lane; i < chunks * (2 + slabs_b); i += 32) {
+          const int slab = i / chunks, at = (r0 * 128) + (i - slab * chunks) * 16;
+          const uint32_t base = slab < 2 ? sA + stage * kABytes + slab * 8192
+                                         : sB + stage * C::B_BYTES + (slab - 2) * 8192;
+          st_shared_v4(base + static_cast<uint32_t>(at), 0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR) mbar_arrive_cluster(cluster_addr(full0 + 8 * stage, 0));
+          else mbar_arrive(full0 + 8 * stage);
+        }
+      }
+      pos += static_cast<unsigned>(t.blocks);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------ epilogue ------------------------------
+    const int quad = warp & 3, side = (warp - 4) >> 2;  // TMEM lanes 32 quad..; every other block of 32 columns
+    int e = 0, ab = 0;
+    uint32_t aphase = 0;
+    for (int u = unit0; u < units; u += unit_step) {
+      const Tile t = tile_at<C, OP>(p, g, u, e);
+      const int64_t m = t.m0 + static_cast<int>(rank) * kTileRows + quad * 32 + lane;
+      const bool in_m = m < p.M;
+      int64_t at = m;
+      if (OP == kGradWeights) at += t.e * p.out_group + static_cast<int64_t>(t.n0) * p.ldo;
+      else at += (static_cast<int64_t>(t.row0) + t.n0) * p.ldo;
+      const bool has = t.blocks > 0;
+      if (has) {
+        if (!warp_wait(accf0 + 8 * ab, aphase, abort_flag, kTimeoutNs)) break;
+        tc_fence_after();
+      }
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(ab * BN);
+      for (int c = 32 * side; c < t.n; c += 64) {
+        uint32_t v[32];
+        if (has) {
+          tmem_ld32(taddr + static_cast<uint32_t>(c), v);
+          tmem_wait_ld(v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0u;
+        }
+        const int64_t o = at + c * p.ldo;
+        const int rows = t.n - c;
+        if (p.out_type == OZK_F32) store_block(static_cast<float*>(p.out) + o, p.ldo, rows, in_m, v, p.alpha);
+        else if (p.out_type == OZK_F16) store_block(static_cast<__half*>(p.out) + o, p.ldo, rows, in_m, v, p.alpha);
+        else store_block(static_cast<__nv_bfloat16*>(p.out) + o, p.ldo, rows, in_m, v, p.alpha);
+      }
+      if (has) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR) mbar_arrive_cluster(cluster_addr(acce0 + 8 * ab, 0));
+          else mbar_arrive(acce0 + 8 * ab);
+        }
+        if (++ab == C::BUFS) {
+          ab = 0;
+          aphase ^= 1u;
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (PAIR) cluster_sync();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    if (PAIR) tmem_dealloc_pair(tmem_base, C::TMEM);
+    else tmem_dealloc(tmem_base, C::TMEM);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+bool make_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const int64_t* dims,
+              const int64_t* strides, const uint32_t* box, bool swizzle) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t d[3], s[2];
+  cuuint32_t b[3];
+  const cuuint32_t step[3] = {1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = static_cast<cuuint64_t>(std::max<int64_t>(dims[i], 1));
+    b[i] = box[i];
+    if (i) s[i - 1] = static_cast<cuuint64_t>(strides[i - 1]);
+  }
+  return enc(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, s, b, step,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Once per device and kernel: the shared-memory opt-in, and for pairs the
+// number of clusters that fit the GPU at once.
+cudaError_t setup(const void* kernel, size_t smem, bool pair, int* resident) {
+  struct Setup {
+    cudaError_t err;
+    int resident;
+  };
+  static std::mutex mu;
+  static std::map<std::pair<int, const void*>, Setup> done;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  auto it = done.find({dev, kernel});
+  if (it == done.end()) {
+    Setup s{cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)), 0};
+    if (s.err == cudaSuccess && pair) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim = {2, 1, 1};
+      cfg.blockDim = dim3(kThreads);
+      cfg.gridDim = dim3(2);
+      cfg.dynamicSmemBytes = smem;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      s.err = cudaOccupancyMaxActiveClusters(&s.resident, kernel, &cfg);
+      if (s.err == cudaSuccess && s.resident < 1) s.err = cudaErrorInvalidConfiguration;
+    }
+    it = done.emplace(std::make_pair(dev, kernel), s).first;
+  }
+  *resident = it->second.resident;
+  return it->second.err;
+}
+
+template <ProductOp OP, int FMT, int BN, bool PAIR>
+cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
+  using C = Config<OP, FMT, BN, PAIR>;
+  ProductParams p = {};
+  p.T = static_cast<int>(q.T);
+  p.M = static_cast<int>(q.M);
+  p.N = static_cast<int>(q.N);
+  p.K = static_cast<int>(q.K);
+  p.groups = q.groups;
+  p.offsets = q.offsets;
+  p.out = q.out;
+  p.out_type = q.out_type;
+  p.ldo = q.ldo;
+  p.out_group = q.out_group;
+  p.alpha = q.alpha;
+  const int64_t tile_m = kTileRows * C::CTAS;
+  p.tiles_m = static_cast<int>((q.M + tile_m - 1) / tile_m);
+  p.tiles_n = static_cast<int>((q.N + BN - 1) / BN);
+  // D fp32; types; MN-major operands; M of the MMA
+  p.idesc = static_cast<uint32_t>(tile_m >> 4) << 24;
+  if (C::MX) p.idesc |= (1u << 7) | (1u << 10) | (FMT == kMx ? 1u << 23 : 0u);
+  else
+    p.idesc |= (1u << 4) | (q.dtype == OZK_BF16 ? (1u << 7) | (1u << 10) : 0u) | (C::A_MN ? 1u << 15 : 0u) |
+               (C::B_MN ? 1u << 16 : 0u);
+
+  CUtensorMap tmA, tmB, tmSA, tmSB;
+  std::memset(&tmA, 0, sizeof tmA);
+  std::memset(&tmB, 0, sizeof tmB);
+  std::memset(&tmSA, 0, sizeof tmSA);
+  std::memset(&tmSB, 0, sizeof tmSB);
+  const bool loads = q.T > 0 && q.K != 0;  // otherwise no tile has a term, and nothing is read
+  if (loads && !C::MX) {
+    const CUtensorMapDataType type = q.dtype == OZK_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const int64_t inner_rows = OP == kGradWeights ? q.N : q.K;
+    const int64_t dims_b[2] = {inner_rows, q.T}, strides_b[1] = {2 * q.ld_rows};
+    const uint32_t box_b[2] = {64, C::B_MN ? 64u : static_cast<uint32_t>(C::BOX)};
+    if (!make_map(&tmB, type, 2, q.rows, dims_b, strides_b, box_b, true)) return cudaErrorInvalidValue;
+    bool ok;
+    if (OP == kGradWeights) {
+      const int64_t dims[2] = {q.M, q.T}, strides[1] = {2 * q.ld_other};
+      const uint32_t box[2] = {64, 64};
+      ok = make_map(&tmA, type, 2, q.other, dims, strides, box, true);
+    } else {
+      const int64_t dims[3] = {OP == kForward ? q.K : q.M, OP == kForward ? q.M : q.K, q.groups};
+      const int64_t strides[2] = {2 * q.ld_other, 2 * q.other_group};
+      const uint32_t box[3] = {64, OP == kForward ? 128u : 64u, 1};
+      ok = make_map(&tmA, type, 3, q.other, dims, strides, box, true);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+  }
+  if (loads && C::MX) {
+    const int64_t half = ozk_kpad(q.K) / 2, kg = mx4_kgroups(q.K, FMT);
+    const int64_t dims_a[3] = {half, q.M, q.groups}, strides_a[2] = {half, half * q.M};
+    const uint32_t box_a[3] = {kRowBytes, kTileRows, 1};
+    const int64_t dims_b[2] = {half, q.T}, strides_b[1] = {half};
+    const uint32_t box_b[2] = {kRowBytes, static_cast<uint32_t>(C::BOX)};
+    const int64_t strides_s[2] = {kScaleTile, kScaleTile * kg};
+    const int64_t dims_sa[3] = {kScaleTile / 4, kg, mx4_row_blocks(q.b.rows, q.b.groups)};
+    const int64_t dims_sb[3] = {kScaleTile / 4, kg, mx4_row_blocks(q.T, q.groups)};
+    const uint32_t box_sa[3] = {kScaleTile / 4, C::KG, 1}, box_sb[3] = {kScaleTile / 4, C::KG, C::NB};
+    if (!make_map(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, q.b.codes, dims_a, strides_a, box_a, true) ||
+        !make_map(&tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, q.a.codes, dims_b, strides_b, box_b, true) ||
+        !make_map(&tmSA, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, q.b.scales, dims_sa, strides_s, box_sa, false) ||
+        !make_map(&tmSB, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, q.a.scales, dims_sb, strides_s, box_sb, false))
+      return cudaErrorInvalidValue;
+  }
+  auto kernel = product_kernel<OP, FMT, BN, PAIR>;
+  const size_t table = (3 * static_cast<size_t>(q.groups) + 1) * sizeof(int);
+  int resident = 0;
+  cudaError_t e = setup(reinterpret_cast<const void*>(kernel),
+                        C::FIXED + (3 * static_cast<size_t>(kMaxGroups) + 1) * sizeof(int), PAIR, &resident);
+  if (e != cudaSuccess) return e;
+  // no more CTAs than there can be tiles; how many there are only the offsets say
+  int64_t tiles = p.tiles_m;
+  if (OP == kGradWeights) tiles *= static_cast<int64_t>(p.tiles_n) * q.groups;
+  else tiles *= std::min<int64_t>(q.T, q.T / BN + q.groups);
+  if (tiles == 0) return cudaSuccess;
+  int64_t slots = PAIR ? std::min(num_sms / 2, resident) : num_sms;
+  slots = std::min(slots, tiles);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cfg.gridDim = dim3(static_cast<unsigned>(slots * C::CTAS));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::FIXED + table;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see grid_dependency_sync
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 1;
+  if (PAIR) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {2, 1, 1};
+    cfg.numAttrs = 2;
+  }
+  cfg.attrs = attr;
+  return cudaLaunchKernelEx(&cfg, kernel, tmA, tmB, tmSA, tmSB, p);
+}
+
+template <ProductOp OP, int FMT>
+cudaError_t choose(const Product& q, int num_sms, cudaStream_t stream) {
+  return launch<OP, FMT, 128, false>(q, num_sms, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_product(const Product& q, int num_sms, cudaStream_t stream) {
+  switch (q.op) {
+    case kForward: return choose<kForward, k16>(q, num_sms, stream);
+    case kGradRows: return choose<kGradRows, k16>(q, num_sms, stream);
+    case kGradWeights: return choose<kGradWeights, k16>(q, num_sms, stream);
+    default:
+      return q.a.format == OZK_MXFP4 ? choose<kMx4, kMx>(q, num_sms, stream) : choose<kMx4, kNv>(q, num_sms, stream);
+  }
+}
+
+int take_product_status(int* status) { return take_status(status); }
+
+}  // namespace ozk

@@ -349,6 +349,110 @@ int ozk_crt_lift(int64_t M, int64_t N, int n_moduli, const void* in, int in_kind
                  int64_t ldi, int splits, uint32_t* X, ozk_stream_t stream);
 
 /* ------------------------------------------------------------------ */
+/* Products at a model's precision: microscaled 4-bit floating point,  */
+/* and rows grouped by expert.                                         */
+/* ------------------------------------------------------------------ */
+/* Conventions beside the general ones (row-major, leading dimensions in
+ * elements, stream order, argument errors before anything is launched):
+ *  - Groups ("experts"): the T rows of x are sorted by group; offsets is a
+ *    device array of groups + 1 int32 with offsets[g] <= offsets[g + 1], rows
+ *    offsets[g] .. offsets[g + 1] - 1 belonging to group g (any number of
+ *    them, none included).  It is read on the device, in stream order, so a
+ *    router's result needs no copy to the host and a captured graph may be
+ *    replayed with other offsets.  Rows before offsets[0] and from
+ *    offsets[groups] on belong to no group: no result is written for them.
+ *    Offsets outside [0, T] or running backwards are cut to shorter groups
+ *    and reported by ozk_stream_status as OZK_ERR_INVALID_ARG.  At most
+ *    OZK_MAX_GROUPS groups.
+ *  - Sums are formed in fp32 on the tensor cores and rounded once, to the
+ *    output's type.  The order of a sum depends on the sizes alone: the same
+ *    call gives the same bits.  An Inf or NaN reaches only the results whose
+ *    sums it enters: never another group's, and not a row's or column's that
+ *    lies beside it in memory.
+ *  - No workspace is used and nothing is allocated; after one call of a kind
+ *    on the device every call can be captured into a CUDA graph.
+ *  - Sizes up to 2^30 rows, 2^22 columns; beyond them OZK_ERR_UNSUPPORTED. */
+#define OZK_MAX_GROUPS 1024
+
+typedef enum { OZK_BF16 = 0, OZK_F16 = 1, OZK_F32 = 2, OZK_F64 = 3 } ozk_dtype;
+
+/* Microscaled 4-bit formats: blocks of consecutive elements of a row, E2M1
+ * codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign) and one scale byte a block.
+ * NVFP4: 16 elements under an E4M3 scale.  MXFP4: 32 under a power of two
+ * (E8M0). */
+typedef enum { OZK_NVFP4 = 0, OZK_MXFP4 = 1 } ozk_mx4_format;
+
+/* Bytes of the scales of a rows x K matrix in `groups` groups:
+ * (rows / 128 + groups) row blocks times ceil(ozk_kpad(K) / 64) (NVFP4) or
+ * ceil(ozk_kpad(K) / 128) (MXFP4) tiles of 512 bytes.  0 for unsupported
+ * arguments. */
+size_t ozk_mx4_scale_bytes(int64_t rows, int64_t K, int format, int groups);
+
+/* Quantises the rows of X (rows x K, dtype any ozk_dtype, any alignment of
+ * its own type).  With x' = prescale times x, both in fp32 (an FP64 element
+ * is rounded to fp32 first), and amax the largest |x'| of a block:
+ *   NVFP4: scale s = amax / 6 rounded to E4M3 (to nearest even, at most 448);
+ *   MXFP4: s = 2^(floor(log2 amax) - 2), its exponent limited to [-127, 127];
+ *   code = x' / s rounded to E2M1, to nearest, ties to even, at most 6 (the
+ *   quotient is not rounded before).
+ * A block whose s is 0 stands for zeros; a block that holds an Inf or NaN
+ * gets the NaN scale (0x7F, 0xFF) and codes 0, and stands for NaNs.
+ * codes: rows x ozk_kpad(K) / 2 bytes, element 2i of a row in the low half of
+ * its byte i, zeros past K.  scales (ozk_mx4_scale_bytes): block b of row r of
+ * a group (r counted from the group's start o) at
+ *   ((o / 128 + g + r / 128) * tiles + b / 4) * 512 + r % 32 * 16
+ *   + r / 32 % 4 * 4 + b % 4,
+ * tiles per row block as above: every group starts a row block of its own.
+ * Bytes of rows that do not exist are left as they are.  Groups: offsets as
+ * above, or NULL for `groups` groups of rows / groups rows each (1: a plain
+ * matrix; the weights of E experts: E * N rows, E groups).  Rows in no group
+ * are skipped.  codes and scales must be 16-byte aligned and overlap nothing. */
+int ozk_mx4_quantize(int64_t rows, int64_t K, const void* X, int64_t ldx, int dtype, int format, float prescale,
+                     const int32_t* offsets, int groups, uint8_t* codes, uint8_t* scales, ozk_stream_t stream);
+
+/* The values stored codes and scales stand for, rounded to dtype (exact in
+ * fp32 and FP64; in bf16 too; fp16 only within its range). */
+int ozk_mx4_dequantize(int64_t rows, int64_t K, const uint8_t* codes, const uint8_t* scales, int format,
+                       const int32_t* offsets, int groups, void* X, int64_t ldx, int dtype, ozk_stream_t stream);
+
+/* C[i, j] = alpha * sum_k a_ik b_jk for 4-bit matrices A (M x K) and B (N x K:
+ * the transposed form, weights as a layer holds them), both of one group and
+ * one format.  C: M x N of out_dtype OZK_BF16, OZK_F16 or OZK_F32 (others:
+ * OZK_ERR_UNSUPPORTED), ldc >= N, any alignment of its own type.  K = 0 gives
+ * zeros. */
+int ozk_mx4_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a_codes, const uint8_t* a_scales,
+                 const uint8_t* b_codes, const uint8_t* b_scales, int format, float alpha, void* C, int64_t ldc,
+                 int out_dtype, ozk_stream_t stream);
+
+/* Y[t, j] = alpha * sum_k x_tk w_g(t),j,k: each group's rows times its own
+ * weights.  x: T x K quantised with the same offsets and groups; w: groups * N
+ * rows quantised as `groups` equal groups.  Otherwise as ozk_mx4_gemm. */
+int ozk_mx4_grouped_gemm(int64_t T, int64_t N, int64_t K, int groups, const int32_t* offsets, const uint8_t* x_codes,
+                         const uint8_t* x_scales, const uint8_t* w_codes, const uint8_t* w_scales, int format,
+                         float alpha, void* Y, int64_t ldy, int out_dtype, ozk_stream_t stream);
+
+/* Y[t, j] = sum_k x_tk w_g(t),j,k for 16-bit operands (dtype OZK_BF16 or
+ * OZK_F16): X is T x K, W holds one N x K matrix per group, w_stride elements
+ * apart, Y is T x N of dtype or OZK_F32.  X and W are read by bulk tensor
+ * copies: their addresses must be multiples of 16 bytes, ldx, ldw and w_stride
+ * of 8 elements (else OZK_ERR_UNSUPPORTED); N and K are free.  Y needs the
+ * alignment of its type only.  Y must not overlap X or W. */
+int ozk_grouped_gemm(int64_t T, int64_t N, int64_t K, int groups, const int32_t* offsets, const void* X, int64_t ldx,
+                     const void* W, int64_t ldw, int64_t w_stride, int dtype, void* Y, int64_t ldy, int out_dtype,
+                     ozk_stream_t stream);
+
+/* Its gradients.  dX[t, k] = sum_j dy_tj w_g(t),j,k (T x K), and
+ * dW[g, j, k] = the sum of dy_tj x_tk over the rows t of group g (N x K per
+ * group, dw_stride elements apart; zeros for a group without rows).  Operand
+ * requirements as above. */
+int ozk_grouped_gemm_dx(int64_t T, int64_t N, int64_t K, int groups, const int32_t* offsets, const void* dY,
+                        int64_t lddy, const void* W, int64_t ldw, int64_t w_stride, int dtype, void* dX, int64_t lddx,
+                        int out_dtype, ozk_stream_t stream);
+int ozk_grouped_gemm_dw(int64_t T, int64_t N, int64_t K, int groups, const int32_t* offsets, const void* dY,
+                        int64_t lddy, const void* X, int64_t ldx, int dtype, void* dW, int64_t lddw, int64_t dw_stride,
+                        int out_dtype, ozk_stream_t stream);
+
+/* ------------------------------------------------------------------ */
 /* Test hook of the failure path.                                      */
 /* ------------------------------------------------------------------ */
 
