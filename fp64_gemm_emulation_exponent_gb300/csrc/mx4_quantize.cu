@@ -29,14 +29,17 @@ namespace ozk {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 constexpr int kLaneElems = 16;                // elements a lane quantises at once
-constexpr int kWarpElems = 32 * kLaneElems;   // of one row
+constexpr int kWarpElems = 32 * kLaneElems;   // columns a warp takes at once: a chunk of a row
+constexpr int kMaxRun = 4;                    // chunks of one row a warp takes one after the other
 
 struct Mx4Params {
   int64_t rows, K, ld;         // matrix and its leading dimension (elements)
-  int64_t units;               // (row, 512-column chunk) pairs
-  int kpad, kgroups, chunks;   // kgroups: scale words (4 blocks) per row
-  FastDiv div_chunks;
+  int64_t units;               // (row, run of chunks) pairs, a warp's work
+  int kpad, kgroups, chunks;   // chunks of a row; kgroups: scale words (4 blocks) of a row
+  int run, runs;               // chunks a unit takes; units of a row
+  FastDiv div_runs;            // used while units < 2^31
   const int32_t* offsets;      // group starts (groups + 1), or null: groups of rows_per_group
   int groups;
   int64_t rows_per_group;
@@ -62,15 +65,25 @@ __device__ __forceinline__ T from_f32(float v) {
   else return v;
 }
 
+// Row and first chunk of unit u.
+__device__ __forceinline__ int64_t row_of(const Mx4Params& p, int64_t u, int* chunk) {
+  if (p.units < (int64_t{1} << 31)) {
+    const uint32_t row = div_fast(static_cast<uint32_t>(u), p.div_runs);
+    *chunk = static_cast<int>(static_cast<uint32_t>(u) - row * static_cast<uint32_t>(p.runs)) * p.run;
+    return row;
+  }
+  const int64_t row = u / p.runs;
+  *chunk = static_cast<int>(u - row * p.runs) * p.run;
+  return row;
+}
+
 // Byte offset of the scale word (4 blocks) kg = 0 of `row`, or -1 for a row
 // outside every group.  Groups that overlap or run backwards cannot take it
 // out of the buffer: o_g <= row gives a row block of at most row / 128 + g.
-__device__ __forceinline__ int64_t scale_row(const Mx4Params& p, int64_t row) {
-  int64_t g, o;
-  if (p.offsets == nullptr) {
-    g = p.groups == 1 ? 0 : row / p.rows_per_group;
-    o = g * p.rows_per_group;
-  } else {
+__device__ __forceinline__ int64_t scale_row(const Mx4Params& p, int64_t row64) {
+  const int row = static_cast<int>(row64);  // below 2^30
+  int g = 0, o = 0;
+  if (p.offsets != nullptr) {
     int lo = 0, hi = p.groups;  // the last group that starts at or before the row
     while (lo + 1 < hi) {
       const int mid = (lo + hi) / 2;
@@ -80,39 +93,135 @@ __device__ __forceinline__ int64_t scale_row(const Mx4Params& p, int64_t row) {
     g = lo;
     o = p.offsets[lo];
     if (o < 0 || o > row || row >= p.offsets[lo + 1]) return -1;
+  } else if (p.groups > 1) {
+    const int per = static_cast<int>(p.rows_per_group);
+    g = row / per;
+    o = g * per;
   }
-  const int64_t r = row - o;
-  return (o / 128 + g + r / 128) * p.kgroups * 512 + (r % 32) * 16 + (r / 32 % 4) * 4;
+  const int r = row - o;
+  return (static_cast<int64_t>((o >> 7) + g + (r >> 7)) * p.kgroups) * 512 + ((r & 31) << 4) + ((r >> 3) & 12);
 }
 
-// 16 elements k0.. of a row as fp32, zeros past K.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load16(const T* row, int64_t k0, int64_t K, float (&v)[kLaneElems]) {
-  if (VEC && k0 + kLaneElems <= K) {
-    constexpr int per = 16 / sizeof(T);
-    uint4 raw[kLaneElems / per];
+// 16 elements of a row per lane, raw: lane l takes columns k0 + 16 l .. + 15,
+// zeros past K.  Read as 32- or 16-byte words where base and row stride allow it;
+// otherwise the warp reads its chunk in words of ALIGN bytes, neighbouring
+// lanes neighbouring words, and turns it round in shared memory.
+template <typename T>
+struct Raw {
+  alignas(32) T v[kLaneElems];
+};
+// 32 bytes at once (32-byte aligned): a lane's whole sector in one access.
+__device__ __forceinline__ void load32(const void* src, uint32_t* d) {
+  asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]), "=r"(d[4]), "=r"(d[5]), "=r"(d[6]), "=r"(d[7])
+      : "l"(src));
+}
+__device__ __forceinline__ void store32(void* dst, const uint32_t* d) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(d[0]), "r"(d[1]), "r"(d[2]),
+               "r"(d[3]), "r"(d[4]), "r"(d[5]), "r"(d[6]), "r"(d[7])
+               : "memory");
+}
+
+template <typename T, int ALIGN>
+__device__ __forceinline__ void load_raw(const T* row, int k0, int64_t K, int lane, uint8_t* stage, Raw<T>& r) {
+  if constexpr (ALIGN >= 16) {
+    const int k = k0 + lane * kLaneElems;
+    if (k + kLaneElems <= K) {
+      if constexpr (ALIGN == 32) {
 #pragma unroll
-    for (int i = 0; i < kLaneElems / per; ++i) raw[i] = __ldg(reinterpret_cast<const uint4*>(row + k0) + i);
-    const T* e = reinterpret_cast<const T*>(raw);
+        for (int i = 0; i < kLaneElems * static_cast<int>(sizeof(T)) / 32; ++i)
+          load32(reinterpret_cast<const uint8_t*>(row + k) + 32 * i, reinterpret_cast<uint32_t*>(r.v) + 8 * i);
+      } else {
 #pragma unroll
-    for (int i = 0; i < kLaneElems; ++i) v[i] = to_f32(e[i]);
+        for (int i = 0; i < kLaneElems * static_cast<int>(sizeof(T)) / 16; ++i)
+          reinterpret_cast<uint4*>(r.v)[i] = __ldg(reinterpret_cast<const uint4*>(row + k) + i);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLaneElems; ++i) r.v[i] = k + i < K ? row[k + i] : T(0.0f);
+    }
+  } else if constexpr (ALIGN == 4 && sizeof(T) == 2) {
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(row);
+    uint32_t w[kLaneElems / 2];
+#pragma unroll
+    for (int i = 0; i < kLaneElems / 2; ++i) {
+      const int64_t k = k0 + 2 * (32 * i + lane);
+      w[i] = k + 1 < K ? __ldg(words + k / 2) : k < K ? *reinterpret_cast<const uint16_t*>(row + k) : 0u;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kLaneElems / 2; ++i) reinterpret_cast<uint32_t*>(stage)[32 * i + lane] = w[i];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) reinterpret_cast<uint4*>(r.v)[i] = reinterpret_cast<const uint4*>(stage)[2 * lane + i];
   } else {
+    T w[kLaneElems];
 #pragma unroll
-    for (int i = 0; i < kLaneElems; ++i) v[i] = k0 + i < K ? to_f32(row[k0 + i]) : 0.0f;
+    for (int i = 0; i < kLaneElems; ++i) {
+      const int64_t k = k0 + 32 * i + lane;
+      w[i] = k < K ? row[k] : T(0.0f);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kLaneElems; ++i) reinterpret_cast<T*>(stage)[32 * i + lane] = w[i];
+    __syncwarp();
+    constexpr int words = kLaneElems * static_cast<int>(sizeof(T)) / 16;
+#pragma unroll
+    for (int i = 0; i < words; ++i)
+      reinterpret_cast<uint4*>(r.v)[i] = reinterpret_cast<const uint4*>(stage)[words * lane + i];
   }
 }
 
-// Codes of eight values, the first in the low half of the low byte.
-__device__ __forceinline__ uint32_t codes8(const float* q) {
+// Largest magnitude of a lane's elements, times prescale, as fp32 bits: Inf
+// and NaN compare above every finite value.  Rounding is monotone, so this is
+// the largest |x'|.  16-bit types take the maximum of two elements at a time.
+template <typename T>
+__device__ __forceinline__ uint32_t top_of(const Raw<T>& r, float prescale) {
+  float top;
+  if constexpr (sizeof(T) == 2) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(r.v);
+    uint32_t m = w[0] & 0x7FFF7FFFu;
+#pragma unroll
+    for (int i = 1; i < kLaneElems / 2; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+    const unsigned short h = static_cast<unsigned short>(max(m & 0xFFFFu, m >> 16));
+    if constexpr (std::is_same<T, __half>::value) top = __half2float(__ushort_as_half(h));
+    else top = __uint_as_float(static_cast<uint32_t>(h) << 16);
+  } else {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kLaneElems; ++i) m = max(m, __float_as_uint(to_f32(r.v[i])) & 0x7FFFFFFFu);
+    top = __uint_as_float(m);
+  }
+  return __float_as_uint(top * prescale) & 0x7FFFFFFFu;
+}
+
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// Codes of eight values (four pairs), the first in the low half of the low byte.
+__device__ __forceinline__ uint32_t codes8(const uint64_t* q) {
   uint32_t r;
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t.reg .f32 l, h;\n\t"
+      "mov.b64 {l, h}, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b0, h, l;\n\t"
+      "mov.b64 {l, h}, %2;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, h, l;\n\t"
+      "mov.b64 {l, h}, %3;\n\tcvt.rn.satfinite.e2m1x2.f32 b2, h, l;\n\t"
+      "mov.b64 {l, h}, %4;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, h, l;\n\t"
       "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
       : "=r"(r)
-      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+      : "l"(q[0]), "l"(q[1]), "l"(q[2]), "l"(q[3]));
   return r;
 }
 
@@ -128,106 +237,168 @@ __device__ __forceinline__ float e4m3_value(uint32_t b) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xFFFFu)));
 }
 
-template <typename T, int FMT, bool VEC>
+// Quantises one lane's 16 elements at column k and stores codes and scales.
+template <typename T, int FMT>
+__device__ __forceinline__ void quantize16(const Mx4Params& p, const Raw<T>& r, int64_t row, int k, int64_t at, int lane) {
+  uint32_t top = top_of(r, p.prescale);
+  if (FMT == OZK_MXFP4) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+  uint64_t v[kLaneElems / 2];
+#pragma unroll
+  for (int i = 0; i < kLaneElems / 2; ++i) v[i] = pack2(to_f32(r.v[2 * i]), to_f32(r.v[2 * i + 1]));
+  if (p.prescale != 1.0f) {
+    const uint64_t ps = pack2(p.prescale, p.prescale);
+#pragma unroll
+    for (int i = 0; i < kLaneElems / 2; ++i) v[i] = mul2(v[i], ps);
+  }
+  uint32_t byte, lo = 0, hi = 0;
+  if (FMT == OZK_MXFP4) {
+    byte = static_cast<uint32_t>(max(static_cast<int>(top >> 23) - 2, 0));
+    const float f = __uint_as_float((254u - byte) << 23);
+    const uint64_t inv = pack2(f, f);  // 1 / s, exact
+#pragma unroll
+    for (int i = 0; i < kLaneElems / 2; ++i) v[i] = mul2(v[i], inv);
+  } else {
+    byte = e4m3_of(__fdiv_rn(__uint_as_float(top), 6.0f));
+    const float s = e4m3_value(byte);
+    const float f = byte ? __frcp_rn(s) : 0.0f;
+    const uint64_t inv = pack2(f, f), neg = pack2(-s, -s);
+    // x' / s correctly rounded (Markstein's residual step from the rounded
+    // reciprocal): the ties of the E2M1 rounding, multiples t s with few
+    // bits, come out exactly, and nothing else rounds onto them
+#pragma unroll
+    for (int i = 0; i < kLaneElems / 2; ++i) {
+      const uint64_t q = mul2(v[i], inv);
+      v[i] = fma2(fma2(q, neg, v[i]), inv, q);
+    }
+  }
+  if (top < 0x7F800000u) {
+    lo = codes8(v);
+    hi = codes8(v + 4);
+  } else {
+    byte = FMT == OZK_MXFP4 ? 0xFFu : 0x7Fu;
+  }
+  if (k < p.kpad) *reinterpret_cast<uint2*>(p.codes + row * (p.kpad / 2) + k / 2) = make_uint2(lo, hi);
+  // four scale bytes to a word: of 4 lanes (nvfp4), of lanes 0, 2, 4, 6 of 8 (mxfp4)
+  constexpr int step = FMT == OZK_MXFP4 ? 2 : 1;
+  uint32_t word = byte << (8 * ((lane / step) & 3));
+  word |= __shfl_xor_sync(0xFFFFFFFFu, word, step);
+  word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2 * step);
+  const int kg = k / (64 * step);
+  if (lane % (4 * step) == 0 && kg < p.kgroups)
+    *reinterpret_cast<uint32_t*>(p.scales + at + static_cast<int64_t>(kg) * 512) = word;
+}
+
+template <typename T, int FMT, int ALIGN>
 __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const Mx4Params p) {
   grid_dependency_sync();
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); u < p.units; u += warps) {
-    const int64_t row = u / p.chunks;
-    const int chunk = static_cast<int>(u - row * p.chunks);
+  __shared__ alignas(16) uint8_t stages[ALIGN >= 16 ? 16 : kWarps * kWarpElems * sizeof(T)];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint8_t* stage = ALIGN >= 16 ? stages : stages + warp * kWarpElems * sizeof(T);
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < p.units; u += warps) {
+    int c;
+    const int64_t row = row_of(p, u, &c);
+    const T* src = static_cast<const T*>(p.x) + row * p.ld;
+    const int c1 = min(c + p.run, p.chunks);
+    Raw<T> r;
+    load_raw<T, ALIGN>(src, c * kWarpElems, p.K, lane, stage, r);
     const int64_t at = scale_row(p, row);
     if (at < 0) continue;
-    const int k0 = chunk * kWarpElems + lane * kLaneElems;
-    float v[kLaneElems];
-    load16<T, VEC>(static_cast<const T*>(p.x) + row * p.ld, k0, p.K, v);
-    uint32_t top = 0;  // largest |x'| as bits: Inf and NaN compare above every finite value
-#pragma unroll
-    for (int i = 0; i < kLaneElems; ++i) {
-      v[i] *= p.prescale;
-      top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    for (;;) {  // the next chunk is on its way while this one is quantised
+      Raw<T> next;
+      if (c + 1 < c1) load_raw<T, ALIGN>(src, (c + 1) * kWarpElems, p.K, lane, stage, next);
+      quantize16<T, FMT>(p, r, row, c * kWarpElems + lane * kLaneElems, at, lane);
+      if (++c >= c1) break;
+      r = next;
     }
-    if (FMT == OZK_MXFP4) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-    const bool finite = top < 0x7F800000u;
-    uint32_t byte, lo = 0, hi = 0;
-    if (FMT == OZK_MXFP4) {
-      const int e = static_cast<int>(top >> 23) - 2;
-      byte = static_cast<uint32_t>(max(e, 0));
-      const float inv = __uint_as_float((254u - byte) << 23);  // exact: 1 / s
-#pragma unroll
-      for (int i = 0; i < kLaneElems; ++i) v[i] *= inv;
-    } else {
-      byte = e4m3_of(__fdiv_rn(__uint_as_float(top), 6.0f));
-      const float s = e4m3_value(byte);
-      const float inv = byte ? __frcp_rn(s) : 0.0f;
-      // x' / s correctly rounded (Markstein's residual step from the rounded
-      // reciprocal): the ties of the E2M1 rounding, multiples t s with few
-      // bits, come out exactly, and nothing else rounds onto them
-#pragma unroll
-      for (int i = 0; i < kLaneElems; ++i) {
-        const float q = v[i] * inv;
-        v[i] = fmaf(fmaf(-q, s, v[i]), inv, q);
-      }
-    }
-    if (finite) {
-      lo = codes8(v);
-      hi = codes8(v + 8);
-    } else {
-      byte = FMT == OZK_MXFP4 ? 0xFFu : 0x7Fu;
-    }
-    if (k0 < p.kpad)
-      *reinterpret_cast<uint2*>(p.codes + row * (p.kpad / 2) + k0 / 2) = make_uint2(lo, hi);
-    // four scale bytes to a word: of 4 lanes (nvfp4), of lanes 0, 2, 4, 6 of 8 (mxfp4)
-    constexpr int step = FMT == OZK_MXFP4 ? 2 : 1;
-    uint32_t word = byte << (8 * ((lane / step) & 3));
-    word |= __shfl_xor_sync(0xFFFFFFFFu, word, step);
-    word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2 * step);
-    const int kg = k0 / (64 * step);
-    if (lane % (4 * step) == 0 && kg < p.kgroups)
-      *reinterpret_cast<uint32_t*>(p.scales + at + static_cast<int64_t>(kg) * 512) = word;
   }
 }
 
 // The values 16 codes stand for: the E2M1 value, exact in fp16, times the
 // scale (at most 6 significant bits, exact in fp32; a NaN scale gives NaN).
-template <typename T, int FMT, bool VEC>
+template <typename T, int FMT, int ALIGN>
 __global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(const Mx4Params p) {
   grid_dependency_sync();
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); u < p.units; u += warps) {
-    const int64_t row = u / p.chunks;
-    const int k0 = static_cast<int>(u - row * p.chunks) * kWarpElems + lane * kLaneElems;
+  __shared__ alignas(16) uint8_t stages[ALIGN >= 16 ? 16 : kWarps * kWarpElems * sizeof(T)];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T* stage = reinterpret_cast<T*>(ALIGN >= 16 ? stages : stages + warp * kWarpElems * sizeof(T));
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < p.units; u += warps) {
+    int c;
+    const int64_t row = row_of(p, u, &c);
     const int64_t at = scale_row(p, row);
-    if (at < 0 || k0 >= p.K) continue;
-    const uint2 c = *reinterpret_cast<const uint2*>(p.codes + row * (p.kpad / 2) + k0 / 2);
-    constexpr int block = FMT == OZK_MXFP4 ? 32 : 16;
-    const int b = k0 / block;
-    const uint32_t byte = p.scales[at + static_cast<int64_t>(b / 4) * 512 + b % 4];
-    float s;
-    if (FMT == OZK_MXFP4)
-      s = byte == 0xFFu ? __uint_as_float(0x7FC00000u) : byte ? __uint_as_float(byte << 23) : __uint_as_float(1u << 22);
-    else
-      s = e4m3_value(byte);
-    T v[kLaneElems];
+    if (at < 0) continue;
+    const int c1 = min(c + p.run, p.chunks);
+    const uint8_t* codes = p.codes + row * (p.kpad / 2);
+    T* dst = static_cast<T*>(p.out) + row * p.ld;
+    uint2 run_codes[kMaxRun];  // all of the unit's loads at once
+    uint32_t run_bytes[kMaxRun];
 #pragma unroll
-    for (int i = 0; i < kLaneElems / 2; ++i) {
-      uint32_t h;
-      const uint32_t two = ((i < 4 ? c.x : c.y) >> (8 * (i & 3))) & 0xFFu;
-      asm("{\n\t.reg .b8 b, z;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(h) : "r"(two));
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      v[2 * i] = from_f32<T>(f.x * s);
-      v[2 * i + 1] = from_f32<T>(f.y * s);
+    for (int i = 0; i < kMaxRun; ++i) {
+      const int k = (c + i) * kWarpElems + lane * kLaneElems;
+      run_codes[i] = make_uint2(0, 0);
+      run_bytes[i] = 0;
+      if (c + i < c1 && k < p.K) {
+        run_codes[i] = __ldg(reinterpret_cast<const uint2*>(codes + k / 2));
+        const int b = k / (FMT == OZK_MXFP4 ? 32 : 16);
+        run_bytes[i] = __ldg(p.scales + at + static_cast<int64_t>(b / 4) * 512 + b % 4);
+      }
     }
-    T* dst = static_cast<T*>(p.out) + row * p.ld + k0;
-    if (VEC && k0 + kLaneElems <= p.K) {
 #pragma unroll
-      for (int i = 0; i < kLaneElems * static_cast<int>(sizeof(T)) / 16; ++i)
-        reinterpret_cast<uint4*>(dst)[i] = reinterpret_cast<const uint4*>(v)[i];
-    } else {
+    for (int j = 0; j < kMaxRun; ++j, ++c) {
+      if (c >= c1) break;
+      const int k = c * kWarpElems + lane * kLaneElems;
+      const uint2 code = run_codes[j];
+      const uint32_t byte = run_bytes[j];
+      float s;
+      if (FMT == OZK_MXFP4)
+        s = byte == 0xFFu ? __uint_as_float(0x7FC00000u) : byte ? __uint_as_float(byte << 23) : __uint_as_float(1u << 22);
+      else
+        s = e4m3_value(byte);
+      Raw<T> r;
 #pragma unroll
-      for (int i = 0; i < kLaneElems; ++i)
-        if (k0 + i < p.K) dst[i] = v[i];
+      for (int i = 0; i < kLaneElems / 2; ++i) {
+        uint32_t h;
+        const uint32_t two = ((i < 4 ? code.x : code.y) >> (8 * (i & 3))) & 0xFFu;
+        asm("{\n\t.reg .b8 b;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(h) : "r"(two));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        r.v[2 * i] = from_f32<T>(f.x * s);
+        r.v[2 * i + 1] = from_f32<T>(f.y * s);
+      }
+      if (ALIGN == 32 && k + kLaneElems <= p.K) {
+#pragma unroll
+        for (int i = 0; i < kLaneElems * static_cast<int>(sizeof(T)) / 32; ++i)
+          store32(reinterpret_cast<uint8_t*>(dst + k) + 32 * i, reinterpret_cast<const uint32_t*>(r.v) + 8 * i);
+      } else if (ALIGN == 16 && k + kLaneElems <= p.K) {
+#pragma unroll
+        for (int i = 0; i < kLaneElems * static_cast<int>(sizeof(T)) / 16; ++i)
+          reinterpret_cast<uint4*>(dst + k)[i] = reinterpret_cast<const uint4*>(r.v)[i];
+      } else if (ALIGN >= 16) {
+#pragma unroll
+        for (int i = 0; i < kLaneElems; ++i)
+          if (k + i < p.K) dst[k + i] = r.v[i];
+      } else {  // turned round in shared memory: neighbouring lanes write neighbouring words
+        constexpr int words = kLaneElems * static_cast<int>(sizeof(T)) / 16;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < words; ++i)
+          reinterpret_cast<uint4*>(stage)[words * lane + i] = reinterpret_cast<const uint4*>(r.v)[i];
+        __syncwarp();
+        const int64_t k0 = static_cast<int64_t>(c) * kWarpElems;
+        if constexpr (ALIGN == 4 && sizeof(T) == 2) {
+#pragma unroll
+          for (int i = 0; i < kLaneElems / 2; ++i) {
+            const int64_t at2 = k0 + 2 * (32 * i + lane);
+            const uint32_t w = reinterpret_cast<const uint32_t*>(stage)[32 * i + lane];
+            if (at2 + 1 < p.K) reinterpret_cast<uint32_t*>(dst)[at2 / 2] = w;
+            else if (at2 < p.K) *reinterpret_cast<uint16_t*>(dst + at2) = static_cast<uint16_t>(w);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kLaneElems; ++i)
+            if (k0 + 32 * i + lane < p.K) dst[k0 + 32 * i + lane] = stage[32 * i + lane];
+        }
+      }
     }
   }
 }
@@ -244,60 +415,79 @@ auto pick_type(int dtype, F&& f) {
 
 size_t type_bytes(int dtype) { return dtype == OZK_F64 ? 8 : dtype == OZK_F32 ? 4 : 2; }
 
-Mx4Params make_params(const Mx4Matrix& m, int64_t ld) {
+// Warps that keep the memory busy: units of one chunk until every SM has
+// kFullWarps of them, then runs of up to kMaxRun chunks, which share the row's
+// addressing and have the next chunk's loads in flight.
+constexpr int kFullWarps = 48;
+
+Mx4Params make_params(const Mx4Matrix& m, int64_t ld, int num_sms) {
   Mx4Params p = {};
   p.rows = m.rows;
   p.K = m.K;
   p.ld = ld;
   p.kpad = static_cast<int>(ozk_kpad(m.K));
   p.kgroups = mx4_kgroups(m.K, m.format);
-  // enough 512-column chunks for the codes and the scale words (a word covers 64 or 128 columns)
+  // enough chunks for the codes and the scale words (a word covers 64 or 128 columns)
   p.chunks = (p.kgroups * (m.format == OZK_MXFP4 ? 128 : 64) + kWarpElems - 1) / kWarpElems;
-  p.units = m.rows * p.chunks;
+  const int64_t per_warp = m.rows * p.chunks / (static_cast<int64_t>(num_sms) * kFullWarps);
+  p.run = static_cast<int>(std::min<int64_t>(std::min<int64_t>(kMaxRun, p.chunks), std::max<int64_t>(per_warp, 1)));
+  p.runs = (p.chunks + p.run - 1) / p.run;
+  p.units = m.rows * p.runs;
+  p.div_runs = fast_div(p.runs);
   p.offsets = m.offsets;
   p.groups = m.groups;
-  p.rows_per_group = m.groups > 0 ? std::max<int64_t>(m.rows / m.groups, 1) : 1;
+  p.rows_per_group = std::max<int64_t>(m.rows / m.groups, 1);
   p.codes = m.codes;
   p.scales = m.scales;
   return p;
 }
 
 unsigned grid_of(int64_t units, int num_sms) {
-  const int64_t blocks = (units + kThreads / 32 - 1) / (kThreads / 32);
-  return static_cast<unsigned>(std::min<int64_t>(blocks, static_cast<int64_t>(num_sms) * 8));
+  return static_cast<unsigned>(std::min<int64_t>((units + kWarps - 1) / kWarps, static_cast<int64_t>(num_sms) * 8));
 }
 
-bool vec_ok(const void* x, int64_t ld, int dtype) {
-  return reinterpret_cast<uintptr_t>(x) % 16 == 0 && (static_cast<size_t>(ld) * type_bytes(dtype)) % 16 == 0;
+// The widest word every row's first element is aligned to: 32, 16, 4 or 2 bytes.
+int alignment(const void* x, int64_t ld, int dtype) {
+  const size_t a = reinterpret_cast<uintptr_t>(x) | (static_cast<size_t>(ld) * type_bytes(dtype));
+  return a % 32 == 0 ? 32 : a % 16 == 0 ? 16 : a % 4 == 0 ? 4 : 2;
+}
+
+// f(element type, format, alignment) with constants.
+template <typename F>
+cudaError_t dispatch(int dtype, int format, int align, F&& f) {
+  return pick_type(dtype, [&](auto t) {
+    using T = decltype(t);
+    auto with = [&](auto fmt) {
+      if (align == 32) return f(t, fmt, std::integral_constant<int, 32>{});
+      if (align == 16) return f(t, fmt, std::integral_constant<int, 16>{});
+      if (align == 4 || sizeof(T) > 2) return f(t, fmt, std::integral_constant<int, 4>{});
+      return f(t, fmt, std::integral_constant<int, sizeof(T) == 2 ? 2 : 4>{});
+    };
+    return format == OZK_MXFP4 ? with(std::integral_constant<int, OZK_MXFP4>{})
+                               : with(std::integral_constant<int, OZK_NVFP4>{});
+  });
 }
 
 }  // namespace
 
 cudaError_t launch_mx4_quantize(const Mx4Matrix& m, const void* x, int64_t ldx, int dtype, float prescale,
                                 int num_sms, cudaStream_t stream) {
-  Mx4Params p = make_params(m, ldx);
+  Mx4Params p = make_params(m, ldx, num_sms);
   p.x = x;
   p.prescale = prescale;
-  const bool vec = vec_ok(x, ldx, dtype);
-  return pick_type(dtype, [&](auto t) {
-    using T = decltype(t);
-    auto k = m.format == OZK_MXFP4 ? (vec ? mx4_quantize_kernel<T, OZK_MXFP4, true> : mx4_quantize_kernel<T, OZK_MXFP4, false>)
-                                   : (vec ? mx4_quantize_kernel<T, OZK_NVFP4, true> : mx4_quantize_kernel<T, OZK_NVFP4, false>);
-    return launch_dependent(k, dim3(grid_of(p.units, num_sms)), dim3(kThreads), 0, stream, p);
+  return dispatch(dtype, m.format, alignment(x, ldx, dtype), [&](auto t, auto fmt, auto align) {
+    return launch_dependent(mx4_quantize_kernel<decltype(t), fmt.value, align.value>, dim3(grid_of(p.units, num_sms)),
+                            dim3(kThreads), 0, stream, p);
   });
 }
 
 cudaError_t launch_mx4_dequantize(const Mx4Matrix& m, void* out, int64_t ldo, int dtype, int num_sms,
                                   cudaStream_t stream) {
-  Mx4Params p = make_params(m, ldo);
+  Mx4Params p = make_params(m, ldo, num_sms);
   p.out = out;
-  const bool vec = vec_ok(out, ldo, dtype);
-  return pick_type(dtype, [&](auto t) {
-    using T = decltype(t);
-    auto k = m.format == OZK_MXFP4
-                 ? (vec ? mx4_dequantize_kernel<T, OZK_MXFP4, true> : mx4_dequantize_kernel<T, OZK_MXFP4, false>)
-                 : (vec ? mx4_dequantize_kernel<T, OZK_NVFP4, true> : mx4_dequantize_kernel<T, OZK_NVFP4, false>);
-    return launch_dependent(k, dim3(grid_of(p.units, num_sms)), dim3(kThreads), 0, stream, p);
+  return dispatch(dtype, m.format, alignment(out, ldo, dtype), [&](auto t, auto fmt, auto align) {
+    return launch_dependent(mx4_dequantize_kernel<decltype(t), fmt.value, align.value>, dim3(grid_of(p.units, num_sms)),
+                            dim3(kThreads), 0, stream, p);
   });
 }
 

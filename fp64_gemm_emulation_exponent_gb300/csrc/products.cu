@@ -24,6 +24,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <cstdlib>
 #include <map>
 #include <mutex>
 
@@ -65,13 +66,18 @@ struct Config {
   static constexpr uint32_t SFB_BYTES = MX ? NB * KG * kScaleTile : 0;
   static constexpr uint32_t STAGE = kABytes + B_BYTES + SFA_BYTES + SFB_BYTES;
   static constexpr int STAGES = MX ? 5 : 6;
-  static constexpr int BUFS = BN >= 256 && MX ? 1 : 2;
+  // Two accumulators and the scales in 512 TMEM columns: with 256-column
+  // accumulators beside scales the two share their last and first columns
+  // (48 or 24).  The epilogue takes those first, and the next tile's MMAs
+  // start once it has, while it works on the rest.
   static constexpr uint32_t SF_COLS = MX ? KG * 4 + KG * 4 * NB : 0;
-  static constexpr uint32_t SF_BASE = BUFS * BN;
-  static constexpr uint32_t TMEM = BUFS * BN + SF_COLS <= 256 ? 256 : 512;
-  static_assert(BUFS * BN + SF_COLS <= 512, "TMEM");
-  // full, empty and tail per stage; accumulator full and empty; drain
-  static constexpr int BARS = 3 * STAGES + 5;
+  static constexpr bool SHARED = 2 * BN + SF_COLS > 512;
+  static constexpr uint32_t TMEM = 2 * BN + SF_COLS <= 256 ? 256 : 512;
+  static constexpr uint32_t ACC1 = SHARED ? TMEM - SF_COLS - BN : BN;  // first column of the second accumulator
+  static constexpr uint32_t SF_BASE = TMEM - SF_COLS;
+  static_assert(!SHARED || (BN == 256 && ACC1 >= 192), "the shared columns lie in two blocks of 32 of each accumulator");
+  // full, empty, tail and peer tail per stage; accumulator full and empty; drain
+  static constexpr int BARS = 4 * STAGES + 5;
   static constexpr uint32_t FIXED = 1024 + STAGES * STAGE + 256;
   static_assert(8 * BARS + 8 <= 256, "barriers");
   static_assert(BN % 32 == 0 && B_ROWS % BOX == 0, "tile");
@@ -87,6 +93,14 @@ struct ProductParams {
   float alpha;
   uint32_t idesc;  // types, majorness, M; N is filled in per tile
 };
+
+// One lane of a converged warp.  The compiler then knows that a single thread
+// runs the branch, and takes tcgen05's warp-uniform operands from it directly.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
 
 __device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -291,14 +305,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t accf0 = empty0 + 8 * C::STAGES;
   const uint32_t acce0 = accf0 + 16;
   const uint32_t drain = acce0 + 16;
-  const uint32_t tail0 = drain + 8;
+  const uint32_t tail0 = drain + 8;               // this CTA's part of a group's last block is in
+  const uint32_t peer0 = tail0 + 8 * C::STAGES;   // leader: the peer has cleared its part
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      // on a pair that clears tails, both CTAs say when their part is in place
-      mbar_init(full0 + 8 * s, PAIR && OP == kGradWeights ? 2 : 1);
+      mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
       mbar_init(tail0 + 8 * s, 1);
+      mbar_init(peer0 + 8 * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf0 + 8 * b, 1);
@@ -330,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------ TMA producer ------------------------------
-    if (lane == 0) {
+    if (elect_one()) {
       int stage = 0, e = 0;
       uint32_t phase = 0;
       int issued_parity[C::STAGES];
@@ -361,7 +376,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             if (leader) mbar_expect_tx(bar, 2 * bytes);
             bar = cluster_addr(bar, 0);
-            if (OP == kGradWeights && !leader) mbar_arrive_cluster(bar);
           }
           auto load2 = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1) {
             if (PAIR) tma_load_2d_pair(dst, map, c0, c1, clear ? cluster_addr(bar, rank) : bar);
@@ -410,23 +424,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1 && leader) {
     // ------------------------------ MMA issuer ------------------------------
-    if (lane == 0) {
+    if (elect_one()) {
       int stage = 0, e = 0, ab = 0;
       uint32_t phase = 0, aphase = 0;
-      bool ok = true;
+      bool ok = true, first = true;
       for (int u = unit0; u < units && ok; u += unit_step) {
         const Tile t = tile_at<C, OP>(p, g, u, e);
         if (t.blocks == 0) continue;
-        if (!mbar_wait(acce0 + 8 * ab, aphase ^ 1u, abort_flag, kTimeoutNs)) break;
+        // free: this accumulator's previous tile (two ago) is out; or, with
+        // shared columns, the tile before this one is out of them
+        if (C::SHARED ? (!first && !mbar_wait(acce0 + 8 * (ab ^ 1), ab ? aphase : aphase ^ 1u, abort_flag, kTimeoutNs))
+                      : !mbar_wait(acce0 + 8 * ab, aphase ^ 1u, abort_flag, kTimeoutNs))
+          break;
+        first = false;
         tc_fence_after();
-        const uint32_t d = tmem_base + static_cast<uint32_t>(ab * BN);
+        const uint32_t d = tmem_base + (ab ? C::ACC1 : 0u);
         const uint32_t idesc = p.idesc | (static_cast<uint32_t>(t.half * C::CTAS >> 3) << 17);
         for (int kb = 0; kb < t.blocks; ++kb) {
           if (!mbar_wait(full0 + 8 * stage, phase, abort_flag, kTimeoutNs)) {
             ok = false;
             break;
           }
-          if (PAIR && OP == kGradWeights) mbar_test_cluster(full0 + 8 * stage, phase);  // acquire the peer's clearing
           tc_fence_after();
           const uint64_t da = operand_desc<C::A_MN>(sA + stage * kABytes);
           const uint64_t db = operand_desc<C::B_MN>(sB + stage * C::B_BYTES);
@@ -441,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 copy_scales<PAIR>(sfb + 4 * (C::NB * i + r),
                                   scale_desc(sSB + stage * C::SFB_BYTES + (r * C::KG + i) * kScaleTile));
             }
-            for (int s = 0; s < steps; ++s) {
+            _Pragma("unroll") for (int s = 0; s < 4; ++s) if (s < steps) {
               const int word = FMT == kNv ? s : s / 2;                       // scale word of the step
               const uint32_t id = FMT == kNv ? 0u : 2u * (s & 1);            // its first byte
               mma_scaled<FMT, PAIR>(d, da + 2ull * s, db + 2ull * s, idesc | (id << 4) | (id << 29), sfa + 4 * word,
@@ -450,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             // 32 bytes of K, or 16 rows of 128 bytes
             constexpr uint64_t step_a = C::A_MN ? (16 * kRowBytes) >> 4 : 2, step_b = C::B_MN ? (16 * kRowBytes) >> 4 : 2;
-            for (int s = 0; s < steps; ++s) {
+            _Pragma("unroll") for (int s = 0; s < 4; ++s) if (s < steps) {
               const uint32_t acc = (kb > 0 || s > 0) ? 1u : 0u;
               if (PAIR) mma_f16_pair(d, da + step_a * s, db + step_b * s, idesc, acc);
               else mma_f16(d, da + step_a * s, db + step_b * s, idesc, acc);
@@ -466,10 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         if (PAIR) mma_commit_both(accf0 + 8 * ab);
         else mma_commit(accf0 + 8 * ab);
-        if (++ab == C::BUFS) {
-          ab = 0;
-          aphase ^= 1u;
-        }
+        ab ^= 1;
+        if (ab == 0) aphase ^= 1u;
       }
       if (PAIR) mma_commit_local(drain);
       else mma_commit(drain);
@@ -499,8 +515,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
+        // the leader passes the stage on once the peer's part is cleared too
+        if (PAIR && leader) {
+          if (!warp_wait(peer0 + 8 * stage, ((tails >> stage) & 1u) ^ 1u, abort_flag, kTimeoutNs)) break;
+          mbar_test_cluster(peer0 + 8 * stage, ((tails >> stage) & 1u) ^ 1u);  // acquire at cluster scope
+        }
         if (lane == 0) {
-          if (PAIR) mbar_arrive_cluster(cluster_addr(full0 + 8 * stage, 0));
+          if (PAIR && !leader) mbar_arrive_cluster(cluster_addr(peer0 + 8 * stage, 0));
           else mbar_arrive(full0 + 8 * stage);
         }
       }
@@ -523,33 +544,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!warp_wait(accf0 + 8 * ab, aphase, abort_flag, kTimeoutNs)) break;
         tc_fence_after();
       }
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(ab * BN);
-      for (int c = 32 * side; c < t.n; c += 64) {
-        uint32_t v[32];
-        if (has) {
-          tmem_ld32(taddr + static_cast<uint32_t>(c), v);
-          tmem_wait_ld(v);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0u;
-        }
-        const int64_t o = at + c * p.ldo;
-        const int rows = t.n - c;
-        if (p.out_type == OZK_F32) store_block(static_cast<float*>(p.out) + o, p.ldo, rows, in_m, v, p.alpha);
-        else if (p.out_type == OZK_F16) store_block(static_cast<__half*>(p.out) + o, p.ldo, rows, in_m, v, p.alpha);
-        else store_block(static_cast<__nv_bfloat16*>(p.out) + o, p.ldo, rows, in_m, v, p.alpha);
-      }
-      if (has) {
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + (ab ? C::ACC1 : 0u);
+      // blocks of 32 columns, alternating between the two warps of a lane
+      // quadrant; of accumulator 0 with shared columns the last two first
+      constexpr int kBlocks = BN / 64;
+      bool held = has;
+      auto release = [&]() {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
           if (PAIR) mbar_arrive_cluster(cluster_addr(acce0 + 8 * ab, 0));
           else mbar_arrive(acce0 + 8 * ab);
         }
-        if (++ab == C::BUFS) {
-          ab = 0;
-          aphase ^= 1u;
+        held = false;
+      };
+#pragma unroll 1
+      for (int i = 0; i < kBlocks; ++i) {
+        const int c = 64 * (C::SHARED && ab == 0 ? (i + kBlocks - 1) % kBlocks : i) + 32 * side;
+        const int rows = t.n - c;
+        uint32_t v[32];
+        if (rows > 0) {
+          if (has) {
+            tmem_ld32(taddr + static_cast<uint32_t>(c), v);
+            tmem_wait_ld(v);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0u;
+          }
         }
+        if (held && (C::SHARED || i == kBlocks - 1)) release();
+        if (rows <= 0) continue;
+        const int64_t o = at + c * p.ldo;
+        if (p.out_type == OZK_F32) store_block(static_cast<float*>(p.out) + o, p.ldo, rows, in_m, v, p.alpha);
+        else if (p.out_type == OZK_F16) store_block(static_cast<__half*>(p.out) + o, p.ldo, rows, in_m, v, p.alpha);
+        else store_block(static_cast<__nv_bfloat16*>(p.out) + o, p.ldo, rows, in_m, v, p.alpha);
+      }
+      if (has) {
+        ab ^= 1;
+        if (ab == 0) aphase ^= 1u;
       }
     }
   }
@@ -719,6 +751,8 @@ cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
 
 template <ProductOp OP, int FMT>
 cudaError_t choose(const Product& q, int num_sms, cudaStream_t stream) {
+  const char* ev = getenv("OZK_PAIR");
+  if (ev && ev[0] == '1') return launch<OP, FMT, 256, true>(q, num_sms, stream);
   return launch<OP, FMT, 128, false>(q, num_sms, stream);
 }
 

@@ -305,17 +305,27 @@ def ozk_crt_lift(M, N, n_moduli, inp, in_kind, ldi, splits, X, stream=None):
 
 
 # ---------------------------------------------------------------- 4-bit matrices and grouped products
+# A small call takes a few microseconds on the GPU, so these wrappers do no
+# more than check and marshal: pointers go as plain integers, the stream comes
+# from the device index, sizes are computed here rather than by another call.
 _FORMATS = {"nvfp4": OZK_NVFP4, "mxfp4": OZK_MXFP4}
+_WORD_COLUMNS = {"nvfp4": 64, "mxfp4": 128}  # columns one word of four scale bytes covers
 _DTYPES = {}
+_torch = None
+
+
+def _load_torch():
+    global _torch
+    import torch
+
+    _DTYPES.update({torch.bfloat16: OZK_BF16, torch.float16: OZK_F16, torch.float32: OZK_F32,
+                    torch.float64: OZK_F64})
+    _torch = torch
+    return torch
 
 
 def _dtype(t):
     """The ozk_dtype of a torch dtype."""
-    if not _DTYPES:
-        import torch
-
-        _DTYPES.update({torch.bfloat16: OZK_BF16, torch.float16: OZK_F16, torch.float32: OZK_F32,
-                        torch.float64: OZK_F64})
     try:
         return _DTYPES[t]
     except KeyError:
@@ -329,48 +339,62 @@ def _format(fmt):
         raise ValueError(f"unknown 4-bit format {fmt!r} (nvfp4, mxfp4)") from None
 
 
+def _stream_on(device, stream):
+    """Handle of the given stream, or of the device's current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _empty(shape, dtype, device, stream):
     """A new tensor whose memory belongs to the stream that writes it."""
-    import torch
-
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _torch.empty(shape, dtype=dtype, device=device)
+    with _torch.cuda.stream(stream):
+        return _torch.empty(shape, dtype=dtype, device=device)
 
 
 def _result(out, shape, dtype, device, stream):
+    """out, or a new tensor; dtype None: out's own."""
+    if device.type != "cuda":
+        raise ValueError("expected CUDA tensors")
     if out is None:
         return _empty(shape, dtype, device, stream)
     if tuple(out.shape) != tuple(shape):
         raise ValueError(f"out has shape {tuple(out.shape)}, the result {tuple(shape)}")
     if dtype is not None and out.dtype != dtype:
         raise TypeError(f"out is {out.dtype}, the result {dtype}")
+    if out.device != device:
+        raise ValueError(f"out is on {out.device}, the operands on {device}")
     return out
 
 
-def _offsets(offsets, groups=None):
-    import torch
-
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous() or offsets.numel() < 2:
-        raise TypeError("offsets: a contiguous int32 vector of groups + 1 entries is expected")
-    if groups is not None and offsets.numel() != groups + 1:
-        raise ValueError(f"{offsets.numel()} offsets for {groups} groups")
-    return offsets
-
-
-def _cuda(*tensors):
+def _same_device(device, *tensors):
     for t in tensors:
-        if t is not None and not t.is_cuda:
-            raise ValueError("expected CUDA tensors")
+        if t.device != device:
+            raise ValueError(f"operands on {device} and {t.device}")
+
+
+def _offsets(offsets, groups=None):
+    n = offsets.numel()
+    if offsets.dtype != _torch.int32 or offsets.dim() != 1 or n < 2 or not offsets.is_contiguous():
+        raise TypeError("offsets: a contiguous int32 vector of groups + 1 entries is expected")
+    if groups is not None and n != groups + 1:
+        raise ValueError(f"{n} offsets for {groups} groups")
+    return n - 1
 
 
 def _ld3(t):
     """(leading dimension, group stride) in elements of a [groups, rows, columns] tensor with unit column stride."""
-    if t.dim() != 3 or (t.stride(2) != 1 and t.size(2) > 1):
+    if t.dim() != 3:
         raise ValueError("expected a [groups, rows, columns] tensor with unit column stride")
-    ld = max(t.stride(1) if t.size(1) > 1 else t.size(2), t.size(2), 1)
-    return ld, max(t.stride(0) if t.size(0) > 1 else 0, (t.size(1) - 1) * ld + t.size(2))
+    (g, r, c), (sg, sr, sc) = t.shape, t.stride()
+    if sc != 1 and c > 1:
+        raise ValueError("expected a [groups, rows, columns] tensor with unit column stride")
+    ld = sr if r > 1 and sr > c else max(c, 1)
+    if r > 1 and sr < c or g > 1 and sg < (r - 1) * ld + c:
+        raise ValueError("rows or groups that overlap")
+    return ld, sg if g > 1 else r * ld
 
 
 class Mx4:
@@ -381,82 +405,87 @@ class Mx4:
     __slots__ = ("codes", "scales", "rows", "K", "fmt", "groups", "offsets")
 
     def __init__(self, codes, scales, rows, K, fmt, groups=1, offsets=None):
-        f = _format(fmt)
+        if _torch is None:
+            _load_torch()
         if offsets is not None:
-            groups = _offsets(offsets).numel() - 1
+            groups = _offsets(offsets)
+        if codes.dtype != _torch.uint8 or scales.dtype != _torch.uint8:
+            raise TypeError("codes and scales: uint8 tensors are expected")
         if codes.numel() != rows * (-(-K // 64) * 32) or not codes.is_contiguous():
             raise ValueError("codes: rows x kpad / 2 contiguous bytes are expected")
         if scales.numel() < mx4_scale_bytes(rows, K, fmt, groups) or not scales.is_contiguous():
             raise ValueError("scales: too few bytes, or not contiguous")
-        if codes.element_size() != 1 or scales.element_size() != 1:
-            raise TypeError("codes and scales are bytes")
-        del f
+        if offsets is None and rows % groups:
+            raise ValueError(f"{rows} rows in {groups} equal groups")
+        _same_device(codes.device, scales)
         self.codes, self.scales, self.rows, self.K, self.fmt = codes, scales, rows, K, fmt
         self.groups, self.offsets = groups, offsets
 
 
 def mx4_scale_bytes(rows: int, K: int, fmt: str = "nvfp4", groups: int = 1) -> int:
-    return lib().ozk_mx4_scale_bytes(rows, K, _format(fmt), groups)
+    """ozk_mx4_scale_bytes, without the limits on its arguments."""
+    _format(fmt)
+    return (rows // 128 + groups) * -(-(-(-K // 64) * 64) // _WORD_COLUMNS[fmt]) * 512
 
 
 def mx4_quantize(x, fmt: str = "nvfp4", offsets=None, prescale: float = 1.0, stream=None) -> Mx4:
     """x as a microscaled 4-bit matrix (ozk_mx4_quantize).  x: [rows, K] with
     unit column stride, its rows in ragged groups where offsets (int32, on the
-    device) is given; or contiguous [groups, rows, K], one group per matrix."""
-    import torch
-
-    groups, f = 1, _format(fmt)
+    device) is given; or [groups, rows, K], one group per matrix."""
+    torch = _torch or _load_torch()
+    groups, f, device = 1, _format(fmt), x.device
+    if device.type != "cuda":
+        raise ValueError("expected a CUDA tensor")
     if x.dim() == 3:
         if offsets is not None:
             raise ValueError("offsets are for the rows of a 2-D matrix")
         groups = x.size(0)
-        x = x.reshape(groups * x.size(1), x.size(2)) if x.is_contiguous() else x.contiguous().flatten(0, 1)
+        if groups == 0:
+            raise ValueError("no groups")
+        x = x.reshape(groups * x.size(1), x.size(2))
     elif offsets is not None:
-        groups = _offsets(offsets).numel() - 1
-    _cuda(x, offsets)
+        groups = _offsets(offsets)
+        _same_device(device, offsets)
     ld = _ld(x)
     rows, K = x.shape
-    codes = _empty((rows, -(-K // 64) * 32), torch.uint8, x.device, stream)
-    scales = _empty((max(mx4_scale_bytes(rows, K, fmt, max(groups, 1)), 1),), torch.uint8, x.device, stream)
-    if groups:
-        _call("ozk_mx4_quantize", rows, K, _ptr(x), ld, _dtype(x.dtype), f, prescale, _ptr(offsets), groups,
-              _ptr(codes), _ptr(scales), _stream(stream))
-    return Mx4(codes, scales, rows, K, fmt, max(groups, 1), offsets)
+    codes = _empty((rows, -(-K // 64) * 32), torch.uint8, device, stream)
+    scales = _empty((mx4_scale_bytes(rows, K, fmt, groups),), torch.uint8, device, stream)
+    _call("ozk_mx4_quantize", rows, K, x.data_ptr(), ld, _dtype(x.dtype), f, prescale,
+          None if offsets is None else offsets.data_ptr(), groups, codes.data_ptr(), scales.data_ptr(),
+          _stream_on(device, stream))
+    q = object.__new__(Mx4)
+    q.codes, q.scales, q.rows, q.K, q.fmt, q.groups, q.offsets = codes, scales, rows, K, fmt, groups, offsets
+    return q
 
 
 def mx4_dequantize(q: Mx4, dtype=None, out=None, stream=None):
     """The values q stands for, [rows, K] of dtype (default float32).  Rows in
     no group are not written."""
-    import torch
-
-    if dtype is None:
-        dtype = torch.float32 if out is None else out.dtype
-    out = _result(out, (q.rows, q.K), dtype, q.codes.device, stream)
-    _cuda(q.codes, out)
-    _call("ozk_mx4_dequantize", q.rows, q.K, _ptr(q.codes), _ptr(q.scales), _FORMATS[q.fmt], _ptr(q.offsets), q.groups,
-          _ptr(out), _ld(out), _dtype(out.dtype), _stream(stream))
+    device = q.codes.device
+    if dtype is None and out is None:
+        dtype = _torch.float32
+    out = _result(out, (q.rows, q.K), dtype, device, stream)
+    _call("ozk_mx4_dequantize", q.rows, q.K, q.codes.data_ptr(), q.scales.data_ptr(), _FORMATS[q.fmt],
+          None if q.offsets is None else q.offsets.data_ptr(), q.groups, out.data_ptr(), _ld(out), _dtype(out.dtype),
+          _stream_on(device, stream))
     return out
-
-
-def _same_format(a, b):
-    if a.fmt != b.fmt or a.K != b.K:
-        raise ValueError(f"operands differ: {a.fmt}, K = {a.K} and {b.fmt}, K = {b.K}")
 
 
 def mx4_gemm(a: Mx4, b: Mx4, alpha: float = 1.0, out_dtype=None, out=None, stream=None):
     """alpha * A @ B^T of two 4-bit matrices of one group each (ozk_mx4_gemm):
     [a.rows, b.rows] of out_dtype (default bfloat16)."""
-    import torch
-
-    _same_format(a, b)
+    if a.fmt != b.fmt or a.K != b.K:
+        raise ValueError(f"operands differ: {a.fmt}, K = {a.K} and {b.fmt}, K = {b.K}")
     if a.groups != 1 or b.groups != 1 or a.offsets is not None or b.offsets is not None:
         raise ValueError("matrices of one group are expected; mx4_grouped_gemm takes grouped ones")
-    if out_dtype is None:
-        out_dtype = torch.bfloat16 if out is None else out.dtype
-    out = _result(out, (a.rows, b.rows), out_dtype, a.codes.device, stream)
-    _cuda(a.codes, b.codes, out)
-    _call("ozk_mx4_gemm", a.rows, b.rows, a.K, _ptr(a.codes), _ptr(a.scales), _ptr(b.codes), _ptr(b.scales),
-          _FORMATS[a.fmt], alpha, _ptr(out), _ld(out), _dtype(out.dtype), _stream(stream))
+    device = a.codes.device
+    _same_device(device, b.codes)
+    if out_dtype is None and out is None:
+        out_dtype = _torch.bfloat16
+    out = _result(out, (a.rows, b.rows), out_dtype, device, stream)
+    _call("ozk_mx4_gemm", a.rows, b.rows, a.K, a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(),
+          b.scales.data_ptr(), _FORMATS[a.fmt], alpha, out.data_ptr(), _ld(out), _dtype(out.dtype),
+          _stream_on(device, stream))
     return out
 
 
@@ -464,27 +493,30 @@ def mx4_grouped_gemm(x: Mx4, w: Mx4, alpha: float = 1.0, out_dtype=None, out=Non
     """alpha * x_t @ w_g(t)^T (ozk_mx4_grouped_gemm): x quantised with offsets,
     w from a [groups, N, K] tensor; [x.rows, N] of out_dtype (default
     bfloat16).  Rows in no group are not written."""
-    import torch
-
-    _same_format(x, w)
+    if x.fmt != w.fmt or x.K != w.K:
+        raise ValueError(f"operands differ: {x.fmt}, K = {x.K} and {w.fmt}, K = {w.K}")
     if x.offsets is None or w.offsets is not None or x.groups != w.groups:
         raise ValueError("rows quantised with offsets and weights of as many equal groups are expected")
-    if out_dtype is None:
-        out_dtype = torch.bfloat16 if out is None else out.dtype
+    device = x.codes.device
+    _same_device(device, w.codes)
+    if out_dtype is None and out is None:
+        out_dtype = _torch.bfloat16
     N = w.rows // w.groups
-    out = _result(out, (x.rows, N), out_dtype, x.codes.device, stream)
-    _cuda(x.codes, w.codes, out)
-    _call("ozk_mx4_grouped_gemm", x.rows, N, x.K, x.groups, _ptr(x.offsets), _ptr(x.codes), _ptr(x.scales),
-          _ptr(w.codes), _ptr(w.scales), _FORMATS[x.fmt], alpha, _ptr(out), _ld(out), _dtype(out.dtype),
-          _stream(stream))
+    out = _result(out, (x.rows, N), out_dtype, device, stream)
+    _call("ozk_mx4_grouped_gemm", x.rows, N, x.K, x.groups, x.offsets.data_ptr(), x.codes.data_ptr(),
+          x.scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(), _FORMATS[x.fmt], alpha, out.data_ptr(),
+          _ld(out), _dtype(out.dtype), _stream_on(device, stream))
     return out
 
 
-def _operands(*tensors):
-    first = tensors[0]
-    for t in tensors:
-        if t.dtype != first.dtype:
-            raise TypeError(f"operands of different types: {first.dtype} and {t.dtype}")
+def _grouped(first, second, offsets, groups):
+    """Checks what the operands of a grouped product share; their ozk_dtype."""
+    if _torch is None:
+        _load_torch()
+    if first.dtype != second.dtype:
+        raise TypeError(f"operands of different types: {first.dtype} and {second.dtype}")
+    _same_device(first.device, second, offsets)
+    _offsets(offsets, groups)
     return _dtype(first.dtype)
 
 
@@ -492,47 +524,43 @@ def grouped_gemm(x, w, offsets, out_dtype=None, out=None, stream=None):
     """y[t] = x[t] @ w[g(t)]^T (ozk_grouped_gemm): x [T, K], w [groups, N, K] of
     one 16-bit type, offsets int32 [groups + 1] on the device; [T, N] of their
     type or float32.  Rows in no group are not written."""
-    kind = _operands(x, w)
     ld, stride = _ld3(w)
     groups, N, K = w.shape
+    kind = _grouped(x, w, offsets, groups)
     if x.dim() != 2 or x.size(1) != K:
         raise ValueError(f"x is {tuple(x.shape)}, the weights {tuple(w.shape)}")
-    _offsets(offsets, groups)
-    out = _result(out, (x.size(0), N), out_dtype or (x.dtype if out is None else None), x.device, stream)
-    _cuda(x, w, offsets, out)
-    _call("ozk_grouped_gemm", x.size(0), N, K, groups, _ptr(offsets), _ptr(x), _ld(x), _ptr(w), ld, stride, kind,
-          _ptr(out), _ld(out), _dtype(out.dtype), _stream(stream))
+    T, device = x.size(0), x.device
+    out = _result(out, (T, N), out_dtype or (x.dtype if out is None else None), device, stream)
+    _call("ozk_grouped_gemm", T, N, K, groups, offsets.data_ptr(), x.data_ptr(), _ld(x), w.data_ptr(), ld, stride,
+          kind, out.data_ptr(), _ld(out), _dtype(out.dtype), _stream_on(device, stream))
     return out
 
 
 def grouped_gemm_dx(dy, w, offsets, out_dtype=None, out=None, stream=None):
     """The gradient of grouped_gemm with respect to x: dx[t] = dy[t] @ w[g(t)], [T, K]."""
-    kind = _operands(dy, w)
     ld, stride = _ld3(w)
     groups, N, K = w.shape
+    kind = _grouped(dy, w, offsets, groups)
     if dy.dim() != 2 or dy.size(1) != N:
         raise ValueError(f"dy is {tuple(dy.shape)}, the weights {tuple(w.shape)}")
-    _offsets(offsets, groups)
-    out = _result(out, (dy.size(0), K), out_dtype or (dy.dtype if out is None else None), dy.device, stream)
-    _cuda(dy, w, offsets, out)
-    _call("ozk_grouped_gemm_dx", dy.size(0), N, K, groups, _ptr(offsets), _ptr(dy), _ld(dy), _ptr(w), ld, stride, kind,
-          _ptr(out), _ld(out), _dtype(out.dtype), _stream(stream))
+    T, device = dy.size(0), dy.device
+    out = _result(out, (T, K), out_dtype or (dy.dtype if out is None else None), device, stream)
+    _call("ozk_grouped_gemm_dx", T, N, K, groups, offsets.data_ptr(), dy.data_ptr(), _ld(dy), w.data_ptr(), ld,
+          stride, kind, out.data_ptr(), _ld(out), _dtype(out.dtype), _stream_on(device, stream))
     return out
 
 
 def grouped_gemm_dw(dy, x, offsets, out_dtype=None, out=None, stream=None):
     """The gradient with respect to w: dw[g] = the sum of dy[t]^T x[t] over the
     rows of group g, [groups, N, K] (zeros for a group without rows)."""
-    kind = _operands(dy, x)
+    kind = _grouped(dy, x, offsets, None)
     if dy.dim() != 2 or x.dim() != 2 or dy.size(0) != x.size(0):
         raise ValueError(f"dy is {tuple(dy.shape)}, x {tuple(x.shape)}")
-    groups = _offsets(offsets).numel() - 1
-    T, N, K = dy.size(0), dy.size(1), x.size(1)
-    out = _result(out, (groups, N, K), out_dtype or (x.dtype if out is None else None), x.device, stream)
-    _cuda(dy, x, offsets, out)
+    groups, T, N, K, device = offsets.numel() - 1, dy.size(0), dy.size(1), x.size(1), dy.device
+    out = _result(out, (groups, N, K), out_dtype or (x.dtype if out is None else None), device, stream)
     ld, stride = _ld3(out)
-    _call("ozk_grouped_gemm_dw", T, N, K, groups, _ptr(offsets), _ptr(dy), _ld(dy), _ptr(x), _ld(x), kind, _ptr(out),
-          ld, stride, _dtype(out.dtype), _stream(stream))
+    _call("ozk_grouped_gemm_dw", T, N, K, groups, offsets.data_ptr(), dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x),
+          kind, out.data_ptr(), ld, stride, _dtype(out.dtype), _stream_on(device, stream))
     return out
 
 
