@@ -23,8 +23,8 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstring>
-#include <cstdlib>
 #include <map>
 #include <mutex>
 
@@ -51,15 +51,17 @@ struct Config {
   static constexpr bool PAIR = PAIR_;
   static constexpr int BN = BN_;
   static constexpr bool MX = OP == kMx4;
-  static constexpr bool A_MN = OP == kGradRows || OP == kGradWeights;  // M side read across K
+  // operands read across K: the weights of the gradient of x, both of the gradient of w
+  static constexpr bool A_MN = OP == kGradRows || OP == kGradWeights;
   static constexpr bool B_MN = OP == kGradWeights;
-  static constexpr int CTAS = PAIR ? 2 : 1;
+  static constexpr int CTAS = PAIR ? 2 : 1;               // CTAs a tile is laid across
   static constexpr int BLOCK_K = MX ? 256 : 64;          // K elements of a stage
   static constexpr int MMA_K = MX ? 64 : 16;             // of one MMA: 32 bytes
   static constexpr int B_ROWS = BN / CTAS;               // N rows a CTA stages
-  static constexpr int BOX = B_MN ? 64 : (BN >= 256 ? 64 : 32);  // rows of one B copy
+  // grouped rows (gradient of w: columns of dy, one slab) of one copy
+  static constexpr int BOX = OP == kGradWeights || BN >= 256 ? 64 : 32;
   static constexpr uint32_t B_BYTES = B_ROWS * kRowBytes;
-  static constexpr uint32_t BOX_BYTES = (B_MN ? 64 : BOX) * kRowBytes;
+  static constexpr uint32_t BOX_BYTES = BOX * kRowBytes;
   static constexpr int KG = FMT == kNv ? 4 : 2;          // scale words of a stage
   static constexpr int NB = (BN + 127) / 128;            // 128-row scale tiles of the N side
   static constexpr uint32_t SFA_BYTES = MX ? KG * kScaleTile : 0;
@@ -76,11 +78,14 @@ struct Config {
   static constexpr uint32_t ACC1 = SHARED ? TMEM - SF_COLS - BN : BN;  // first column of the second accumulator
   static constexpr uint32_t SF_BASE = TMEM - SF_COLS;
   static_assert(!SHARED || (BN == 256 && ACC1 >= 192), "the shared columns lie in two blocks of 32 of each accumulator");
-  // full, empty, tail and peer tail per stage; accumulator full and empty; drain
-  static constexpr int BARS = 4 * STAGES + 5;
-  static constexpr uint32_t FIXED = 1024 + STAGES * STAGE + 256;
+  // full, empty, tail and peer tail per stage (the tails: gradient of w);
+  // accumulator full and empty; drain
+  static constexpr int BARS = (OP == kGradWeights ? 4 : 2) * STAGES + 5;
+  static constexpr uint32_t OUT_STAGE = 2048;            // one epilogue warp's 32 x 32 block in 16 bits
+  static constexpr uint32_t FIXED = 1024 + STAGES * STAGE + kEpiWarps * OUT_STAGE + 256;
   static_assert(8 * BARS + 8 <= 256, "barriers");
-  static_assert(BN % 32 == 0 && B_ROWS % BOX == 0, "tile");
+  static_assert(FIXED + 4 * (3 * kMaxGroups + 1) <= 232448, "shared memory");
+  static_assert(BN % 32 == 0 && B_ROWS % BOX == 0, "copies of whole boxes fill a stage exactly");
 };
 
 struct ProductParams {
@@ -91,6 +96,7 @@ struct ProductParams {
   int out_type;
   int64_t ldo, out_group;
   float alpha;
+  bool vec;        // 16-byte stores: a 16-bit output whose rows are 16-byte aligned
   uint32_t idesc;  // types, majorness, M; N is filled in per tile
 };
 
@@ -101,6 +107,13 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
 }
+
+// A value that is the same in every lane, made so for the compiler: loops and
+// addresses built on it then run on the warp's uniform registers, which TMA
+// and MMA instructions take their operands from.  With the loops inside a
+// one-thread branch every operand was moved over for every instruction, and
+// the loader took 380 cycles a stage.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 
 __device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -220,7 +233,7 @@ __device__ __forceinline__ void build_groups(const ProductParams& p, const Group
   if (lane == 0) g.first[p.groups] = carry;
 }
 
-struct Tile {
+struct Tile {  // the same in every lane
   int e, row0;     // group and its first row
   int m0, n0;      // first output column; first output row within the group
   int n;           // output rows of the tile
@@ -230,21 +243,26 @@ struct Tile {
 
 template <typename C, ProductOp OP>
 __device__ __forceinline__ Tile tile_at(const ProductParams& p, const Groups& g, int u, int& e) {
-  while (u >= g.first[e + 1]) ++e;  // u only grows
+  while (u >= uniform(g.first[e + 1])) ++e;  // u only grows
   Tile t;
   t.e = e;
-  t.row0 = g.row0[e];
-  const int in = u - g.first[e];
-  const int total_n = OP == kGradWeights ? p.N : g.rows[e];
+  t.row0 = uniform(g.row0[e]);
+  const int in = u - uniform(g.first[e]);
+  const int rows = uniform(g.rows[e]);
+  const int total_n = OP == kGradWeights ? p.N : rows;
   const int tn = (total_n + C::BN - 1) / C::BN;
   const int super = in / (kSuper * tn);
   const int gm = min(kSuper, p.tiles_m - super * kSuper);
   const int r = in - super * kSuper * tn;
   t.m0 = (super * kSuper + r % gm) * (kTileRows * C::CTAS);
-  t.n0 = r / gm * C::BN;
-  t.n = min(C::BN, total_n - t.n0);
+  // rows in equal tiles, not full ones and a rest: their MMAs and copies take
+  // time in proportion to their rows, and equal ones fill the SMs evenly
+  // (4-bit rows keep whole tiles, as their scale tiles lie)
+  const int step = C::MX || tn == 0 ? C::BN : ((total_n + tn - 1) / tn + 31) / 32 * 32;
+  t.n0 = r / gm * step;
+  t.n = min(step, total_n - t.n0);
   t.half = C::PAIR ? (t.n + 31) / 32 * 16 : (t.n + 15) / 16 * 16;
-  t.k = OP == kGradWeights ? g.rows[e] : p.K;
+  t.k = OP == kGradWeights ? rows : p.K;
   t.blocks = (t.k + C::BLOCK_K - 1) / C::BLOCK_K;
   return t;
 }
@@ -275,13 +293,88 @@ __device__ __forceinline__ void store_block(T* out, int64_t ldo, int rows, bool 
     if (c < rows && in_m) out[c * ldo] = out_of<T>(__uint_as_float(v[c]) * alpha);
 }
 
+// The same block of a 16-bit output with rows that start on 16 bytes.  A lane
+// of TMEM is an output column, so a thread that reads its lane holds values
+// that lie a whole row apart in the output; stored from there they take 32
+// two-byte stores.  Read in the 16 x 256-bit form, four lanes share an
+// accumulator row, pairs of output rows pack into a register, and stmatrix
+// writes the 8 x 8 pieces transposed: rows of 32 output columns (64 bytes,
+// 16-byte pieces swizzled by the row), which go out in four 16-byte stores a
+// thread.
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_rows(uint32_t (&a)[16], uint32_t (&b)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
+                 "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]), "+r"(a[15]),
+                 "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]), "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7]),
+                 "+r"(b[8]), "+r"(b[9]), "+r"(b[10]), "+r"(b[11]), "+r"(b[12]), "+r"(b[13]), "+r"(b[14]), "+r"(b[15])
+               :
+               : "memory");
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack16(uint32_t lo, uint32_t hi, float alpha) {
+  uint32_t r;
+  const float l = __uint_as_float(lo) * alpha, h = __uint_as_float(hi) * alpha;
+  if constexpr (std::is_same<T, __half>::value) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(h), "f"(l));
+  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(h), "f"(l));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void store_block_vec(T* out, int64_t ldo, int rows, int cols, uint32_t stage, int lane,
+                                                const uint32_t (&lo)[16], const uint32_t (&hi)[16], float alpha) {
+  // lane l gives the address of row l % 8 of piece l / 8: output rows 8 (2 q + l / 16) .. and columns 16 half + 8 (l / 8 % 2) ..
+  const int piece = lane >> 3;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const uint32_t(&v)[16] = half ? hi : lo;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int n = 8 * (2 * q + (piece >> 1)) + (lane & 7);
+      const int chunk = 2 * half + (piece & 1);
+      const uint32_t addr = stage + static_cast<uint32_t>(n * 64 + ((chunk ^ ((n >> 1) & 3)) * 16));
+      asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                   "r"(pack16<T>(v[8 * q], v[8 * q + 1], alpha)), "r"(pack16<T>(v[8 * q + 2], v[8 * q + 3], alpha)),
+                   "r"(pack16<T>(v[8 * q + 4], v[8 * q + 5], alpha)), "r"(pack16<T>(v[8 * q + 6], v[8 * q + 7], alpha))
+                   : "memory");
+    }
+  }
+  __syncwarp();
+  const int chunk = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = 8 * i + (lane >> 2);
+    uint4 w;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                 : "r"(stage + static_cast<uint32_t>(n * 64 + ((chunk ^ ((n >> 1) & 3)) * 16)))
+                 : "memory");
+    if (n >= rows) continue;
+    T* dst = out + n * ldo + 8 * chunk;
+    if (8 * chunk + 8 <= cols) {
+      *reinterpret_cast<uint4*>(dst) = w;
+    } else {
+      const T* e = reinterpret_cast<const T*>(&w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (8 * chunk + j < cols) dst[j] = e[j];
+    }
+  }
+  __syncwarp();
+}
+
 template <ProductOp OP, int FMT, int BN, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
-    product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+    product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmR,
+                   const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmSR,
                    const ProductParams p) {
   using C = Config<OP, FMT, BN, PAIR>;
-  grid_dependency_sync();
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -289,16 +382,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sB = sA + C::STAGES * kABytes;
   const uint32_t sSA = sB + C::STAGES * C::B_BYTES;
   const uint32_t sSB = sSA + C::STAGES * C::SFA_BYTES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE);
+  uint8_t* out_stage = smem + C::STAGES * C::STAGE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(out_stage + kEpiWarps * C::OUT_STAGE);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   Groups g;
-  g.first = reinterpret_cast<int*>(smem + C::STAGES * C::STAGE + 256);
+  g.first = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 256);
   g.row0 = g.first + p.groups + 1;
   g.rows = g.row0 + p.groups;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = PAIR ? cluster_rank() : 0;
+  const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_rank() : 0;               // in a pair
   const bool leader = rank == 0;
   const uint32_t full0 = smem_u32(bars);
   const uint32_t empty0 = full0 + 8 * C::STAGES;
@@ -312,8 +406,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
-      mbar_init(tail0 + 8 * s, 1);
-      mbar_init(peer0 + 8 * s, 1);
+      if (OP == kGradWeights) {
+        mbar_init(tail0 + 8 * s, 1);
+        mbar_init(peer0 + 8 * s, 1);
+      }
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf0 + 8 * b, 1);
@@ -322,8 +418,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(drain, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    prefetch_tmap(&tmA);
-    prefetch_tmap(&tmB);
+    prefetch_tmap(&tmW);
+    prefetch_tmap(&tmR);
   }
   if (warp == 1) {
     if (PAIR) {
@@ -334,43 +430,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_relinquish();
     }
   }
+  // the set-up above touches nothing the kernel before this one writes
+  grid_dependency_sync();
   if (warp == 2) build_groups<C, OP>(p, g, lane);
   tc_fence_before();
   __syncthreads();
-  if (PAIR) cluster_sync();
+  if (C::CTAS > 1) cluster_sync();
   tc_fence_after();
-  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
-  const int units = g.first[p.groups];
+  const uint32_t tmem_base = static_cast<uint32_t>(uniform(static_cast<int>(*reinterpret_cast<volatile uint32_t*>(tmem_slot))));
+  const int units = uniform(g.first[p.groups]);
   const int unit0 = static_cast<int>(blockIdx.x) / C::CTAS, unit_step = static_cast<int>(gridDim.x) / C::CTAS;
 
-  if (warp == 0) {
-    // ------------------------------ TMA producer ------------------------------
-    if (elect_one()) {
-      int stage = 0, e = 0;
-      uint32_t phase = 0;
-      int issued_parity[C::STAGES];
-      for (int s = 0; s < C::STAGES; ++s) issued_parity[s] = -1;
-      uint32_t tails = 0;  // bit s: parity of the next tail in stage s
-      int tail_stage = -1;
-      bool ok = true;
-      for (int u = unit0; u < units && ok; u += unit_step) {
-        const Tile t = tile_at<C, OP>(p, g, u, e);
-        const int m0 = t.m0 + static_cast<int>(rank) * kTileRows;
-        const int n0 = t.n0 + static_cast<int>(rank) * t.half;
-        const int boxes = (t.half + C::BOX - 1) / C::BOX;
-        const uint32_t bytes = kABytes + static_cast<uint32_t>(boxes) * C::BOX_BYTES + C::SFA_BYTES + C::SFB_BYTES;
-        for (int kb = 0; kb < t.blocks; ++kb) {
-          if (!mbar_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, kTimeoutNs)) {
-            ok = false;
-            break;
-          }
-          const bool clear = has_tail<OP>(t) && kb == t.blocks - 1;
+  if (warp == 0 || warp == 3) {
+    // ------------------------------ TMA producers ------------------------------
+    // Two warps fill the stages in turn: filling one takes a warp about 330
+    // cycles (waits, barrier, two to four copies), more than a stage of a
+    // small tile takes to arrive or to be used.
+    int stage = 0, e = 0, issued = 0;
+    const int turn = warp == 3;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = unit0; u < units && ok; u += unit_step) {
+      const Tile t = tile_at<C, OP>(p, g, u, e);
+      const int m0 = t.m0 + static_cast<int>(rank) * kTileRows;
+      const int n0 = t.n0 + static_cast<int>(rank) * t.half;
+      const int boxes = (t.half + C::BOX - 1) / C::BOX;
+      const uint32_t bytes = kABytes + static_cast<uint32_t>(boxes) * C::BOX_BYTES + C::SFA_BYTES + C::SFB_BYTES;
+      for (int kb = 0; kb < t.blocks; ++kb) {
+        const bool mine = (issued & 1) == turn;
+        if (mine && !warp_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, kTimeoutNs)) {
+          ok = false;
+          break;
+        }
+        const bool clear = has_tail<OP>(t) && kb == t.blocks - 1;
+        if (mine && elect_one()) {
           uint32_t bar = full0 + 8 * stage;
           if (clear) {  // warp 2 passes the stage on once it has cleared the rows
             bar = tail0 + 8 * stage;
             mbar_expect_tx(bar, bytes);
-            tails ^= 1u << stage;
-            tail_stage = stage;
           } else if (!PAIR) {
             mbar_expect_tx(bar, bytes);
           } else {
@@ -387,106 +484,112 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           const uint32_t a = sA + stage * kABytes, b = sB + stage * C::B_BYTES;
           const int k0 = kb * C::BLOCK_K;
-          if constexpr (OP == kForward) load3(a, &tmA, k0, m0, t.e);
-          if constexpr (OP == kMx4) load3(a, &tmA, k0 / 2, m0, t.e);
+          if constexpr (OP == kForward) load3(a, &tmW, k0, m0, t.e);
+          if constexpr (OP == kMx4) load3(a, &tmW, k0 / 2, m0, t.e);
           if constexpr (OP == kGradRows) {
-            load3(a, &tmA, m0, k0, t.e);
-            load3(a + kABytes / 2, &tmA, m0 + 64, k0, t.e);
+            load3(a, &tmW, m0, k0, t.e);
+            load3(a + kABytes / 2, &tmW, m0 + 64, k0, t.e);
           }
           if constexpr (OP == kGradWeights) {
-            load2(a, &tmA, m0, t.row0 + k0);
-            load2(a + kABytes / 2, &tmA, m0 + 64, t.row0 + k0);
+            load2(a, &tmW, m0, t.row0 + k0);
+            load2(a + kABytes / 2, &tmW, m0 + 64, t.row0 + k0);
           }
           for (int j = 0; j < boxes; ++j) {
-            if constexpr (OP == kGradWeights) load2(b + j * C::BOX_BYTES, &tmB, n0 + 64 * j, t.row0 + k0);
-            else load2(b + j * C::BOX_BYTES, &tmB, C::MX ? k0 / 2 : k0, t.row0 + n0 + C::BOX * j);
+            if constexpr (OP == kGradWeights) load2(b + j * C::BOX_BYTES, &tmR, n0 + C::BOX * j, t.row0 + k0);
+            else load2(b + j * C::BOX_BYTES, &tmR, C::MX ? k0 / 2 : k0, t.row0 + n0 + C::BOX * j);
           }
           if constexpr (C::MX) {
-            // scale tiles: of these 128 weight rows, and of the tile's rows (both CTAs: all of them)
-            const int64_t wrow = static_cast<int64_t>(t.e) * p.M;
-            load3(sSA + stage * C::SFA_BYTES, &tmSA, 0, kb * C::KG, static_cast<int>(wrow / 128) + t.e + m0 / 128);
-            load3(sSB + stage * C::SFB_BYTES, &tmSB, 0, kb * C::KG, t.row0 / 128 + t.e + t.n0 / 128);
-          }
-          if (!clear) issued_parity[stage] = static_cast<int>(phase);
-          if (++stage == C::STAGES) {
-            stage = 0;
-            phase ^= 1u;
+            // scale tiles: of these weight rows, and of the tile's rows (on a pair both CTAs take all of them)
+            const int wrow = static_cast<int>(static_cast<int64_t>(t.e) * p.M / 128);
+            load3(sSA + stage * C::SFA_BYTES, &tmSW, 0, kb * C::KG, wrow + t.e + m0 / 128);
+            load3(sSB + stage * C::SFB_BYTES, &tmSR, 0, kb * C::KG, t.row0 / 128 + t.e + t.n0 / 128);
           }
         }
-      }
-      if (!ok) {  // let copies still in flight land before the CTA exits
-        if (leader)
-          for (int s = 0; s < C::STAGES; ++s)
-            if (issued_parity[s] >= 0) mbar_wait_drain(full0 + 8 * s, static_cast<uint32_t>(issued_parity[s]));
-        if (tail_stage >= 0) mbar_wait_drain(tail0 + 8 * tail_stage, ((tails >> tail_stage) & 1u) ^ 1u);
+        ++issued;
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
     }
+    if (!ok && leader && lane == 0)  // let copies still in flight land before the CTA exits
+      for (int i = max(issued - C::STAGES, 0); i < issued; ++i)
+        if ((i & 1) == turn) mbar_wait_drain(full0 + 8 * (i % C::STAGES), static_cast<uint32_t>(i / C::STAGES) & 1u);
     __syncwarp();
   } else if (warp == 1 && leader) {
     // ------------------------------ MMA issuer ------------------------------
-    if (elect_one()) {
-      int stage = 0, e = 0, ab = 0;
-      uint32_t phase = 0, aphase = 0;
-      bool ok = true, first = true;
-      for (int u = unit0; u < units && ok; u += unit_step) {
-        const Tile t = tile_at<C, OP>(p, g, u, e);
-        if (t.blocks == 0) continue;
-        // free: this accumulator's previous tile (two ago) is out; or, with
-        // shared columns, the tile before this one is out of them
-        if (C::SHARED ? (!first && !mbar_wait(acce0 + 8 * (ab ^ 1), ab ? aphase : aphase ^ 1u, abort_flag, kTimeoutNs))
-                      : !mbar_wait(acce0 + 8 * ab, aphase ^ 1u, abort_flag, kTimeoutNs))
+    // first TMEM column of a stage's scale word: of the M side, and of the N side
+    auto sfa_of = [&](int word) { return tmem_base + C::SF_BASE + 4u * word; };
+    auto sfb_of = [&](int word) { return tmem_base + C::SF_BASE + 4u * C::KG + 4u * C::NB * word; };
+    int stage = 0, e = 0, ab = 0;
+    uint32_t phase = 0, aphase = 0;
+    bool ok = true, first = true;
+    for (int u = unit0; u < units && ok; u += unit_step) {
+      const Tile t = tile_at<C, OP>(p, g, u, e);
+      if (t.blocks == 0) continue;
+      // free: this accumulator's previous tile (two ago) is out; or, with
+      // shared columns, the tile before this one is out of them
+      if (C::SHARED ? (!first && !warp_wait(acce0 + 8 * (ab ^ 1), ab ? aphase : aphase ^ 1u, abort_flag, kTimeoutNs))
+                    : !warp_wait(acce0 + 8 * ab, aphase ^ 1u, abort_flag, kTimeoutNs))
+        break;
+      first = false;
+      tc_fence_after();
+      const uint32_t d = tmem_base + (ab ? C::ACC1 : 0u);
+      const uint32_t idesc = p.idesc | (static_cast<uint32_t>(t.half * C::CTAS >> 3) << 17);
+      for (int kb = 0; kb < t.blocks; ++kb) {
+        if (!warp_wait(full0 + 8 * stage, phase, abort_flag, kTimeoutNs)) {
+          ok = false;
           break;
-        first = false;
+        }
         tc_fence_after();
-        const uint32_t d = tmem_base + (ab ? C::ACC1 : 0u);
-        const uint32_t idesc = p.idesc | (static_cast<uint32_t>(t.half * C::CTAS >> 3) << 17);
-        for (int kb = 0; kb < t.blocks; ++kb) {
-          if (!mbar_wait(full0 + 8 * stage, phase, abort_flag, kTimeoutNs)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t da = operand_desc<C::A_MN>(sA + stage * kABytes);
-          const uint64_t db = operand_desc<C::B_MN>(sB + stage * C::B_BYTES);
-          const int steps = min(4, (t.k - kb * C::BLOCK_K + C::MMA_K - 1) / C::MMA_K);
+        const uint64_t da = operand_desc<C::A_MN>(sA + stage * kABytes);
+        const uint64_t db = operand_desc<C::B_MN>(sB + stage * C::B_BYTES);
+        const int steps = min(4, (t.k - kb * C::BLOCK_K + C::MMA_K - 1) / C::MMA_K);
+        if (elect_one()) {
           if constexpr (C::MX) {
-            const uint32_t sfa = tmem_base + C::SF_BASE, sfb = sfa + 4 * C::KG;
 #pragma unroll
             for (int i = 0; i < C::KG; ++i) {
-              copy_scales<PAIR>(sfa + 4 * i, scale_desc(sSA + stage * C::SFA_BYTES + i * kScaleTile));
+              copy_scales<PAIR>(sfa_of(i), scale_desc(sSA + stage * C::SFA_BYTES + i * kScaleTile));
 #pragma unroll
               for (int r = 0; r < C::NB; ++r)
-                copy_scales<PAIR>(sfb + 4 * (C::NB * i + r),
+                copy_scales<PAIR>(sfb_of(i) + 4 * r,
                                   scale_desc(sSB + stage * C::SFB_BYTES + (r * C::KG + i) * kScaleTile));
             }
-            _Pragma("unroll") for (int s = 0; s < 4; ++s) if (s < steps) {
-              const int word = FMT == kNv ? s : s / 2;                       // scale word of the step
-              const uint32_t id = FMT == kNv ? 0u : 2u * (s & 1);            // its first byte
-              mma_scaled<FMT, PAIR>(d, da + 2ull * s, db + 2ull * s, idesc | (id << 4) | (id << 29), sfa + 4 * word,
-                                    sfb + 4 * C::NB * word, (kb > 0 || s > 0) ? 1u : 0u);
-            }
-          } else {
-            // 32 bytes of K, or 16 rows of 128 bytes
-            constexpr uint64_t step_a = C::A_MN ? (16 * kRowBytes) >> 4 : 2, step_b = C::B_MN ? (16 * kRowBytes) >> 4 : 2;
-            _Pragma("unroll") for (int s = 0; s < 4; ++s) if (s < steps) {
-              const uint32_t acc = (kb > 0 || s > 0) ? 1u : 0u;
+          }
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            if (s >= steps) continue;
+            const uint32_t acc = (kb > 0 || s > 0) ? 1u : 0u;
+            if constexpr (C::MX) {
+              const int word = FMT == kNv ? s : s / 2;             // scale word of the step
+              const uint32_t id = FMT == kNv ? 0u : 2u * (s & 1);  // its first byte
+              mma_scaled<FMT, PAIR>(d, da + 2ull * s, db + 2ull * s, idesc | (id << 4) | (id << 29), sfa_of(word),
+                                    sfb_of(word), acc);
+            } else {
+              // 32 bytes of K, or 16 rows of 128 bytes
+              constexpr uint64_t step_a = C::A_MN ? (16 * kRowBytes) >> 4 : 2;
+              constexpr uint64_t step_b = C::B_MN ? (16 * kRowBytes) >> 4 : 2;
               if (PAIR) mma_f16_pair(d, da + step_a * s, db + step_b * s, idesc, acc);
               else mma_f16(d, da + step_a * s, db + step_b * s, idesc, acc);
             }
           }
           if (PAIR) mma_commit_both(empty0 + 8 * stage);
           else mma_commit(empty0 + 8 * stage);
-          if (++stage == C::STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
         }
-        if (!ok) break;
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      if (elect_one()) {
         if (PAIR) mma_commit_both(accf0 + 8 * ab);
         else mma_commit(accf0 + 8 * ab);
-        ab ^= 1;
-        if (ab == 0) aphase ^= 1u;
       }
+      ab ^= 1;
+      if (ab == 0) aphase ^= 1u;
+    }
+    if (elect_one()) {
       if (PAIR) mma_commit_local(drain);
       else mma_commit(drain);
       mbar_wait_drain(drain, 0);
@@ -530,6 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 4) {
     // ------------------------------ epilogue ------------------------------
     const int quad = warp & 3, side = (warp - 4) >> 2;  // TMEM lanes 32 quad..; every other block of 32 columns
+    const uint32_t stage = smem_u32(out_stage) + static_cast<uint32_t>(warp - 4) * C::OUT_STAGE;
     int e = 0, ab = 0;
     uint32_t aphase = 0;
     for (int u = unit0; u < units; u += unit_step) {
@@ -547,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + (ab ? C::ACC1 : 0u);
       // blocks of 32 columns, alternating between the two warps of a lane
       // quadrant; of accumulator 0 with shared columns the last two first
-      constexpr int kBlocks = BN / 64;
+      constexpr int kBlocks = (BN + 63) / 64;
       bool held = has;
       auto release = [&]() {
         tc_fence_before();
@@ -562,6 +666,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < kBlocks; ++i) {
         const int c = 64 * (C::SHARED && ab == 0 ? (i + kBlocks - 1) % kBlocks : i) + 32 * side;
         const int rows = t.n - c;
+        const int64_t o = at + c * p.ldo;
+        if (p.vec) {
+          uint32_t lo[16], hi[16];
+          if (rows > 0) {
+            if (has) {
+              tmem_ld_rows(taddr + static_cast<uint32_t>(c), lo);
+              tmem_ld_rows(taddr + static_cast<uint32_t>(c) + (16u << 16), hi);
+              tmem_wait_rows(lo, hi);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) lo[j] = hi[j] = 0u;
+            }
+          }
+          if (held && (C::SHARED || i == kBlocks - 1)) release();
+          if (rows <= 0) continue;
+          const int cols = static_cast<int>(min(static_cast<int64_t>(32), p.M - (m - lane)));
+          if (p.out_type == OZK_F16)
+            store_block_vec(static_cast<__half*>(p.out) + o - lane, p.ldo, rows, cols, stage, lane, lo, hi, p.alpha);
+          else
+            store_block_vec(static_cast<__nv_bfloat16*>(p.out) + o - lane, p.ldo, rows, cols, stage, lane, lo, hi, p.alpha);
+          continue;
+        }
         uint32_t v[32];
         if (rows > 0) {
           if (has) {
@@ -574,7 +700,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (held && (C::SHARED || i == kBlocks - 1)) release();
         if (rows <= 0) continue;
-        const int64_t o = at + c * p.ldo;
         if (p.out_type == OZK_F32) store_block(static_cast<float*>(p.out) + o, p.ldo, rows, in_m, v, p.alpha);
         else if (p.out_type == OZK_F16) store_block(static_cast<__half*>(p.out) + o, p.ldo, rows, in_m, v, p.alpha);
         else store_block(static_cast<__nv_bfloat16*>(p.out) + o, p.ldo, rows, in_m, v, p.alpha);
@@ -588,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (PAIR) cluster_sync();
+  if (C::CTAS > 1) cluster_sync();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
@@ -617,9 +742,9 @@ bool make_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* 
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Once per device and kernel: the shared-memory opt-in, and for pairs the
-// number of clusters that fit the GPU at once.
-cudaError_t setup(const void* kernel, size_t smem, bool pair, int* resident) {
+// Once per device and kernel: the shared-memory opt-in, and the number of
+// clusters that fit the GPU at once.
+cudaError_t setup(const void* kernel, size_t smem, int cluster, int* resident) {
   struct Setup {
     cudaError_t err;
     int resident;
@@ -633,13 +758,13 @@ cudaError_t setup(const void* kernel, size_t smem, bool pair, int* resident) {
   auto it = done.find({dev, kernel});
   if (it == done.end()) {
     Setup s{cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)), 0};
-    if (s.err == cudaSuccess && pair) {
+    if (s.err == cudaSuccess && cluster > 1) {
       cudaLaunchConfig_t cfg = {};
       cudaLaunchAttribute attr[1];
       attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim = {2, 1, 1};
+      attr[0].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
       cfg.blockDim = dim3(kThreads);
-      cfg.gridDim = dim3(2);
+      cfg.gridDim = dim3(static_cast<unsigned>(cluster));
       cfg.dynamicSmemBytes = smem;
       cfg.attrs = attr;
       cfg.numAttrs = 1;
@@ -667,69 +792,71 @@ cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
   p.ldo = q.ldo;
   p.out_group = q.out_group;
   p.alpha = q.alpha;
-  const int64_t tile_m = kTileRows * C::CTAS;
-  p.tiles_m = static_cast<int>((q.M + tile_m - 1) / tile_m);
-  p.tiles_n = static_cast<int>((q.N + BN - 1) / BN);
+  p.vec = q.out_type != OZK_F32 && reinterpret_cast<uintptr_t>(q.out) % 16 == 0 && q.ldo % 8 == 0 &&
+          (OP != kGradWeights || q.groups == 1 || q.out_group % 8 == 0);
+  p.tiles_m = static_cast<int>((q.M + (kTileRows * C::CTAS) - 1) / (kTileRows * C::CTAS));
+  p.tiles_n = static_cast<int>((q.N + C::BN - 1) / C::BN);
   // D fp32; types; MN-major operands; M of the MMA
-  p.idesc = static_cast<uint32_t>(tile_m >> 4) << 24;
+  p.idesc = static_cast<uint32_t>(kTileRows * C::CTAS >> 4) << 24;
   if (C::MX) p.idesc |= (1u << 7) | (1u << 10) | (FMT == kMx ? 1u << 23 : 0u);
   else
     p.idesc |= (1u << 4) | (q.dtype == OZK_BF16 ? (1u << 7) | (1u << 10) : 0u) | (C::A_MN ? 1u << 15 : 0u) |
                (C::B_MN ? 1u << 16 : 0u);
 
-  CUtensorMap tmA, tmB, tmSA, tmSB;
-  std::memset(&tmA, 0, sizeof tmA);
-  std::memset(&tmB, 0, sizeof tmB);
-  std::memset(&tmSA, 0, sizeof tmSA);
-  std::memset(&tmSB, 0, sizeof tmSB);
+  CUtensorMap tmW, tmR, tmSW, tmSR;
+  std::memset(&tmW, 0, sizeof tmW);
+  std::memset(&tmR, 0, sizeof tmR);
+  std::memset(&tmSW, 0, sizeof tmSW);
+  std::memset(&tmSR, 0, sizeof tmSR);
   const bool loads = q.T > 0 && q.K != 0;  // otherwise no tile has a term, and nothing is read
   if (loads && !C::MX) {
     const CUtensorMapDataType type = q.dtype == OZK_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     const int64_t inner_rows = OP == kGradWeights ? q.N : q.K;
     const int64_t dims_b[2] = {inner_rows, q.T}, strides_b[1] = {2 * q.ld_rows};
-    const uint32_t box_b[2] = {64, C::B_MN ? 64u : static_cast<uint32_t>(C::BOX)};
-    if (!make_map(&tmB, type, 2, q.rows, dims_b, strides_b, box_b, true)) return cudaErrorInvalidValue;
+    const uint32_t box_b[2] = {64, static_cast<uint32_t>(C::BOX)};
+    if (!make_map(&tmR, type, 2, q.rows, dims_b, strides_b, box_b, true)) return cudaErrorInvalidValue;
     bool ok;
     if (OP == kGradWeights) {
       const int64_t dims[2] = {q.M, q.T}, strides[1] = {2 * q.ld_other};
       const uint32_t box[2] = {64, 64};
-      ok = make_map(&tmA, type, 2, q.other, dims, strides, box, true);
+      ok = make_map(&tmW, type, 2, q.other, dims, strides, box, true);
     } else {
       const int64_t dims[3] = {OP == kForward ? q.K : q.M, OP == kForward ? q.M : q.K, q.groups};
       const int64_t strides[2] = {2 * q.ld_other, 2 * q.other_group};
       const uint32_t box[3] = {64, OP == kForward ? 128u : 64u, 1};
-      ok = make_map(&tmA, type, 3, q.other, dims, strides, box, true);
+      ok = make_map(&tmW, type, 3, q.other, dims, strides, box, true);
     }
     if (!ok) return cudaErrorInvalidValue;
   }
   if (loads && C::MX) {
     const int64_t half = ozk_kpad(q.K) / 2, kg = mx4_kgroups(q.K, FMT);
     const int64_t dims_a[3] = {half, q.M, q.groups}, strides_a[2] = {half, half * q.M};
-    const uint32_t box_a[3] = {kRowBytes, kTileRows, 1};
+    const uint32_t box_a[3] = {kRowBytes, 128u, 1};
     const int64_t dims_b[2] = {half, q.T}, strides_b[1] = {half};
     const uint32_t box_b[2] = {kRowBytes, static_cast<uint32_t>(C::BOX)};
     const int64_t strides_s[2] = {kScaleTile, kScaleTile * kg};
     const int64_t dims_sa[3] = {kScaleTile / 4, kg, mx4_row_blocks(q.b.rows, q.b.groups)};
     const int64_t dims_sb[3] = {kScaleTile / 4, kg, mx4_row_blocks(q.T, q.groups)};
-    const uint32_t box_sa[3] = {kScaleTile / 4, C::KG, 1}, box_sb[3] = {kScaleTile / 4, C::KG, C::NB};
-    if (!make_map(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, q.b.codes, dims_a, strides_a, box_a, true) ||
-        !make_map(&tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, q.a.codes, dims_b, strides_b, box_b, true) ||
-        !make_map(&tmSA, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, q.b.scales, dims_sa, strides_s, box_sa, false) ||
-        !make_map(&tmSB, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, q.a.scales, dims_sb, strides_s, box_sb, false))
+    const uint32_t box_sa[3] = {kScaleTile / 4, C::KG, 1};
+    const uint32_t box_sb[3] = {kScaleTile / 4, C::KG, C::NB};
+    if (!make_map(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, q.b.codes, dims_a, strides_a, box_a, true) ||
+        !make_map(&tmR, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, q.a.codes, dims_b, strides_b, box_b, true) ||
+        !make_map(&tmSW, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, q.b.scales, dims_sa, strides_s, box_sa, false) ||
+        !make_map(&tmSR, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, q.a.scales, dims_sb, strides_s, box_sb, false))
       return cudaErrorInvalidValue;
   }
   auto kernel = product_kernel<OP, FMT, BN, PAIR>;
   const size_t table = (3 * static_cast<size_t>(q.groups) + 1) * sizeof(int);
   int resident = 0;
   cudaError_t e = setup(reinterpret_cast<const void*>(kernel),
-                        C::FIXED + (3 * static_cast<size_t>(kMaxGroups) + 1) * sizeof(int), PAIR, &resident);
+                        C::FIXED + (3 * static_cast<size_t>(kMaxGroups) + 1) * sizeof(int), C::CTAS, &resident);
   if (e != cudaSuccess) return e;
   // no more CTAs than there can be tiles; how many there are only the offsets say
   int64_t tiles = p.tiles_m;
   if (OP == kGradWeights) tiles *= static_cast<int64_t>(p.tiles_n) * q.groups;
-  else tiles *= std::min<int64_t>(q.T, q.T / BN + q.groups);
+  else tiles *= std::min<int64_t>(q.T, q.T / C::BN + q.groups);
   if (tiles == 0) return cudaSuccess;
-  int64_t slots = PAIR ? std::min(num_sms / 2, resident) : num_sms;
+  int64_t slots = C::CTAS > 1 ? std::min(num_sms / C::CTAS, resident) : num_sms;
   slots = std::min(slots, tiles);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -740,20 +867,40 @@ cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see grid_dependency_sync
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs = 1;
-  if (PAIR) {
+  if (C::CTAS > 1) {
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {2, 1, 1};
+    attr[1].val.clusterDim = {C::CTAS, 1, 1};
     cfg.numAttrs = 2;
   }
   cfg.attrs = attr;
-  return cudaLaunchKernelEx(&cfg, kernel, tmA, tmB, tmSA, tmSB, p);
+  return cudaLaunchKernelEx(&cfg, kernel, tmW, tmR, tmSW, tmSR, p);
 }
 
+// The form of the tiles, by modelled time: waves of tiles times (stages of a
+// tile x cycles of a stage + a tile's fixed cycles), for a CTA pair's tile of
+// 256 columns by up to 256 rows and for one CTA's of 128 by up to 128.  Rows
+// per group are taken as their mean (the offsets are on the device).  The
+// constants are measured: a stage takes about 330 cycles (4-bit 400) to issue
+// however few its rows; with full tiles a pair's takes the MMAs' 540 (650), a
+// CTA's the 450 (510) that 32 (36) KB take from L2 with every SM loading.
+// Both forms on the same box: 8192^3 NVFP4 pairs 160, single 233 us; 16 groups
+// of ~512 rows, 4096 -> 2048 bf16, 98 and 117; 1000 x 1537 x 2090 MXFP4 11.2
+// and 7.2; 32 rows in 32 groups, 4096 -> 2048 NVFP4, 21.7 and 19.6.
 template <ProductOp OP, int FMT>
 cudaError_t choose(const Product& q, int num_sms, cudaStream_t stream) {
-  const char* ev = getenv("OZK_PAIR");
-  if (ev && ev[0] == '1') return launch<OP, FMT, 256, true>(q, num_sms, stream);
-  return launch<OP, FMT, 128, false>(q, num_sms, stream);
+  const bool mx = OP == kMx4, sum_rows = OP == kGradWeights;
+  const double t = static_cast<double>(std::max<int64_t>(q.T, 1));
+  const double groups = sum_rows ? q.groups : std::min(static_cast<double>(q.groups), t);
+  const double rows = std::max(sum_rows ? static_cast<double>(q.N) : t / groups, 1.0);
+  const double stages = std::ceil((sum_rows ? t / groups : static_cast<double>(q.K)) / (mx ? 256 : 64));
+  auto cost = [&](int bn, int cols, int slots, double per_row, double fixed) {
+    const double per_group = std::ceil(rows / bn);
+    const double waves = std::ceil(groups * per_group * std::ceil(static_cast<double>(q.M) / cols) / slots);
+    return waves * (stages * std::max(mx ? 400.0 : 330.0, per_row * rows / per_group) + fixed);
+  };
+  const double pair = cost(256, 256, num_sms / 2, mx ? 2.55 : 2.1, 2500);
+  const double single = cost(128, 128, num_sms, mx ? 4.0 : 3.5, 2000);
+  return pair < single ? launch<OP, FMT, 256, true>(q, num_sms, stream) : launch<OP, FMT, 128, false>(q, num_sms, stream);
 }
 
 }  // namespace
