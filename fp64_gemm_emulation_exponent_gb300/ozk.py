@@ -320,6 +320,7 @@ def _load_torch():
 
     _DTYPES.update({torch.bfloat16: OZK_BF16, torch.float16: OZK_F16, torch.float32: OZK_F32,
                     torch.float64: OZK_F64})
+    lib()
     _torch = torch
     return torch
 
@@ -339,11 +340,9 @@ def _format(fmt):
         raise ValueError(f"unknown 4-bit format {fmt!r} (nvfp4, mxfp4)") from None
 
 
-def _stream_on(device, stream):
-    """Handle of the given stream, or of the device's current one."""
-    if stream is not None:
-        return stream.cuda_stream
-    return _torch._C._cuda_getCurrentRawStream(device.index)
+def _stream_at(index, stream):
+    """Handle of the given stream, or of the current one of a device."""
+    return _torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def _empty(shape, dtype, device, stream):
@@ -354,33 +353,41 @@ def _empty(shape, dtype, device, stream):
         return _torch.empty(shape, dtype=dtype, device=device)
 
 
-def _result(out, shape, dtype, device, stream):
-    """out, or a new tensor; dtype None: out's own."""
-    if device.type != "cuda":
-        raise ValueError("expected CUDA tensors")
+def _result(out, rows, cols, dtype, device, stream):
+    """(tensor, leading dimension, ozk_dtype) of a rows x cols result: out, or a new tensor; dtype None: out's own."""
     if out is None:
-        return _empty(shape, dtype, device, stream)
-    if tuple(out.shape) != tuple(shape):
-        raise ValueError(f"out has shape {tuple(out.shape)}, the result {tuple(shape)}")
+        if stream is None:
+            return _torch.empty((rows, cols), dtype=dtype, device=device), cols or 1, _DTYPES[dtype]
+        return _empty((rows, cols), dtype, device, stream), cols or 1, _DTYPES[dtype]
+    if out.shape != (rows, cols):
+        raise ValueError(f"out has shape {tuple(out.shape)}, the result ({rows}, {cols})")
     if dtype is not None and out.dtype != dtype:
         raise TypeError(f"out is {out.dtype}, the result {dtype}")
     if out.device != device:
         raise ValueError(f"out is on {out.device}, the operands on {device}")
-    return out
+    return out, _ld(out), _dtype(out.dtype)
 
 
-def _same_device(device, *tensors):
+def _device_index(t):
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("expected CUDA tensors")
+    return index
+
+
+def _same_device(index, *tensors):
     for t in tensors:
-        if t.device != device:
-            raise ValueError(f"operands on {device} and {t.device}")
+        if t.get_device() != index:
+            raise ValueError(f"operands on cuda:{index} and {t.device}")
 
 
-def _offsets(offsets, groups=None):
+def _offsets(offsets, index):
+    """The number of groups that offsets, a device vector, has."""
     n = offsets.numel()
     if offsets.dtype != _torch.int32 or offsets.dim() != 1 or n < 2 or not offsets.is_contiguous():
         raise TypeError("offsets: a contiguous int32 vector of groups + 1 entries is expected")
-    if groups is not None and n != groups + 1:
-        raise ValueError(f"{n} offsets for {groups} groups")
+    if offsets.get_device() != index:
+        raise ValueError(f"operands on cuda:{index} and {offsets.device}")
     return n - 1
 
 
@@ -391,7 +398,7 @@ def _ld3(t):
     (g, r, c), (sg, sr, sc) = t.shape, t.stride()
     if sc != 1 and c > 1:
         raise ValueError("expected a [groups, rows, columns] tensor with unit column stride")
-    ld = sr if r > 1 and sr > c else max(c, 1)
+    ld = sr if r > 1 and sr > c else c or 1
     if r > 1 and sr < c or g > 1 and sg < (r - 1) * ld + c:
         raise ValueError("rows or groups that overlap")
     return ld, sg if g > 1 else r * ld
@@ -402,29 +409,48 @@ class Mx4:
     ``codes`` and ``scales`` as ozk_mx4_quantize stores them (uint8 tensors),
     ``fmt`` "nvfp4" or "mxfp4"; ``offsets`` where the groups are ragged."""
 
-    __slots__ = ("codes", "scales", "rows", "K", "fmt", "groups", "offsets")
+    __slots__ = ("rows", "K", "fmt", "groups", "offsets", "device", "_memory", "_index", "_codes", "_scales")
 
     def __init__(self, codes, scales, rows, K, fmt, groups=1, offsets=None):
         if _torch is None:
             _load_torch()
+        index = _device_index(codes)
         if offsets is not None:
-            groups = _offsets(offsets)
+            groups = _offsets(offsets, index)
         if codes.dtype != _torch.uint8 or scales.dtype != _torch.uint8:
             raise TypeError("codes and scales: uint8 tensors are expected")
         if codes.numel() != rows * (-(-K // 64) * 32) or not codes.is_contiguous():
             raise ValueError("codes: rows x kpad / 2 contiguous bytes are expected")
         if scales.numel() < mx4_scale_bytes(rows, K, fmt, groups) or not scales.is_contiguous():
             raise ValueError("scales: too few bytes, or not contiguous")
-        if offsets is None and rows % groups:
+        if offsets is None and groups != 1 and rows % groups:
             raise ValueError(f"{rows} rows in {groups} equal groups")
-        _same_device(codes.device, scales)
-        self.codes, self.scales, self.rows, self.K, self.fmt = codes, scales, rows, K, fmt
-        self.groups, self.offsets = groups, offsets
+        _same_device(index, scales)
+        self.rows, self.K, self.fmt, self.groups, self.offsets = rows, K, fmt, groups, offsets
+        self._memory, self._index, self.device = (codes, scales), index, codes.device
+        self._codes, self._scales = codes.data_ptr(), scales.data_ptr()
+
+    @property
+    def codes(self):
+        if isinstance(self._memory, tuple):
+            return self._memory[0]
+        half = -(-self.K // 64) * 32
+        return self._memory[: self.rows * half].view(self.rows, half)
+
+    @property
+    def scales(self):
+        if isinstance(self._memory, tuple):
+            return self._memory[1]
+        return self._memory[self._scales - self._codes:]
+
+
+_new_mx4 = object.__new__
 
 
 def mx4_scale_bytes(rows: int, K: int, fmt: str = "nvfp4", groups: int = 1) -> int:
     """ozk_mx4_scale_bytes, without the limits on its arguments."""
-    _format(fmt)
+    if fmt not in _WORD_COLUMNS:
+        _format(fmt)
     return (rows // 128 + groups) * -(-(-(-K // 64) * 64) // _WORD_COLUMNS[fmt]) * 512
 
 
@@ -433,9 +459,10 @@ def mx4_quantize(x, fmt: str = "nvfp4", offsets=None, prescale: float = 1.0, str
     unit column stride, its rows in ragged groups where offsets (int32, on the
     device) is given; or [groups, rows, K], one group per matrix."""
     torch = _torch or _load_torch()
-    groups, f, device = 1, _format(fmt), x.device
-    if device.type != "cuda":
-        raise ValueError("expected a CUDA tensor")
+    groups, f, index, at = 1, _format(fmt), _device_index(x), None
+    if offsets is not None:
+        groups = _offsets(offsets, index)
+        at = offsets.data_ptr()
     if x.dim() == 3:
         if offsets is not None:
             raise ValueError("offsets are for the rows of a 2-D matrix")
@@ -443,49 +470,57 @@ def mx4_quantize(x, fmt: str = "nvfp4", offsets=None, prescale: float = 1.0, str
         if groups == 0:
             raise ValueError("no groups")
         x = x.reshape(groups * x.size(1), x.size(2))
-    elif offsets is not None:
-        groups = _offsets(offsets)
-        _same_device(device, offsets)
     ld = _ld(x)
     rows, K = x.shape
-    codes = _empty((rows, -(-K // 64) * 32), torch.uint8, device, stream)
-    scales = _empty((mx4_scale_bytes(rows, K, fmt, groups),), torch.uint8, device, stream)
-    _call("ozk_mx4_quantize", rows, K, x.data_ptr(), ld, _dtype(x.dtype), f, prescale,
-          None if offsets is None else offsets.data_ptr(), groups, codes.data_ptr(), scales.data_ptr(),
-          _stream_on(device, stream))
-    q = object.__new__(Mx4)
-    q.codes, q.scales, q.rows, q.K, q.fmt, q.groups, q.offsets = codes, scales, rows, K, fmt, groups, offsets
+    # codes, then scales, in one allocation
+    code_bytes = -(-rows * (-(-K // 64) * 32) // 256) * 256
+    size, device = code_bytes + mx4_scale_bytes(rows, K, fmt, groups), x.device
+    memory = torch.empty(size, dtype=torch.uint8, device=device) if stream is None else _empty(size, torch.uint8, device, stream)
+    codes = memory.data_ptr()
+    rc = _lib.ozk_mx4_quantize(rows, K, x.data_ptr(), ld, _dtype(x.dtype), f, prescale, at, groups, codes,
+                               codes + code_bytes, _stream_at(index, stream))
+    if rc:
+        raise OzkError("ozk_mx4_quantize", rc)
+    q = _new_mx4(Mx4)
+    q.rows, q.K, q.fmt, q.groups, q.offsets, q.device = rows, K, fmt, groups, offsets, device
+    q._memory, q._index, q._codes, q._scales = memory, index, codes, codes + code_bytes
     return q
 
 
 def mx4_dequantize(q: Mx4, dtype=None, out=None, stream=None):
     """The values q stands for, [rows, K] of dtype (default float32).  Rows in
     no group are not written."""
-    device = q.codes.device
     if dtype is None and out is None:
         dtype = _torch.float32
-    out = _result(out, (q.rows, q.K), dtype, device, stream)
-    _call("ozk_mx4_dequantize", q.rows, q.K, q.codes.data_ptr(), q.scales.data_ptr(), _FORMATS[q.fmt],
-          None if q.offsets is None else q.offsets.data_ptr(), q.groups, out.data_ptr(), _ld(out), _dtype(out.dtype),
-          _stream_on(device, stream))
+    out, ld, kind = _result(out, q.rows, q.K, dtype, q.device, stream)
+    rc = _lib.ozk_mx4_dequantize(q.rows, q.K, q._codes, q._scales, _FORMATS[q.fmt],
+                                 None if q.offsets is None else q.offsets.data_ptr(), q.groups, out.data_ptr(), ld, kind,
+                                 _stream_at(q._index, stream))
+    if rc:
+        raise OzkError("ozk_mx4_dequantize", rc)
     return out
+
+
+def _pair_of(a, b):
+    if a.fmt != b.fmt or a.K != b.K:
+        raise ValueError(f"operands differ: {a.fmt}, K = {a.K} and {b.fmt}, K = {b.K}")
+    if a._index != b._index:
+        raise ValueError(f"operands on cuda:{a._index} and cuda:{b._index}")
 
 
 def mx4_gemm(a: Mx4, b: Mx4, alpha: float = 1.0, out_dtype=None, out=None, stream=None):
     """alpha * A @ B^T of two 4-bit matrices of one group each (ozk_mx4_gemm):
     [a.rows, b.rows] of out_dtype (default bfloat16)."""
-    if a.fmt != b.fmt or a.K != b.K:
-        raise ValueError(f"operands differ: {a.fmt}, K = {a.K} and {b.fmt}, K = {b.K}")
+    _pair_of(a, b)
     if a.groups != 1 or b.groups != 1 or a.offsets is not None or b.offsets is not None:
         raise ValueError("matrices of one group are expected; mx4_grouped_gemm takes grouped ones")
-    device = a.codes.device
-    _same_device(device, b.codes)
     if out_dtype is None and out is None:
         out_dtype = _torch.bfloat16
-    out = _result(out, (a.rows, b.rows), out_dtype, device, stream)
-    _call("ozk_mx4_gemm", a.rows, b.rows, a.K, a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(),
-          b.scales.data_ptr(), _FORMATS[a.fmt], alpha, out.data_ptr(), _ld(out), _dtype(out.dtype),
-          _stream_on(device, stream))
+    out, ld, kind = _result(out, a.rows, b.rows, out_dtype, a.device, stream)
+    rc = _lib.ozk_mx4_gemm(a.rows, b.rows, a.K, a._codes, a._scales, b._codes, b._scales, _FORMATS[a.fmt], alpha,
+                           out.data_ptr(), ld, kind, _stream_at(a._index, stream))
+    if rc:
+        raise OzkError("ozk_mx4_gemm", rc)
     return out
 
 
@@ -493,74 +528,88 @@ def mx4_grouped_gemm(x: Mx4, w: Mx4, alpha: float = 1.0, out_dtype=None, out=Non
     """alpha * x_t @ w_g(t)^T (ozk_mx4_grouped_gemm): x quantised with offsets,
     w from a [groups, N, K] tensor; [x.rows, N] of out_dtype (default
     bfloat16).  Rows in no group are not written."""
-    if x.fmt != w.fmt or x.K != w.K:
-        raise ValueError(f"operands differ: {x.fmt}, K = {x.K} and {w.fmt}, K = {w.K}")
+    _pair_of(x, w)
     if x.offsets is None or w.offsets is not None or x.groups != w.groups:
         raise ValueError("rows quantised with offsets and weights of as many equal groups are expected")
-    device = x.codes.device
-    _same_device(device, w.codes)
     if out_dtype is None and out is None:
         out_dtype = _torch.bfloat16
     N = w.rows // w.groups
-    out = _result(out, (x.rows, N), out_dtype, device, stream)
-    _call("ozk_mx4_grouped_gemm", x.rows, N, x.K, x.groups, x.offsets.data_ptr(), x.codes.data_ptr(),
-          x.scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(), _FORMATS[x.fmt], alpha, out.data_ptr(),
-          _ld(out), _dtype(out.dtype), _stream_on(device, stream))
+    out, ld, kind = _result(out, x.rows, N, out_dtype, x.device, stream)
+    rc = _lib.ozk_mx4_grouped_gemm(x.rows, N, x.K, x.groups, x.offsets.data_ptr(), x._codes, x._scales, w._codes, w._scales,
+                                   _FORMATS[x.fmt], alpha, out.data_ptr(), ld, kind, _stream_at(x._index, stream))
+    if rc:
+        raise OzkError("ozk_mx4_grouped_gemm", rc)
     return out
 
 
 def _grouped(first, second, offsets, groups):
-    """Checks what the operands of a grouped product share; their ozk_dtype."""
+    """(ozk_dtype, device index) that the operands of a grouped product share."""
     if _torch is None:
         _load_torch()
     if first.dtype != second.dtype:
         raise TypeError(f"operands of different types: {first.dtype} and {second.dtype}")
-    _same_device(first.device, second, offsets)
-    _offsets(offsets, groups)
-    return _dtype(first.dtype)
+    index = _device_index(first)
+    _same_device(index, second)
+    n = _offsets(offsets, index)
+    if groups is not None and n != groups:
+        raise ValueError(f"offsets of {n} groups, weights of {groups}")
+    return _dtype(first.dtype), index
 
 
 def grouped_gemm(x, w, offsets, out_dtype=None, out=None, stream=None):
     """y[t] = x[t] @ w[g(t)]^T (ozk_grouped_gemm): x [T, K], w [groups, N, K] of
     one 16-bit type, offsets int32 [groups + 1] on the device; [T, N] of their
     type or float32.  Rows in no group are not written."""
-    ld, stride = _ld3(w)
+    ldw, stride = _ld3(w)
     groups, N, K = w.shape
-    kind = _grouped(x, w, offsets, groups)
+    kind, index = _grouped(x, w, offsets, groups)
     if x.dim() != 2 or x.size(1) != K:
         raise ValueError(f"x is {tuple(x.shape)}, the weights {tuple(w.shape)}")
-    T, device = x.size(0), x.device
-    out = _result(out, (T, N), out_dtype or (x.dtype if out is None else None), device, stream)
-    _call("ozk_grouped_gemm", T, N, K, groups, offsets.data_ptr(), x.data_ptr(), _ld(x), w.data_ptr(), ld, stride,
-          kind, out.data_ptr(), _ld(out), _dtype(out.dtype), _stream_on(device, stream))
+    T = x.size(0)
+    out, ld, out_kind = _result(out, T, N, out_dtype or (x.dtype if out is None else None), x.device, stream)
+    rc = _lib.ozk_grouped_gemm(T, N, K, groups, offsets.data_ptr(), x.data_ptr(), _ld(x), w.data_ptr(), ldw, stride, kind,
+                               out.data_ptr(), ld, out_kind, _stream_at(index, stream))
+    if rc:
+        raise OzkError("ozk_grouped_gemm", rc)
     return out
 
 
 def grouped_gemm_dx(dy, w, offsets, out_dtype=None, out=None, stream=None):
     """The gradient of grouped_gemm with respect to x: dx[t] = dy[t] @ w[g(t)], [T, K]."""
-    ld, stride = _ld3(w)
+    ldw, stride = _ld3(w)
     groups, N, K = w.shape
-    kind = _grouped(dy, w, offsets, groups)
+    kind, index = _grouped(dy, w, offsets, groups)
     if dy.dim() != 2 or dy.size(1) != N:
         raise ValueError(f"dy is {tuple(dy.shape)}, the weights {tuple(w.shape)}")
-    T, device = dy.size(0), dy.device
-    out = _result(out, (T, K), out_dtype or (dy.dtype if out is None else None), device, stream)
-    _call("ozk_grouped_gemm_dx", T, N, K, groups, offsets.data_ptr(), dy.data_ptr(), _ld(dy), w.data_ptr(), ld,
-          stride, kind, out.data_ptr(), _ld(out), _dtype(out.dtype), _stream_on(device, stream))
+    T = dy.size(0)
+    out, ld, out_kind = _result(out, T, K, out_dtype or (dy.dtype if out is None else None), dy.device, stream)
+    rc = _lib.ozk_grouped_gemm_dx(T, N, K, groups, offsets.data_ptr(), dy.data_ptr(), _ld(dy), w.data_ptr(), ldw, stride,
+                                  kind, out.data_ptr(), ld, out_kind, _stream_at(index, stream))
+    if rc:
+        raise OzkError("ozk_grouped_gemm_dx", rc)
     return out
 
 
 def grouped_gemm_dw(dy, x, offsets, out_dtype=None, out=None, stream=None):
     """The gradient with respect to w: dw[g] = the sum of dy[t]^T x[t] over the
     rows of group g, [groups, N, K] (zeros for a group without rows)."""
-    kind = _grouped(dy, x, offsets, None)
+    kind, index = _grouped(dy, x, offsets, None)
     if dy.dim() != 2 or x.dim() != 2 or dy.size(0) != x.size(0):
         raise ValueError(f"dy is {tuple(dy.shape)}, x {tuple(x.shape)}")
-    groups, T, N, K, device = offsets.numel() - 1, dy.size(0), dy.size(1), x.size(1), dy.device
-    out = _result(out, (groups, N, K), out_dtype or (x.dtype if out is None else None), device, stream)
+    groups, (T, N), K = offsets.numel() - 1, dy.shape, x.size(1)
+    if out is None:
+        out = _empty((groups, N, K), out_dtype or x.dtype, x.device, stream)
+    elif out.shape != (groups, N, K):
+        raise ValueError(f"out has shape {tuple(out.shape)}, the result ({groups}, {N}, {K})")
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out is {out.dtype}, the result {out_dtype}")
+    else:
+        _same_device(index, out)
     ld, stride = _ld3(out)
-    _call("ozk_grouped_gemm_dw", T, N, K, groups, offsets.data_ptr(), dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x),
-          kind, out.data_ptr(), ld, stride, _dtype(out.dtype), _stream_on(device, stream))
+    rc = _lib.ozk_grouped_gemm_dw(T, N, K, groups, offsets.data_ptr(), dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x), kind,
+                                  out.data_ptr(), ld, stride, _dtype(out.dtype), _stream_at(index, stream))
+    if rc:
+        raise OzkError("ozk_grouped_gemm_dw", rc)
     return out
 
 
