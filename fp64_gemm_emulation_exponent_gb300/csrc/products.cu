@@ -42,6 +42,9 @@ constexpr uint32_t kABytes = kTileRows * kRowBytes;       // 16 KB
 constexpr uint32_t kScaleTile = 512;                      // 128 rows x 4 scale bytes
 constexpr int kSuper = 16;       // tile rows of the M side that run together (L2 reuse)
 
+constexpr int kTableInts = 4 * kMaxGroups + 1;  // group table: see Groups
+constexpr int kSortGroups = 256;                // up to so many groups are put in order
+
 // Formats of an instance.  k16: 16-bit operands; the 4-bit ones differ in the
 // MMA's kind and in how many blocks a step of 64 takes (4 scale bytes, or 2).
 enum Format { kNv = OZK_NVFP4, kMx = OZK_MXFP4, k16 = 2 };
@@ -84,13 +87,14 @@ struct Config {
   static constexpr uint32_t OUT_STAGE = 2048;            // one epilogue warp's 32 x 32 block in 16 bits
   static constexpr uint32_t FIXED = 1024 + STAGES * STAGE + kEpiWarps * OUT_STAGE + 256;
   static_assert(8 * BARS + 8 <= 256, "barriers");
-  static_assert(FIXED + 4 * (3 * kMaxGroups + 1) <= 232448, "shared memory");
+  static_assert(FIXED + 4 * kTableInts <= 232448, "shared memory");
   static_assert(BN % 32 == 0 && B_ROWS % BOX == 0, "copies of whole boxes fill a stage exactly");
 };
 
 struct ProductParams {
   int T, M, N, K;
   int groups, tiles_m, tiles_n;  // tiles_n: of a group (gradient of w only)
+  bool sort;                     // groups by falling cost of a tile
   const int32_t* offsets;
   void* out;
   int out_type;
@@ -190,48 +194,90 @@ __device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, u
 // ---------------------------------------------------------------------------
 // The schedule
 // ---------------------------------------------------------------------------
-// Group table in shared memory: first tile, first row and rows of each group.
+// Group table in shared memory: first row and rows of each group; the groups
+// in the order their tiles run, and the first tile of each place in it.
 struct Groups {
-  int* first;  // groups + 1
   int* row0;
   int* rows;
+  int* order;
+  int* first;  // groups + 1
 };
 
-// Fills the table (one warp).  Offsets outside [0, T] or running backwards
-// are cut to an empty or shorter group, so every access stays inside the
-// operands, and latched as a fault.
+// Output rows of a tile of a group with `total` of them: equal tiles, not full
+// ones and a rest.  A tile's MMAs and copies take time in proportion to its
+// rows, and equal ones fill the SMs evenly.  4-bit rows keep whole tiles, as
+// their scale tiles lie.
 template <typename C, ProductOp OP>
-__device__ __forceinline__ void build_groups(const ProductParams& p, const Groups& g, int lane) {
-  int carry = 0;
-  for (int b = 0; b < p.groups; b += 32) {
-    const int e = b + lane;
-    int lo = 0, hi = 0;
-    if (e < p.groups) {
-      lo = p.offsets ? p.offsets[e] : 0;
-      hi = p.offsets ? p.offsets[e + 1] : p.T;
-      if (lo < 0 || hi < lo || hi > p.T) {
-        atomicOr(&g_status, 2);
-        lo = min(max(lo, 0), p.T);
-        hi = min(max(hi, lo), p.T);
-      }
-    }
-    int tiles = 0;
-    if (e < p.groups) tiles = (OP == kGradWeights ? p.tiles_n : (hi - lo + C::BN - 1) / C::BN) * p.tiles_m;
-    int sum = tiles;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const int v = __shfl_up_sync(0xFFFFFFFFu, sum, d);
-      if (lane >= d) sum += v;
-    }
-    if (e < p.groups) {
-      g.first[e] = carry + sum - tiles;
-      g.row0[e] = lo;
-      g.rows[e] = hi - lo;
-    }
-    carry += __shfl_sync(0xFFFFFFFFu, sum, 31);
-  }
-  if (lane == 0) g.first[p.groups] = carry;
+__device__ __forceinline__ int tile_rows(int total) {
+  if (C::MX) return C::BN;
+  const int tiles = max((total + C::BN - 1) / C::BN, 1);
+  return ((total + tiles - 1) / tiles + 31) / 32 * 32;
 }
+
+// Fills the table (all threads).  Offsets outside [0, T] or running backwards
+// are cut to an empty or shorter group, so every access stays inside the
+// operands, and latched as a fault.  Where tiles run in several waves, the
+// groups run by falling cost of a tile (its rows; for the gradient of w, the
+// rows it sums), so that the last wave, which not every CTA gets a tile of, is
+// that of the cheapest tiles.
+template <typename C, ProductOp OP>
+__device__ __forceinline__ void build_groups(const ProductParams& p, const Groups& g) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  for (int e = tid; e < p.groups; e += kThreads) {
+    int lo = p.offsets ? p.offsets[e] : 0, hi = p.offsets ? p.offsets[e + 1] : p.T;
+    if (lo < 0 || hi < lo || hi > p.T) {
+      atomicOr(&g_status, 2);
+      lo = min(max(lo, 0), p.T);
+      hi = min(max(hi, lo), p.T);
+    }
+    g.row0[e] = lo;
+    g.rows[e] = hi - lo;
+    g.order[e] = e;
+  }
+  __syncthreads();
+  if (p.sort) {  // at most kSortGroups groups: one thread each
+    int place = 0;
+    if (tid < p.groups) {
+      auto cost = [&](int rows) { return OP == kGradWeights ? rows : tile_rows<C, OP>(rows); };
+      const int mine = cost(g.rows[tid]);
+      for (int e = 0; e < p.groups; ++e) {
+        const int other = cost(g.rows[e]);
+        place += other > mine || (other == mine && e < tid);
+      }
+      g.order[place] = tid;
+    }
+    __syncthreads();
+  }
+  if (tid < 32) {
+    int carry = 0;
+    for (int b = 0; b < p.groups; b += 32) {
+      const int at = b + lane;
+      int tiles = 0;
+      if (at < p.groups)
+        tiles = (OP == kGradWeights ? p.tiles_n : (g.rows[g.order[at]] + C::BN - 1) / C::BN) * p.tiles_m;
+      int sum = tiles;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+        if (lane >= d) sum += v;
+      }
+      if (at < p.groups) g.first[at] = carry + sum - tiles;
+      carry += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    }
+    if (lane == 0) g.first[p.groups] = carry;
+  }
+}
+
+// The tiles of one CTA (pair) `me` of `all`: one of each wave, up the CTAs and
+// down again in turn, which evens out costs that fall along the schedule.
+// -1 past the last tile.
+struct Walk {
+  int me, all, tiles;
+  __device__ __forceinline__ int at(int wave) const {
+    const int u = wave * all + (wave & 1 ? all - 1 - me : me);
+    return u < tiles ? u : -1;
+  }
+};
 
 struct Tile {  // the same in every lane
   int e, row0;     // group and its first row
@@ -245,20 +291,17 @@ template <typename C, ProductOp OP>
 __device__ __forceinline__ Tile tile_at(const ProductParams& p, const Groups& g, int u, int& e) {
   while (u >= uniform(g.first[e + 1])) ++e;  // u only grows
   Tile t;
-  t.e = e;
-  t.row0 = uniform(g.row0[e]);
+  t.e = uniform(g.order[e]);
+  t.row0 = uniform(g.row0[t.e]);
   const int in = u - uniform(g.first[e]);
-  const int rows = uniform(g.rows[e]);
+  const int rows = uniform(g.rows[t.e]);
   const int total_n = OP == kGradWeights ? p.N : rows;
   const int tn = (total_n + C::BN - 1) / C::BN;
   const int super = in / (kSuper * tn);
   const int gm = min(kSuper, p.tiles_m - super * kSuper);
   const int r = in - super * kSuper * tn;
   t.m0 = (super * kSuper + r % gm) * (kTileRows * C::CTAS);
-  // rows in equal tiles, not full ones and a rest: their MMAs and copies take
-  // time in proportion to their rows, and equal ones fill the SMs evenly
-  // (4-bit rows keep whole tiles, as their scale tiles lie)
-  const int step = C::MX || tn == 0 ? C::BN : ((total_n + tn - 1) / tn + 31) / 32 * 32;
+  const int step = tile_rows<C, OP>(total_n);
   t.n0 = r / gm * step;
   t.n = min(step, total_n - t.n0);
   t.half = C::PAIR ? (t.n + 31) / 32 * 16 : (t.n + 15) / 16 * 16;
@@ -387,9 +430,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   Groups g;
-  g.first = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 256);
-  g.row0 = g.first + p.groups + 1;
+  g.row0 = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 256);
   g.rows = g.row0 + p.groups;
+  g.order = g.rows + p.groups;
+  g.first = g.order + p.groups;
 
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_rank() : 0;               // in a pair
@@ -432,14 +476,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // the set-up above touches nothing the kernel before this one writes
   grid_dependency_sync();
-  if (warp == 2) build_groups<C, OP>(p, g, lane);
+  build_groups<C, OP>(p, g);
   tc_fence_before();
   __syncthreads();
   if (C::CTAS > 1) cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = static_cast<uint32_t>(uniform(static_cast<int>(*reinterpret_cast<volatile uint32_t*>(tmem_slot))));
-  const int units = uniform(g.first[p.groups]);
-  const int unit0 = static_cast<int>(blockIdx.x) / C::CTAS, unit_step = static_cast<int>(gridDim.x) / C::CTAS;
+  const Walk walk{static_cast<int>(blockIdx.x) / C::CTAS, static_cast<int>(gridDim.x) / C::CTAS,
+                  uniform(g.first[p.groups])};
 
   if (warp == 0 || warp == 3) {
     // ------------------------------ TMA producers ------------------------------
@@ -450,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int turn = warp == 3;
     uint32_t phase = 0;
     bool ok = true;
-    for (int u = unit0; u < units && ok; u += unit_step) {
+    for (int wave = 0, u; ok && (u = walk.at(wave)) >= 0; ++wave) {
       const Tile t = tile_at<C, OP>(p, g, u, e);
       const int m0 = t.m0 + static_cast<int>(rank) * kTileRows;
       const int n0 = t.n0 + static_cast<int>(rank) * t.half;
@@ -524,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int stage = 0, e = 0, ab = 0;
     uint32_t phase = 0, aphase = 0;
     bool ok = true, first = true;
-    for (int u = unit0; u < units && ok; u += unit_step) {
+    for (int wave = 0, u; ok && (u = walk.at(wave)) >= 0; ++wave) {
       const Tile t = tile_at<C, OP>(p, g, u, e);
       if (t.blocks == 0) continue;
       // free: this accumulator's previous tile (two ago) is out; or, with
@@ -600,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int e = 0;
     unsigned pos = 0;  // stages the producer has filled before this tile
     uint32_t tails = 0;
-    for (int u = unit0; u < units; u += unit_step) {
+    for (int wave = 0, u; (u = walk.at(wave)) >= 0; ++wave) {
       const Tile t = tile_at<C, OP>(p, g, u, e);
       if (t.blocks > 0 && has_tail<OP>(t)) {
         const int stage = static_cast<int>((pos + t.blocks - 1) % C::STAGES);
@@ -636,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t stage = smem_u32(out_stage) + static_cast<uint32_t>(warp - 4) * C::OUT_STAGE;
     int e = 0, ab = 0;
     uint32_t aphase = 0;
-    for (int u = unit0; u < units; u += unit_step) {
+    for (int wave = 0, u; (u = walk.at(wave)) >= 0; ++wave) {
       const Tile t = tile_at<C, OP>(p, g, u, e);
       const int64_t m = t.m0 + static_cast<int>(rank) * kTileRows + quad * 32 + lane;
       const bool in_m = m < p.M;
@@ -846,10 +890,10 @@ cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
       return cudaErrorInvalidValue;
   }
   auto kernel = product_kernel<OP, FMT, BN, PAIR>;
-  const size_t table = (3 * static_cast<size_t>(q.groups) + 1) * sizeof(int);
+  const size_t table = (4 * static_cast<size_t>(q.groups) + 1) * sizeof(int);
   int resident = 0;
   cudaError_t e = setup(reinterpret_cast<const void*>(kernel),
-                        C::FIXED + (3 * static_cast<size_t>(kMaxGroups) + 1) * sizeof(int), C::CTAS, &resident);
+                        C::FIXED + kTableInts * sizeof(int), C::CTAS, &resident);
   if (e != cudaSuccess) return e;
   // no more CTAs than there can be tiles; how many there are only the offsets say
   int64_t tiles = p.tiles_m;
@@ -857,6 +901,7 @@ cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
   else tiles *= std::min<int64_t>(q.T, q.T / C::BN + q.groups);
   if (tiles == 0) return cudaSuccess;
   int64_t slots = C::CTAS > 1 ? std::min(num_sms / C::CTAS, resident) : num_sms;
+  p.sort = tiles > slots && q.groups > 1 && q.groups <= kSortGroups;
   slots = std::min(slots, tiles);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
