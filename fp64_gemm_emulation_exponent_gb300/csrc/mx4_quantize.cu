@@ -50,21 +50,6 @@ struct Mx4Params {
   uint8_t* scales;
 };
 
-template <typename T>
-__device__ __forceinline__ float to_f32(T v) {
-  if constexpr (std::is_same<T, __nv_bfloat16>::value) return __bfloat162float(v);
-  else if constexpr (std::is_same<T, __half>::value) return __half2float(v);
-  else if constexpr (std::is_same<T, double>::value) return __double2float_rn(v);
-  else return v;
-}
-template <typename T>
-__device__ __forceinline__ T from_f32(float v) {
-  if constexpr (std::is_same<T, __nv_bfloat16>::value) return __float2bfloat16_rn(v);
-  else if constexpr (std::is_same<T, __half>::value) return __float2half_rn(v);
-  else if constexpr (std::is_same<T, double>::value) return static_cast<double>(v);
-  else return v;
-}
-
 // Row and first chunk of unit u.
 __device__ __forceinline__ int64_t row_of(const Mx4Params& p, int64_t u, int* chunk) {
   if (p.units < (int64_t{1} << 31)) {
@@ -108,8 +93,23 @@ __device__ __forceinline__ int64_t scale_row(const Mx4Params& p, int64_t row64) 
 // lanes neighbouring words, and turns it round in shared memory.
 template <typename T>
 struct Raw {
-  alignas(32) T v[kLaneElems];
+  static constexpr int kWords = kLaneElems * static_cast<int>(sizeof(T)) / 4;
+  uint32_t w[kWords];
 };
+
+// Element i as fp32.
+template <typename T>
+__device__ __forceinline__ float element(const Raw<T>& r, int i) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)
+    return __uint_as_float(i & 1 ? r.w[i / 2] & 0xFFFF0000u : r.w[i / 2] << 16);
+  else if constexpr (std::is_same<T, __half>::value)
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(r.w[i / 2] >> (16 * (i & 1)))));
+  else if constexpr (std::is_same<T, double>::value)
+    return __double2float_rn(__hiloint2double(static_cast<int>(r.w[2 * i + 1]), static_cast<int>(r.w[2 * i])));
+  else
+    return __uint_as_float(r.w[i]);
+}
+
 // 32 bytes at once (32-byte aligned): a lane's whole sector in one access.
 __device__ __forceinline__ void load32(const void* src, uint32_t* d) {
   asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -122,53 +122,69 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t* d) {
                : "memory");
 }
 
+// The word of a row that starts at element k (with sizeof(T) == 2: k and k + 1), zeros past K; word aligned.
+template <typename T>
+__device__ __forceinline__ uint32_t load_word(const T* row, int64_t k, int64_t K) {
+  const uint16_t* h = reinterpret_cast<const uint16_t*>(row + k);
+  return k + 1 < K ? __ldg(reinterpret_cast<const uint32_t*>(h)) : k < K ? *h : 0u;
+}
+
 template <typename T, int ALIGN>
 __device__ __forceinline__ void load_raw(const T* row, int k0, int64_t K, int lane, uint8_t* stage, Raw<T>& r) {
+  constexpr int kWords = Raw<T>::kWords;
   if constexpr (ALIGN >= 16) {
     const int k = k0 + lane * kLaneElems;
     if (k + kLaneElems <= K) {
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(row + k);
       if constexpr (ALIGN == 32) {
 #pragma unroll
-        for (int i = 0; i < kLaneElems * static_cast<int>(sizeof(T)) / 32; ++i)
-          load32(reinterpret_cast<const uint8_t*>(row + k) + 32 * i, reinterpret_cast<uint32_t*>(r.v) + 8 * i);
+        for (int i = 0; i < kWords / 8; ++i) load32(src + 32 * i, r.w + 8 * i);
       } else {
 #pragma unroll
-        for (int i = 0; i < kLaneElems * static_cast<int>(sizeof(T)) / 16; ++i)
-          reinterpret_cast<uint4*>(r.v)[i] = __ldg(reinterpret_cast<const uint4*>(row + k) + i);
+        for (int i = 0; i < kWords / 4; ++i) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i);
+          r.w[4 * i] = v.x;
+          r.w[4 * i + 1] = v.y;
+          r.w[4 * i + 2] = v.z;
+          r.w[4 * i + 3] = v.w;
+        }
       }
+    } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) r.w[i] = load_word(row, k + 2 * i, K);
     } else {
 #pragma unroll
-      for (int i = 0; i < kLaneElems; ++i) r.v[i] = k + i < K ? row[k + i] : T(0.0f);
+      for (int i = 0; i < kWords; ++i)
+        r.w[i] = k + i / (kWords / kLaneElems) < K ? __ldg(reinterpret_cast<const uint32_t*>(row + k) + i) : 0u;
     }
-  } else if constexpr (ALIGN == 4 && sizeof(T) == 2) {
-    const uint32_t* words = reinterpret_cast<const uint32_t*>(row);
-    uint32_t w[kLaneElems / 2];
-#pragma unroll
-    for (int i = 0; i < kLaneElems / 2; ++i) {
-      const int64_t k = k0 + 2 * (32 * i + lane);
-      w[i] = k + 1 < K ? __ldg(words + k / 2) : k < K ? *reinterpret_cast<const uint16_t*>(row + k) : 0u;
-    }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kLaneElems / 2; ++i) reinterpret_cast<uint32_t*>(stage)[32 * i + lane] = w[i];
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) reinterpret_cast<uint4*>(r.v)[i] = reinterpret_cast<const uint4*>(stage)[2 * lane + i];
   } else {
-    T w[kLaneElems];
+    if constexpr (ALIGN == 4 && sizeof(T) == 2) {
+      uint32_t w[kWords];
 #pragma unroll
-    for (int i = 0; i < kLaneElems; ++i) {
-      const int64_t k = k0 + 32 * i + lane;
-      w[i] = k < K ? row[k] : T(0.0f);
+      for (int i = 0; i < kWords; ++i) w[i] = load_word(row, k0 + 2 * (32 * i + lane), K);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) reinterpret_cast<uint32_t*>(stage)[32 * i + lane] = w[i];
+    } else {
+      T w[kLaneElems];
+#pragma unroll
+      for (int i = 0; i < kLaneElems; ++i) {
+        const int64_t k = k0 + 32 * i + lane;
+        w[i] = k < K ? row[k] : T(0.0f);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kLaneElems; ++i) reinterpret_cast<T*>(stage)[32 * i + lane] = w[i];
     }
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < kLaneElems; ++i) reinterpret_cast<T*>(stage)[32 * i + lane] = w[i];
-    __syncwarp();
-    constexpr int words = kLaneElems * static_cast<int>(sizeof(T)) / 16;
-#pragma unroll
-    for (int i = 0; i < words; ++i)
-      reinterpret_cast<uint4*>(r.v)[i] = reinterpret_cast<const uint4*>(stage)[words * lane + i];
+    for (int i = 0; i < kWords / 4; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(stage)[kWords / 4 * lane + i];
+      r.w[4 * i] = v.x;
+      r.w[4 * i + 1] = v.y;
+      r.w[4 * i + 2] = v.z;
+      r.w[4 * i + 3] = v.w;
+    }
   }
 }
 
@@ -179,20 +195,48 @@ template <typename T>
 __device__ __forceinline__ uint32_t top_of(const Raw<T>& r, float prescale) {
   float top;
   if constexpr (sizeof(T) == 2) {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(r.v);
-    uint32_t m = w[0] & 0x7FFF7FFFu;
+    uint32_t m = r.w[0] & 0x7FFF7FFFu;
 #pragma unroll
-    for (int i = 1; i < kLaneElems / 2; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
-    const unsigned short h = static_cast<unsigned short>(max(m & 0xFFFFu, m >> 16));
-    if constexpr (std::is_same<T, __half>::value) top = __half2float(__ushort_as_half(h));
-    else top = __uint_as_float(static_cast<uint32_t>(h) << 16);
+    for (int i = 1; i < kLaneElems / 2; ++i) m = __vmaxu2(m, r.w[i] & 0x7FFF7FFFu);
+    const uint32_t h = max(m & 0xFFFFu, m >> 16);
+    if constexpr (std::is_same<T, __half>::value) top = __half2float(__ushort_as_half(static_cast<unsigned short>(h)));
+    else top = __uint_as_float(h << 16);
   } else {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < kLaneElems; ++i) m = max(m, __float_as_uint(to_f32(r.v[i])) & 0x7FFFFFFFu);
+    for (int i = 0; i < kLaneElems; ++i) m = max(m, __float_as_uint(element(r, i)) & 0x7FFFFFFFu);
     top = __uint_as_float(m);
   }
   return __float_as_uint(top * prescale) & 0x7FFFFFFFu;
+}
+
+// Elements 2 i and 2 i + 1 of a lane's 16, rounded to T.
+template <typename T>
+__device__ __forceinline__ void set_pair(Raw<T>& r, int i, float lo, float hi) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r.w[i]) : "f"(hi), "f"(lo));
+  } else if constexpr (std::is_same<T, __half>::value) {
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r.w[i]) : "f"(hi), "f"(lo));
+  } else if constexpr (std::is_same<T, double>::value) {
+    const double a = lo, b = hi;
+    r.w[4 * i] = static_cast<uint32_t>(__double2loint(a));
+    r.w[4 * i + 1] = static_cast<uint32_t>(__double2hiint(a));
+    r.w[4 * i + 2] = static_cast<uint32_t>(__double2loint(b));
+    r.w[4 * i + 3] = static_cast<uint32_t>(__double2hiint(b));
+  } else {
+    r.w[2 * i] = __float_as_uint(lo);
+    r.w[2 * i + 1] = __float_as_uint(hi);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_element(T* dst, const Raw<T>& r, int i) {
+  if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(r.w[i / 2] >> (16 * (i & 1)));
+  } else {
+#pragma unroll
+    for (int j = 0; j < static_cast<int>(sizeof(T)) / 4; ++j)
+      reinterpret_cast<uint32_t*>(dst)[j] = r.w[i * (static_cast<int>(sizeof(T)) / 4) + j];
+  }
 }
 
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
@@ -237,6 +281,22 @@ __device__ __forceinline__ float e4m3_value(uint32_t b) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xFFFFu)));
 }
 
+// v / s from an approximate reciprocal and one residual step (Markstein 1990):
+// within a little over half an ulp.  What the rounding to few bits after it
+// needs is that a tie, v = t s with t a boundary between codes (t s has at
+// most 7 bits), comes out as t exactly, which the residual makes it, and that
+// no other fp32 v does: its quotient is at least 2^-23 / m of t away, m < 2 the
+// mantissa of t s, more than half an ulp of t by a margin of 2^-7 of it.
+__device__ __forceinline__ float quotient(float v, float s, float inv) {
+  const float q = v * inv;
+  return fmaf(fmaf(-q, s, v), inv, q);
+}
+__device__ __forceinline__ float reciprocal(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
+}
+
 // Quantises one lane's 16 elements at column k and stores codes and scales.
 template <typename T, int FMT>
 __device__ __forceinline__ void quantize16(const Mx4Params& p, const Raw<T>& r, int64_t row, int k, int64_t at, int lane) {
@@ -244,7 +304,7 @@ __device__ __forceinline__ void quantize16(const Mx4Params& p, const Raw<T>& r, 
   if (FMT == OZK_MXFP4) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
   uint64_t v[kLaneElems / 2];
 #pragma unroll
-  for (int i = 0; i < kLaneElems / 2; ++i) v[i] = pack2(to_f32(r.v[2 * i]), to_f32(r.v[2 * i + 1]));
+  for (int i = 0; i < kLaneElems / 2; ++i) v[i] = pack2(element(r, 2 * i), element(r, 2 * i + 1));
   if (p.prescale != 1.0f) {
     const uint64_t ps = pack2(p.prescale, p.prescale);
 #pragma unroll
@@ -258,16 +318,13 @@ __device__ __forceinline__ void quantize16(const Mx4Params& p, const Raw<T>& r, 
 #pragma unroll
     for (int i = 0; i < kLaneElems / 2; ++i) v[i] = mul2(v[i], inv);
   } else {
-    byte = e4m3_of(__fdiv_rn(__uint_as_float(top), 6.0f));
+    byte = e4m3_of(quotient(__uint_as_float(top), 6.0f, 1.0f / 6.0f));
     const float s = e4m3_value(byte);
-    const float f = byte ? __frcp_rn(s) : 0.0f;
+    const float f = byte ? reciprocal(s) : 0.0f;
     const uint64_t inv = pack2(f, f), neg = pack2(-s, -s);
-    // x' / s correctly rounded (Markstein's residual step from the rounded
-    // reciprocal): the ties of the E2M1 rounding, multiples t s with few
-    // bits, come out exactly, and nothing else rounds onto them
 #pragma unroll
     for (int i = 0; i < kLaneElems / 2; ++i) {
-      const uint64_t q = mul2(v[i], inv);
+      const uint64_t q = mul2(v[i], inv);  // quotient(), two at a time
       v[i] = fma2(fma2(q, neg, v[i]), inv, q);
     }
   }
@@ -304,6 +361,7 @@ __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const Mx4Params 
     load_raw<T, ALIGN>(src, c * kWarpElems, p.K, lane, stage, r);
     const int64_t at = scale_row(p, row);
     if (at < 0) continue;
+#pragma unroll 2
     for (;;) {  // the next chunk is on its way while this one is quantised
       Raw<T> next;
       if (c + 1 < c1) load_raw<T, ALIGN>(src, (c + 1) * kWarpElems, p.K, lane, stage, next);
@@ -362,27 +420,26 @@ __global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(const Mx4Param
         const uint32_t two = ((i < 4 ? code.x : code.y) >> (8 * (i & 3))) & 0xFFu;
         asm("{\n\t.reg .b8 b;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(h) : "r"(two));
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        r.v[2 * i] = from_f32<T>(f.x * s);
-        r.v[2 * i + 1] = from_f32<T>(f.y * s);
+        set_pair(r, i, f.x * s, f.y * s);
       }
+      constexpr int kWords = Raw<T>::kWords;
       if (ALIGN == 32 && k + kLaneElems <= p.K) {
 #pragma unroll
-        for (int i = 0; i < kLaneElems * static_cast<int>(sizeof(T)) / 32; ++i)
-          store32(reinterpret_cast<uint8_t*>(dst + k) + 32 * i, reinterpret_cast<const uint32_t*>(r.v) + 8 * i);
+        for (int i = 0; i < kWords / 8; ++i) store32(reinterpret_cast<uint8_t*>(dst + k) + 32 * i, r.w + 8 * i);
       } else if (ALIGN == 16 && k + kLaneElems <= p.K) {
 #pragma unroll
-        for (int i = 0; i < kLaneElems * static_cast<int>(sizeof(T)) / 16; ++i)
-          reinterpret_cast<uint4*>(dst + k)[i] = reinterpret_cast<const uint4*>(r.v)[i];
+        for (int i = 0; i < kWords / 4; ++i)
+          reinterpret_cast<uint4*>(dst + k)[i] = make_uint4(r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]);
       } else if (ALIGN >= 16) {
 #pragma unroll
         for (int i = 0; i < kLaneElems; ++i)
-          if (k + i < p.K) dst[k + i] = r.v[i];
+          if (k + i < p.K) store_element(dst + k + i, r, i);
       } else {  // turned round in shared memory: neighbouring lanes write neighbouring words
-        constexpr int words = kLaneElems * static_cast<int>(sizeof(T)) / 16;
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < words; ++i)
-          reinterpret_cast<uint4*>(stage)[words * lane + i] = reinterpret_cast<const uint4*>(r.v)[i];
+        for (int i = 0; i < kWords / 4; ++i)
+          reinterpret_cast<uint4*>(stage)[kWords / 4 * lane + i] =
+              make_uint4(r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]);
         __syncwarp();
         const int64_t k0 = static_cast<int64_t>(c) * kWarpElems;
         if constexpr (ALIGN == 4 && sizeof(T) == 2) {
