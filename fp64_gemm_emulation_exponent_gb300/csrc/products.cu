@@ -131,6 +131,15 @@ __device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity)
   return ok != 0;
 }
 
+// Arrival on a barrier of the pair that passes on no memory of this thread's
+// (accumulators handed back: their reads are complete).  A release at cluster
+// scope waits until the thread's global stores are performed, the previous
+// block's among them: 1600 cycles between a tile's last MMA and the next one's
+// first.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
@@ -701,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (PAIR) mbar_arrive_cluster(cluster_addr(acce0 + 8 * ab, 0));
+          if (PAIR) mbar_arrive_remote(cluster_addr(acce0 + 8 * ab, 0));
           else mbar_arrive(acce0 + 8 * ab);
         }
         held = false;
