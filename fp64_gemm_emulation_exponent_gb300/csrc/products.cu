@@ -932,14 +932,17 @@ cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
 
 // The form of the tiles, by modelled time: waves of tiles times (stages of a
 // tile x cycles of a stage + a tile's fixed cycles), for a CTA pair's tile of
-// 256 columns by up to 256 rows and for one CTA's of 128 by up to 128.  Rows
-// per group are taken as their mean (the offsets are on the device).  The
-// constants are measured: a stage takes about 330 cycles (4-bit 400) to issue
-// however few its rows; with full tiles a pair's takes the MMAs' 540 (650), a
-// CTA's the 450 (510) that 32 (36) KB take from L2 with every SM loading.
-// Both forms on the same box: 8192^3 NVFP4 pairs 160, single 233 us; 16 groups
-// of ~512 rows, 4096 -> 2048 bf16, 98 and 117; 1000 x 1537 x 2090 MXFP4 11.2
-// and 7.2; 32 rows in 32 groups, 4096 -> 2048 NVFP4, 21.7 and 19.6.
+// 256 columns by up to 256 rows and for one CTA's of 128 by up to 128; a
+// launch of pairs starts 2000 cycles later.  Rows per group are taken as
+// their mean (the offsets are on the device).  The constants are measured: a
+// stage takes about 330 cycles (4-bit 400) to issue however few its rows; with
+// full tiles a pair's takes the 540 (550) of its MMAs and copies, a CTA's the
+// 450 (510) that 32 (36) KB take from L2 with every SM loading.  Over 48
+// sizes of all the operations, up to 8192 rows in 1 to 32 groups, the choice is
+// 0.2% slower than the better of the two, pairs alone 17%, single CTAs alone
+// 3%, and more where it counts: 8192^3 NVFP4 155 and 233 us; 16 groups of ~512 rows, 4096 -> 2048
+// bf16, 96 and 117; but 1000 x 1537 x 2090 MXFP4 11.2 and 7.2, and 32 rows in
+// 32 groups, 4096 -> 2048 NVFP4, 21.7 and 19.6.
 template <ProductOp OP, int FMT>
 cudaError_t choose(const Product& q, int num_sms, cudaStream_t stream) {
   const bool mx = OP == kMx4, sum_rows = OP == kGradWeights;
@@ -947,14 +950,15 @@ cudaError_t choose(const Product& q, int num_sms, cudaStream_t stream) {
   const double groups = sum_rows ? q.groups : std::min(static_cast<double>(q.groups), t);
   const double rows = std::max(sum_rows ? static_cast<double>(q.N) : t / groups, 1.0);
   const double stages = std::ceil((sum_rows ? t / groups : static_cast<double>(q.K)) / (mx ? 256 : 64));
-  auto cost = [&](int bn, int cols, int slots, double per_row, double fixed) {
+  auto cost = [&](int bn, int cols, int slots, double per_row, double fixed, double launch) {
     const double per_group = std::ceil(rows / bn);
     const double waves = std::ceil(groups * per_group * std::ceil(static_cast<double>(q.M) / cols) / slots);
-    return waves * (stages * std::max(mx ? 400.0 : 330.0, per_row * rows / per_group) + fixed);
+    return waves * (stages * std::max(mx ? 400.0 : 330.0, per_row * rows / per_group) + fixed) + launch;
   };
-  const double pair = cost(256, 256, num_sms / 2, mx ? 2.55 : 2.1, 2500);
-  const double single = cost(128, 128, num_sms, mx ? 4.0 : 3.5, 2000);
-  return pair < single ? launch<OP, FMT, 256, true>(q, num_sms, stream) : launch<OP, FMT, 128, false>(q, num_sms, stream);
+  const double pair = cost(256, 256, num_sms / 2, mx ? 2.15 : 2.1, 3000, 2000);
+  const double single = cost(128, 128, num_sms, mx ? 4.0 : 3.5, 2000, 0);
+  return pair < single ? launch<OP, FMT, 256, true>(q, num_sms, stream)
+                       : launch<OP, FMT, 128, false>(q, num_sms, stream);
 }
 
 }  // namespace
