@@ -40,9 +40,9 @@ constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr uint32_t kRowBytes = 128;                       // K bytes of a stage: one swizzle row
 constexpr uint32_t kABytes = kTileRows * kRowBytes;       // 16 KB
 constexpr uint32_t kScaleTile = 512;                      // 128 rows x 4 scale bytes
-constexpr int kSuper = 16;       // tile rows of the M side that run together (L2 reuse)
+constexpr int kSuper = 16;       // tiles of the M side that run together (L2 reuse)
 
-constexpr int kTableInts = 4 * kMaxGroups + 1;  // group table: see Groups
+constexpr int kTableInts = 4 * (kMaxGroups + 1);  // group table: see Group
 constexpr int kSortGroups = 256;                // up to so many groups are put in order
 
 // Formats of an instance.  k16: 16-bit operands; the 4-bit ones differ in the
@@ -94,6 +94,7 @@ struct Config {
 struct ProductParams {
   int T, M, N, K;
   int groups, tiles_m, tiles_n;  // tiles_n: of a group (gradient of w only)
+  FastDiv div_tail;              // tiles_m mod kSuper
   bool sort;                     // groups by falling cost of a tile
   const int32_t* offsets;
   void* out;
@@ -203,14 +204,13 @@ __device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, u
 // ---------------------------------------------------------------------------
 // The schedule
 // ---------------------------------------------------------------------------
-// Group table in shared memory: first row and rows of each group; the groups
-// in the order their tiles run, and the first tile of each place in it.
-struct Groups {
-  int* row0;
-  int* rows;
-  int* order;
-  int* first;  // groups + 1
+// Group table in shared memory, in the order the groups' tiles run: first
+// tile, first row, rows, and number of each group; after the last the number
+// of tiles.
+struct Group {
+  int first, row0, rows, e;
 };
+static_assert(sizeof(Group) == 16, "one shared-memory load");
 
 // Output rows of a tile of a group with `total` of them: equal tiles, not full
 // ones and a rest.  A tile's MMAs and copies take time in proportion to its
@@ -219,8 +219,9 @@ struct Groups {
 template <typename C, ProductOp OP>
 __device__ __forceinline__ int tile_rows(int total) {
   if (C::MX) return C::BN;
-  const int tiles = max((total + C::BN - 1) / C::BN, 1);
-  return ((total + tiles - 1) / tiles + 31) / 32 * 32;
+  const unsigned n = static_cast<unsigned>(total), tiles = (n + C::BN - 1) / C::BN;
+  const unsigned rows = tiles <= 1 ? n : (n + tiles - 1) / tiles;
+  return static_cast<int>((rows + 31) / 32 * 32);
 }
 
 // Fills the table (all threads).  Offsets outside [0, T] or running backwards
@@ -230,50 +231,59 @@ __device__ __forceinline__ int tile_rows(int total) {
 // rows it sums), so that the last wave, which not every CTA gets a tile of, is
 // that of the cheapest tiles.
 template <typename C, ProductOp OP>
-__device__ __forceinline__ void build_groups(const ProductParams& p, const Groups& g) {
+__device__ __forceinline__ void build_groups(const ProductParams& p, Group* g) {
   const int tid = threadIdx.x, lane = tid & 31;
-  for (int e = tid; e < p.groups; e += kThreads) {
+  auto group_at = [&](int e) {
     int lo = p.offsets ? p.offsets[e] : 0, hi = p.offsets ? p.offsets[e + 1] : p.T;
     if (lo < 0 || hi < lo || hi > p.T) {
       atomicOr(&g_status, 2);
       lo = min(max(lo, 0), p.T);
       hi = min(max(hi, lo), p.T);
     }
-    g.row0[e] = lo;
-    g.rows[e] = hi - lo;
-    g.order[e] = e;
+    return Group{0, lo, hi - lo, e};
+  };
+  auto tiles_of = [&](int rows) {
+    return (OP == kGradWeights ? p.tiles_n : static_cast<int>((static_cast<unsigned>(rows) + C::BN - 1) / C::BN)) * p.tiles_m;
+  };
+  if (p.groups == 1) {
+    if (tid == 0) {
+      g[0] = group_at(0);
+      g[1].first = tiles_of(g[0].rows);
+    }
+    return;
   }
+  Group mine = {};
+  for (int e = tid; e < p.groups; e += kThreads) g[e] = mine = group_at(e);
   __syncthreads();
   if (p.sort) {  // at most kSortGroups groups: one thread each
     int place = 0;
+    auto cost = [&](int rows) { return OP == kGradWeights ? rows : tile_rows<C, OP>(rows); };
     if (tid < p.groups) {
-      auto cost = [&](int rows) { return OP == kGradWeights ? rows : tile_rows<C, OP>(rows); };
-      const int mine = cost(g.rows[tid]);
+      const int own = cost(mine.rows);
       for (int e = 0; e < p.groups; ++e) {
-        const int other = cost(g.rows[e]);
-        place += other > mine || (other == mine && e < tid);
+        const int other = cost(g[e].rows);
+        place += other > own || (other == own && e < tid);
       }
-      g.order[place] = tid;
     }
+    __syncthreads();
+    if (tid < p.groups) g[place] = mine;
     __syncthreads();
   }
   if (tid < 32) {
     int carry = 0;
     for (int b = 0; b < p.groups; b += 32) {
       const int at = b + lane;
-      int tiles = 0;
-      if (at < p.groups)
-        tiles = (OP == kGradWeights ? p.tiles_n : (g.rows[g.order[at]] + C::BN - 1) / C::BN) * p.tiles_m;
+      const int tiles = at < p.groups ? tiles_of(g[at].rows) : 0;
       int sum = tiles;
 #pragma unroll
       for (int d = 1; d < 32; d *= 2) {
         const int v = __shfl_up_sync(0xFFFFFFFFu, sum, d);
         if (lane >= d) sum += v;
       }
-      if (at < p.groups) g.first[at] = carry + sum - tiles;
+      if (at < p.groups) g[at].first = carry + sum - tiles;
       carry += __shfl_sync(0xFFFFFFFFu, sum, 31);
     }
-    if (lane == 0) g.first[p.groups] = carry;
+    if (lane == 0) g[p.groups].first = carry;
   }
 }
 
@@ -296,25 +306,38 @@ struct Tile {  // the same in every lane
   int k, blocks;   // terms, and stages they take
 };
 
+// Tile u of the schedule; `at` is its group's place in the table.  Within a
+// group the tiles run in super rows of kSuper tile columns of the output,
+// row by row: what runs together shares a few operands' tiles in L2.
 template <typename C, ProductOp OP>
-__device__ __forceinline__ Tile tile_at(const ProductParams& p, const Groups& g, int u, int& e) {
-  while (u >= uniform(g.first[e + 1])) ++e;  // u only grows
+__device__ __forceinline__ Tile tile_at(const ProductParams& p, const Group* g, int u, int& at) {
+  while (u >= uniform(g[at + 1].first)) ++at;  // u only grows
+  const int4 v = *reinterpret_cast<const int4*>(g + at);
+  const Group group{uniform(v.x), uniform(v.y), uniform(v.z), uniform(v.w)};
   Tile t;
-  t.e = uniform(g.order[e]);
-  t.row0 = uniform(g.row0[t.e]);
-  const int in = u - uniform(g.first[e]);
-  const int rows = uniform(g.rows[t.e]);
-  const int total_n = OP == kGradWeights ? p.N : rows;
-  const int tn = (total_n + C::BN - 1) / C::BN;
-  const int super = in / (kSuper * tn);
-  const int gm = min(kSuper, p.tiles_m - super * kSuper);
-  const int r = in - super * kSuper * tn;
-  t.m0 = (super * kSuper + r % gm) * (kTileRows * C::CTAS);
-  const int step = tile_rows<C, OP>(total_n);
-  t.n0 = r / gm * step;
-  t.n = min(step, total_n - t.n0);
+  t.e = group.e;
+  t.row0 = group.row0;
+  const unsigned total_n = static_cast<unsigned>(OP == kGradWeights ? p.N : group.rows);
+  const unsigned tn = (total_n + C::BN - 1) / C::BN;
+  unsigned r = static_cast<unsigned>(u - group.first), m = 0, n;
+  if (p.tiles_m > kSuper) {  // several super rows
+    const unsigned super = r / kSuper / tn;
+    r -= super * kSuper * tn;
+    m = super * kSuper;
+  }
+  if (p.tiles_m - m >= kSuper) {
+    n = r / kSuper;
+    m += r % kSuper;
+  } else {  // the last, tiles_m mod kSuper wide
+    n = div_fast(r, p.div_tail);
+    m += r - n * (static_cast<unsigned>(p.tiles_m) % kSuper);
+  }
+  t.m0 = static_cast<int>(m) * (kTileRows * C::CTAS);
+  const int step = tile_rows<C, OP>(static_cast<int>(total_n));
+  t.n0 = static_cast<int>(n) * step;
+  t.n = min(step, static_cast<int>(total_n) - t.n0);
   t.half = C::PAIR ? (t.n + 31) / 32 * 16 : (t.n + 15) / 16 * 16;
-  t.k = OP == kGradWeights ? rows : p.K;
+  t.k = OP == kGradWeights ? group.rows : p.K;
   t.blocks = (t.k + C::BLOCK_K - 1) / C::BLOCK_K;
   return t;
 }
@@ -438,11 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(out_stage + kEpiWarps * C::OUT_STAGE);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  Groups g;
-  g.row0 = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 256);
-  g.rows = g.row0 + p.groups;
-  g.order = g.rows + p.groups;
-  g.first = g.order + p.groups;
+  Group* g = reinterpret_cast<Group*>(reinterpret_cast<uint8_t*>(bars) + 256);
 
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_rank() : 0;               // in a pair
@@ -483,8 +502,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_relinquish();
     }
   }
-  // the set-up above touches nothing the kernel before this one writes
-  grid_dependency_sync();
+  // The set-up above touches nothing that the kernel before this one writes,
+  // and without offsets neither does the table; loads and stores do.
+  if (p.offsets) grid_dependency_sync();
   build_groups<C, OP>(p, g);
   tc_fence_before();
   __syncthreads();
@@ -492,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = static_cast<uint32_t>(uniform(static_cast<int>(*reinterpret_cast<volatile uint32_t*>(tmem_slot))));
   const Walk walk{static_cast<int>(blockIdx.x) / C::CTAS, static_cast<int>(gridDim.x) / C::CTAS,
-                  uniform(g.first[p.groups])};
+                  uniform(g[p.groups].first)};
 
   if (warp == 0 || warp == 3) {
     // ------------------------------ TMA producers ------------------------------
@@ -502,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int stage = 0, e = 0, issued = 0;
     const int turn = warp == 3;
     uint32_t phase = 0;
-    bool ok = true;
+    bool ok = true, waited = p.offsets != nullptr;
     for (int wave = 0, u; ok && (u = walk.at(wave)) >= 0; ++wave) {
       const Tile t = tile_at<C, OP>(p, g, u, e);
       const int m0 = t.m0 + static_cast<int>(rank) * kTileRows;
@@ -515,6 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
+        if (!waited) grid_dependency_sync();  // the first tile is laid out by now
+        waited = true;
         const bool clear = has_tail<OP>(t) && kb == t.blocks - 1;
         if (mine && elect_one()) {
           uint32_t bar = full0 + 8 * stage;
@@ -685,6 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 4) {
     // ------------------------------ epilogue ------------------------------
+    if (!p.offsets) grid_dependency_sync();
     const int quad = warp & 3, side = (warp - 4) >> 2;  // TMEM lanes 32 quad..; every other block of 32 columns
     const uint32_t stage = smem_u32(out_stage) + static_cast<uint32_t>(warp - 4) * C::OUT_STAGE;
     int e = 0, ab = 0;
@@ -849,6 +872,7 @@ cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
           (OP != kGradWeights || q.groups == 1 || q.out_group % 8 == 0);
   p.tiles_m = static_cast<int>((q.M + (kTileRows * C::CTAS) - 1) / (kTileRows * C::CTAS));
   p.tiles_n = static_cast<int>((q.N + C::BN - 1) / C::BN);
+  p.div_tail = fast_div(p.tiles_m % kSuper);
   // D fp32; types; MN-major operands; M of the MMA
   p.idesc = static_cast<uint32_t>(kTileRows * C::CTAS >> 4) << 24;
   if (C::MX) p.idesc |= (1u << 7) | (1u << 10) | (FMT == kMx ? 1u << 23 : 0u);
@@ -899,7 +923,7 @@ cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
       return cudaErrorInvalidValue;
   }
   auto kernel = product_kernel<OP, FMT, BN, PAIR>;
-  const size_t table = (4 * static_cast<size_t>(q.groups) + 1) * sizeof(int);
+  const size_t table = (static_cast<size_t>(q.groups) + 1) * sizeof(Group);
   int resident = 0;
   cudaError_t e = setup(reinterpret_cast<const void*>(kernel),
                         C::FIXED + kTableInts * sizeof(int), C::CTAS, &resident);
