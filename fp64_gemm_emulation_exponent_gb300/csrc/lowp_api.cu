@@ -46,7 +46,11 @@ int run(const Product& q, cudaStream_t stream, int sms) {
   const int64_t tiles_m = (q.M + 127) / 128;
   const int64_t tiles_n = q.op == kGradWeights ? ((q.N + 127) / 128) * q.groups : q.T / 128 + q.groups;
   if (tiles_m > 0 && tiles_n > kMaxTiles / tiles_m) return OZK_ERR_UNSUPPORTED;
-  return launch_product(q, sms, stream) == cudaSuccess ? OZK_OK : OZK_ERR_CUDA;
+  try {  // the launcher's tables may allocate; nothing is thrown across the C boundary
+    return launch_product(q, sms, stream) == cudaSuccess ? OZK_OK : OZK_ERR_CUDA;
+  } catch (...) {
+    return OZK_ERR_CUDA;
+  }
 }
 
 // What the three 16-bit products share: T rows of x (K columns) and of y or

@@ -102,6 +102,7 @@ struct ProductParams {
   int64_t ldo, out_group;
   float alpha;
   bool vec;        // 16-byte stores: a 16-bit output whose rows are 16-byte aligned
+  uint64_t timeout_ns;  // limit of a pipeline wait: what a whole tile's stages may take, and 2 s
   uint32_t idesc;  // types, majorness, M; N is filled in per tile
 };
 
@@ -531,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t bytes = kABytes + static_cast<uint32_t>(boxes) * C::BOX_BYTES + C::SFA_BYTES + C::SFB_BYTES;
       for (int kb = 0; kb < t.blocks; ++kb) {
         const bool mine = (issued & 1) == turn;
-        if (mine && !warp_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, kTimeoutNs)) {
+        if (mine && !warp_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, p.timeout_ns)) {
           ok = false;
           break;
         }
@@ -604,15 +605,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (t.blocks == 0) continue;
       // free: this accumulator's previous tile (two ago) is out; or, with
       // shared columns, the tile before this one is out of them
-      if (C::SHARED ? (!first && !warp_wait(acce0 + 8 * (ab ^ 1), ab ? aphase : aphase ^ 1u, abort_flag, kTimeoutNs))
-                    : !warp_wait(acce0 + 8 * ab, aphase ^ 1u, abort_flag, kTimeoutNs))
+      if (C::SHARED ? (!first && !warp_wait(acce0 + 8 * (ab ^ 1), ab ? aphase : aphase ^ 1u, abort_flag, p.timeout_ns))
+                    : !warp_wait(acce0 + 8 * ab, aphase ^ 1u, abort_flag, p.timeout_ns))
         break;
       first = false;
       tc_fence_after();
       const uint32_t d = tmem_base + (ab ? C::ACC1 : 0u);
       const uint32_t idesc = p.idesc | (static_cast<uint32_t>(t.half * C::CTAS >> 3) << 17);
       for (int kb = 0; kb < t.blocks; ++kb) {
-        if (!warp_wait(full0 + 8 * stage, phase, abort_flag, kTimeoutNs)) {
+        if (!warp_wait(full0 + 8 * stage, phase, abort_flag, p.timeout_ns)) {
           ok = false;
           break;
         }
@@ -679,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Tile t = tile_at<C, OP>(p, g, u, e);
       if (t.blocks > 0 && has_tail<OP>(t)) {
         const int stage = static_cast<int>((pos + t.blocks - 1) % C::STAGES);
-        if (!warp_wait(tail0 + 8 * stage, (tails >> stage) & 1u, abort_flag, kTimeoutNs)) break;
+        if (!warp_wait(tail0 + 8 * stage, (tails >> stage) & 1u, abort_flag, p.timeout_ns)) break;
         tails ^= 1u << stage;
         const int r0 = t.k % 64;                 // first row past the group's end; the MMAs stop at the next 16
         const int r1 = (r0 + 15) / 16 * 16;
@@ -695,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         // the leader passes the stage on once the peer's part is cleared too
         if (PAIR && leader) {
-          if (!warp_wait(peer0 + 8 * stage, ((tails >> stage) & 1u) ^ 1u, abort_flag, kTimeoutNs)) break;
+          if (!warp_wait(peer0 + 8 * stage, ((tails >> stage) & 1u) ^ 1u, abort_flag, p.timeout_ns)) break;
           mbar_test_cluster(peer0 + 8 * stage, ((tails >> stage) & 1u) ^ 1u);  // acquire at cluster scope
         }
         if (lane == 0) {
@@ -721,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       else at += (static_cast<int64_t>(t.row0) + t.n0) * p.ldo;
       const bool has = t.blocks > 0;
       if (has) {
-        if (!warp_wait(accf0 + 8 * ab, aphase, abort_flag, kTimeoutNs)) break;
+        if (!warp_wait(accf0 + 8 * ab, aphase, abort_flag, p.timeout_ns)) break;
         tc_fence_after();
       }
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + (ab ? C::ACC1 : 0u);
@@ -870,6 +871,8 @@ cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
   p.alpha = q.alpha;
   p.vec = q.out_type != OZK_F32 && reinterpret_cast<uintptr_t>(q.out) % 16 == 0 && q.ldo % 8 == 0 &&
           (OP != kGradWeights || q.groups == 1 || q.out_group % 8 == 0);
+  const int64_t terms = OP == kGradWeights ? q.T : q.K;
+  p.timeout_ns = kTimeoutNs + 4000ull * static_cast<uint64_t>(terms / C::BLOCK_K);
   p.tiles_m = static_cast<int>((q.M + (kTileRows * C::CTAS) - 1) / (kTileRows * C::CTAS));
   p.tiles_n = static_cast<int>((q.N + C::BN - 1) / C::BN);
   p.div_tail = fast_div(p.tiles_m % kSuper);

@@ -365,7 +365,7 @@ def _result(out, rows, cols, dtype, device, stream):
         raise TypeError(f"out is {out.dtype}, the result {dtype}")
     if out.device != device:
         raise ValueError(f"out is on {out.device}, the operands on {device}")
-    return out, _ld(out), _dtype(out.dtype)
+    return out, _rows(out), _dtype(out.dtype)
 
 
 def _device_index(t):
@@ -389,6 +389,16 @@ def _offsets(offsets, index):
     if offsets.get_device() != index:
         raise ValueError(f"operands on cuda:{index} and {offsets.device}")
     return n - 1
+
+
+def _rows(t):
+    """Leading dimension (elements) of a [rows, columns] tensor with unit column stride and rows that do not overlap."""
+    if t.dim() != 2:
+        raise ValueError("expected a 2-D row-major tensor with unit column stride")
+    (r, c), (sr, sc) = t.shape, t.stride()
+    if sc != 1 and c > 1 or r > 1 and sr < c:
+        raise ValueError("expected a 2-D row-major tensor with unit column stride, its rows apart (not an expanded one)")
+    return sr if r > 1 and sr > c else c or 1
 
 
 def _ld3(t):
@@ -469,8 +479,12 @@ def mx4_quantize(x, fmt: str = "nvfp4", offsets=None, prescale: float = 1.0, str
         groups = x.size(0)
         if groups == 0:
             raise ValueError("no groups")
-        x = x.reshape(groups * x.size(1), x.size(2))
-    ld = _ld(x)
+        if x.is_contiguous():
+            x = x.view(groups * x.size(1), x.size(2))
+        else:  # copied where the call runs
+            with torch.cuda.stream(stream):
+                x = x.reshape(groups * x.size(1), x.size(2))
+    ld = _rows(x)
     rows, K = x.shape
     # codes, then scales, in one allocation
     code_bytes = -(-rows * (-(-K // 64) * 32) // 256) * 256
@@ -567,7 +581,7 @@ def grouped_gemm(x, w, offsets, out_dtype=None, out=None, stream=None):
         raise ValueError(f"x is {tuple(x.shape)}, the weights {tuple(w.shape)}")
     T = x.size(0)
     out, ld, out_kind = _result(out, T, N, out_dtype or (x.dtype if out is None else None), x.device, stream)
-    rc = _lib.ozk_grouped_gemm(T, N, K, groups, offsets.data_ptr(), x.data_ptr(), _ld(x), w.data_ptr(), ldw, stride, kind,
+    rc = _lib.ozk_grouped_gemm(T, N, K, groups, offsets.data_ptr(), x.data_ptr(), _rows(x), w.data_ptr(), ldw, stride, kind,
                                out.data_ptr(), ld, out_kind, _stream_at(index, stream))
     if rc:
         raise OzkError("ozk_grouped_gemm", rc)
@@ -583,7 +597,7 @@ def grouped_gemm_dx(dy, w, offsets, out_dtype=None, out=None, stream=None):
         raise ValueError(f"dy is {tuple(dy.shape)}, the weights {tuple(w.shape)}")
     T = dy.size(0)
     out, ld, out_kind = _result(out, T, K, out_dtype or (dy.dtype if out is None else None), dy.device, stream)
-    rc = _lib.ozk_grouped_gemm_dx(T, N, K, groups, offsets.data_ptr(), dy.data_ptr(), _ld(dy), w.data_ptr(), ldw, stride,
+    rc = _lib.ozk_grouped_gemm_dx(T, N, K, groups, offsets.data_ptr(), dy.data_ptr(), _rows(dy), w.data_ptr(), ldw, stride,
                                   kind, out.data_ptr(), ld, out_kind, _stream_at(index, stream))
     if rc:
         raise OzkError("ozk_grouped_gemm_dx", rc)
@@ -606,7 +620,7 @@ def grouped_gemm_dw(dy, x, offsets, out_dtype=None, out=None, stream=None):
     else:
         _same_device(index, out)
     ld, stride = _ld3(out)
-    rc = _lib.ozk_grouped_gemm_dw(T, N, K, groups, offsets.data_ptr(), dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x), kind,
+    rc = _lib.ozk_grouped_gemm_dw(T, N, K, groups, offsets.data_ptr(), dy.data_ptr(), _rows(dy), x.data_ptr(), _rows(x), kind,
                                   out.data_ptr(), ld, stride, _dtype(out.dtype), _stream_at(index, stream))
     if rc:
         raise OzkError("ozk_grouped_gemm_dw", rc)

@@ -265,6 +265,12 @@ def test_wrapper_refusals():
         ozk.grouped_gemm(x, w, off.long())
     with pytest.raises(ValueError):
         ozk.grouped_gemm(x, w.transpose(1, 2), off)
+    with pytest.raises(ValueError):  # one row for all: nothing there to read at a row's distance
+        ozk.grouped_gemm(x[:1].expand(8, 64), w, off)
+    with pytest.raises(ValueError):  # as a sum's gradient comes
+        ozk.grouped_gemm_dx(torch.ones(1, 1, device="cuda", dtype=torch.bfloat16).expand(8, 32), w, off)
+    with pytest.raises(ValueError):
+        ozk.grouped_gemm(x, w[:1].expand(2, 32, 64), off)
     with pytest.raises(ValueError):
         ozk.grouped_gemm(x, w, off.cpu())
     with pytest.raises(ozk.OzkError):

@@ -141,6 +141,13 @@ def test_quantize_groups(fmt, counts):
 def test_quantize_equal_groups(fmt):
     w = spread(3 * 150, 192, 2, torch.bfloat16).view(3, 150, 192)
     check_quantized(ozk.mx4_quantize(w, fmt), w.view(450, 192), starts=[0, 150, 300, 450])
+    wide = torch.zeros(3, 160, 200, device="cuda", dtype=torch.bfloat16)
+    wide[:, :150, :192] = w
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    q = ozk.mx4_quantize(wide[:, :150, :192], fmt, stream=s)
+    s.synchronize()
+    check_quantized(q, w.view(450, 192), starts=[0, 150, 300, 450])
 
 
 def check_product(c, a, b, alpha, K):
@@ -301,6 +308,8 @@ def test_wrapper_refusals():
         ozk.mx4_quantize(x, "fp4")
     with pytest.raises(ValueError):
         ozk.mx4_quantize(x.t())
+    with pytest.raises(ValueError):
+        ozk.mx4_quantize(x[:1].expand(8, 64))
     with pytest.raises(ValueError):
         ozk.mx4_quantize(x.cpu())
     with pytest.raises(TypeError):
