@@ -30,8 +30,9 @@
 //     weights are read for two tiles of rows only, HBM and MMAs about even
 //   1 x 8192 x 4096 NVFP4: 5.4 us, 2.1 of them a launch with nothing to do; one
 //     SM takes in 64-74 bytes a cycle, and the 64 tiles are on 64 SMs
-// What did not help: prefetching the next tile's operands into L2 (10-20%
-// slower: the copies' requests are what is short), scale tiles multicast in
+// What did not help: prefetching the next tile's operands into L2 by TMA (10-20%
+// slower: the copies' requests are what is short) or the weights' lines by an
+// idle warp 16 stages ahead (no change; 40 ahead 18% slower), scale tiles multicast in
 // the pair, a cluster of two or four CTAs along the terms of a small call (the
 // cluster's launch and barriers cost 1.9 us, the split saves 1.7), weights on
 // the N side in tiles of 64, stores by TMA instead of by the epilogue's warps.
