@@ -365,7 +365,7 @@ def _result(out, rows, cols, dtype, device, stream):
         raise TypeError(f"out is {out.dtype}, the result {dtype}")
     if out.device != device:
         raise ValueError(f"out is on {out.device}, the operands on {device}")
-    return out, _rows(out), _dtype(out.dtype)
+    return out, _rows(out)[2], _dtype(out.dtype)
 
 
 def _device_index(t):
@@ -383,35 +383,38 @@ def _same_device(index, *tensors):
 
 def _offsets(offsets, index):
     """The number of groups that offsets, a device vector, has."""
-    n = offsets.numel()
-    if offsets.dtype != _torch.int32 or offsets.dim() != 1 or n < 2 or not offsets.is_contiguous():
+    shape = offsets.shape
+    if len(shape) != 1 or shape[0] < 2 or offsets.dtype != _torch.int32 or not offsets.is_contiguous():
         raise TypeError("offsets: a contiguous int32 vector of groups + 1 entries is expected")
     if offsets.get_device() != index:
         raise ValueError(f"operands on cuda:{index} and {offsets.device}")
-    return n - 1
+    return shape[0] - 1
 
 
 def _rows(t):
-    """Leading dimension (elements) of a [rows, columns] tensor with unit column stride and rows that do not overlap."""
-    if t.dim() != 2:
+    """(rows, columns, leading dimension) of a matrix with unit column stride and rows that do not overlap."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2:
         raise ValueError("expected a 2-D row-major tensor with unit column stride")
-    (r, c), (sr, sc) = t.shape, t.stride()
+    (r, c), (sr, sc) = shape, stride
     if sc != 1 and c > 1 or r > 1 and sr < c:
         raise ValueError("expected a 2-D row-major tensor with unit column stride, its rows apart (not an expanded one)")
-    return sr if r > 1 and sr > c else c or 1
+    return r, c, sr if r > 1 and sr > c else c or 1
 
 
-def _ld3(t):
-    """(leading dimension, group stride) in elements of a [groups, rows, columns] tensor with unit column stride."""
-    if t.dim() != 3:
+def _groups(t):
+    """(groups, rows, columns, leading dimension, group stride) of a [groups, rows, columns] tensor with unit column
+    stride, rows and groups that do not overlap."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3:
         raise ValueError("expected a [groups, rows, columns] tensor with unit column stride")
-    (g, r, c), (sg, sr, sc) = t.shape, t.stride()
+    (g, r, c), (sg, sr, sc) = shape, stride
     if sc != 1 and c > 1:
         raise ValueError("expected a [groups, rows, columns] tensor with unit column stride")
     ld = sr if r > 1 and sr > c else c or 1
     if r > 1 and sr < c or g > 1 and sg < (r - 1) * ld + c:
         raise ValueError("rows or groups that overlap")
-    return ld, sg if g > 1 else r * ld
+    return g, r, c, ld, sg if g > 1 else r * ld
 
 
 class Mx4:
@@ -473,7 +476,7 @@ def mx4_quantize(x, fmt: str = "nvfp4", offsets=None, prescale: float = 1.0, str
     if offsets is not None:
         groups = _offsets(offsets, index)
         at = offsets.data_ptr()
-    if x.dim() == 3:
+    if len(x.shape) == 3:
         if offsets is not None:
             raise ValueError("offsets are for the rows of a 2-D matrix")
         groups = x.size(0)
@@ -484,12 +487,14 @@ def mx4_quantize(x, fmt: str = "nvfp4", offsets=None, prescale: float = 1.0, str
         else:  # copied where the call runs
             with torch.cuda.stream(stream):
                 x = x.reshape(groups * x.size(1), x.size(2))
-    ld = _rows(x)
-    rows, K = x.shape
+    rows, K, ld = _rows(x)
     # codes, then scales, in one allocation
     code_bytes = -(-rows * (-(-K // 64) * 32) // 256) * 256
     size, device = code_bytes + mx4_scale_bytes(rows, K, fmt, groups), x.device
-    memory = torch.empty(size, dtype=torch.uint8, device=device) if stream is None else _empty(size, torch.uint8, device, stream)
+    if stream is None:
+        memory = torch.empty(size, dtype=torch.uint8, device=device)
+    else:
+        memory = _empty(size, torch.uint8, device, stream)
     codes = memory.data_ptr()
     rc = _lib.ozk_mx4_quantize(rows, K, x.data_ptr(), ld, _dtype(x.dtype), f, prescale, at, groups, codes,
                                codes + code_bytes, _stream_at(index, stream))
@@ -549,39 +554,40 @@ def mx4_grouped_gemm(x: Mx4, w: Mx4, alpha: float = 1.0, out_dtype=None, out=Non
         out_dtype = _torch.bfloat16
     N = w.rows // w.groups
     out, ld, kind = _result(out, x.rows, N, out_dtype, x.device, stream)
-    rc = _lib.ozk_mx4_grouped_gemm(x.rows, N, x.K, x.groups, x.offsets.data_ptr(), x._codes, x._scales, w._codes, w._scales,
-                                   _FORMATS[x.fmt], alpha, out.data_ptr(), ld, kind, _stream_at(x._index, stream))
+    rc = _lib.ozk_mx4_grouped_gemm(x.rows, N, x.K, x.groups, x.offsets.data_ptr(), x._codes, x._scales, w._codes,
+                                   w._scales, _FORMATS[x.fmt], alpha, out.data_ptr(), ld, kind, _stream_at(x._index, stream))
     if rc:
         raise OzkError("ozk_mx4_grouped_gemm", rc)
     return out
 
 
 def _grouped(first, second, offsets, groups):
-    """(ozk_dtype, device index) that the operands of a grouped product share."""
+    """(groups, ozk_dtype, device index) that the operands of a grouped product share."""
     if _torch is None:
         _load_torch()
-    if first.dtype != second.dtype:
-        raise TypeError(f"operands of different types: {first.dtype} and {second.dtype}")
+    kind = first.dtype
+    if kind != second.dtype:
+        raise TypeError(f"operands of different types: {kind} and {second.dtype}")
     index = _device_index(first)
-    _same_device(index, second)
+    if second.get_device() != index:
+        raise ValueError(f"operands on cuda:{index} and {second.device}")
     n = _offsets(offsets, index)
     if groups is not None and n != groups:
         raise ValueError(f"offsets of {n} groups, weights of {groups}")
-    return _dtype(first.dtype), index
+    return n, _dtype(kind), index
 
 
 def grouped_gemm(x, w, offsets, out_dtype=None, out=None, stream=None):
     """y[t] = x[t] @ w[g(t)]^T (ozk_grouped_gemm): x [T, K], w [groups, N, K] of
     one 16-bit type, offsets int32 [groups + 1] on the device; [T, N] of their
     type or float32.  Rows in no group are not written."""
-    ldw, stride = _ld3(w)
-    groups, N, K = w.shape
-    kind, index = _grouped(x, w, offsets, groups)
-    if x.dim() != 2 or x.size(1) != K:
+    groups, N, K, ldw, stride = _groups(w)
+    _, kind, index = _grouped(x, w, offsets, groups)
+    T, k, ldx = _rows(x)
+    if k != K:
         raise ValueError(f"x is {tuple(x.shape)}, the weights {tuple(w.shape)}")
-    T = x.size(0)
     out, ld, out_kind = _result(out, T, N, out_dtype or (x.dtype if out is None else None), x.device, stream)
-    rc = _lib.ozk_grouped_gemm(T, N, K, groups, offsets.data_ptr(), x.data_ptr(), _rows(x), w.data_ptr(), ldw, stride, kind,
+    rc = _lib.ozk_grouped_gemm(T, N, K, groups, offsets.data_ptr(), x.data_ptr(), ldx, w.data_ptr(), ldw, stride, kind,
                                out.data_ptr(), ld, out_kind, _stream_at(index, stream))
     if rc:
         raise OzkError("ozk_grouped_gemm", rc)
@@ -590,14 +596,13 @@ def grouped_gemm(x, w, offsets, out_dtype=None, out=None, stream=None):
 
 def grouped_gemm_dx(dy, w, offsets, out_dtype=None, out=None, stream=None):
     """The gradient of grouped_gemm with respect to x: dx[t] = dy[t] @ w[g(t)], [T, K]."""
-    ldw, stride = _ld3(w)
-    groups, N, K = w.shape
-    kind, index = _grouped(dy, w, offsets, groups)
-    if dy.dim() != 2 or dy.size(1) != N:
+    groups, N, K, ldw, stride = _groups(w)
+    _, kind, index = _grouped(dy, w, offsets, groups)
+    T, n, lddy = _rows(dy)
+    if n != N:
         raise ValueError(f"dy is {tuple(dy.shape)}, the weights {tuple(w.shape)}")
-    T = dy.size(0)
     out, ld, out_kind = _result(out, T, K, out_dtype or (dy.dtype if out is None else None), dy.device, stream)
-    rc = _lib.ozk_grouped_gemm_dx(T, N, K, groups, offsets.data_ptr(), dy.data_ptr(), _rows(dy), w.data_ptr(), ldw, stride,
+    rc = _lib.ozk_grouped_gemm_dx(T, N, K, groups, offsets.data_ptr(), dy.data_ptr(), lddy, w.data_ptr(), ldw, stride,
                                   kind, out.data_ptr(), ld, out_kind, _stream_at(index, stream))
     if rc:
         raise OzkError("ozk_grouped_gemm_dx", rc)
@@ -607,20 +612,21 @@ def grouped_gemm_dx(dy, w, offsets, out_dtype=None, out=None, stream=None):
 def grouped_gemm_dw(dy, x, offsets, out_dtype=None, out=None, stream=None):
     """The gradient with respect to w: dw[g] = the sum of dy[t]^T x[t] over the
     rows of group g, [groups, N, K] (zeros for a group without rows)."""
-    kind, index = _grouped(dy, x, offsets, None)
-    if dy.dim() != 2 or x.dim() != 2 or dy.size(0) != x.size(0):
+    groups, kind, index = _grouped(dy, x, offsets, None)
+    (T, N, lddy), (t, K, ldx) = _rows(dy), _rows(x)
+    if t != T:
         raise ValueError(f"dy is {tuple(dy.shape)}, x {tuple(x.shape)}")
-    groups, (T, N), K = offsets.numel() - 1, dy.shape, x.size(1)
     if out is None:
         out = _empty((groups, N, K), out_dtype or x.dtype, x.device, stream)
-    elif out.shape != (groups, N, K):
-        raise ValueError(f"out has shape {tuple(out.shape)}, the result ({groups}, {N}, {K})")
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise TypeError(f"out is {out.dtype}, the result {out_dtype}")
+        ld, stride = K or 1, N * (K or 1)
     else:
+        if out.shape != (groups, N, K):
+            raise ValueError(f"out has shape {tuple(out.shape)}, the result ({groups}, {N}, {K})")
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError(f"out is {out.dtype}, the result {out_dtype}")
         _same_device(index, out)
-    ld, stride = _ld3(out)
-    rc = _lib.ozk_grouped_gemm_dw(T, N, K, groups, offsets.data_ptr(), dy.data_ptr(), _rows(dy), x.data_ptr(), _rows(x), kind,
+        ld, stride = _groups(out)[3:]
+    rc = _lib.ozk_grouped_gemm_dw(T, N, K, groups, offsets.data_ptr(), dy.data_ptr(), lddy, x.data_ptr(), ldx, kind,
                                   out.data_ptr(), ld, stride, _dtype(out.dtype), _stream_at(index, stream))
     if rc:
         raise OzkError("ozk_grouped_gemm_dw", rc)
