@@ -133,9 +133,9 @@ __device__ __forceinline__ bool elect_one() {
 
 // A value that is the same in every lane, made so for the compiler: loops and
 // addresses built on it then run on the warp's uniform registers, which TMA
-// and MMA instructions take their operands from.  With the loops inside a
-// one-thread branch every operand was moved over for every instruction, and
-// the loader took 380 cycles a stage.
+// and MMA instructions take their operands from.  Inside a one-thread branch
+// every operand is moved over for every instruction (a loaded stage 380 cycles
+// of the loader, 336 so).
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 
 __device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity) {
@@ -242,22 +242,23 @@ __device__ __forceinline__ int tile_rows(int total) {
   return static_cast<int>((rows + 31) / 32 * 32);
 }
 
-// Fills the table (all threads).  Offsets outside [0, T] or running backwards
-// are cut to an empty or shorter group, so every access stays inside the
-// operands, and latched as a fault.  Where tiles run in several waves, the
+// Fills the table (all threads).  Where any offset lies outside [0, T] or runs
+// backwards, that is latched as a fault and the groups are cut to a rising
+// sequence inside [0, T]: every access stays inside the operands, no row
+// belongs to two groups, and the tiles' count stays the one the host allowed
+// for.  Where tiles run in several waves, the
 // groups run by falling cost of a tile (its rows; for the gradient of w, the
 // rows it sums), so that the last wave, which not every CTA gets a tile of, is
 // that of the cheapest tiles.
 template <typename C, ProductOp OP>
 __device__ __forceinline__ void build_groups(const ProductParams& p, Group* g) {
   const int tid = threadIdx.x, lane = tid & 31;
-  auto group_at = [&](int e) {
-    int lo = p.offsets ? p.offsets[e] : 0, hi = p.offsets ? p.offsets[e + 1] : p.T;
-    if (lo < 0 || hi < lo || hi > p.T) {
-      atomicOr(&g_status, 2);
-      lo = min(max(lo, 0), p.T);
-      hi = min(max(hi, lo), p.T);
-    }
+  auto offset = [&](int e) { return p.offsets ? p.offsets[e] : e ? p.T : 0; };
+  bool bad = false;
+  auto group_at = [&](int e, int from) {  // `from`: the end of the group before it, where offsets are bad
+    const int first = offset(e), end = offset(e + 1);
+    const int lo = min(max(first, from), p.T), hi = min(max(end, lo), p.T);
+    bad |= lo != first || hi != end;
     return Group{0, lo, hi - lo, e};
   };
   auto tiles_of = [&](int rows) {
@@ -265,18 +266,30 @@ __device__ __forceinline__ void build_groups(const ProductParams& p, Group* g) {
   };
   if (p.groups == 1) {
     if (tid == 0) {
-      g[0] = group_at(0);
+      g[0] = group_at(0, 0);
       g[1].first = tiles_of(g[0].rows);
+      if (bad) atomicOr(&g_status, 2);
     }
     return;
   }
-  Group mine = {};
-  for (int e = tid; e < p.groups; e += kThreads) g[e] = mine = group_at(e);
-  __syncthreads();
+  for (int e = tid; e < p.groups; e += kThreads) g[e] = group_at(e, 0);
+  if (__syncthreads_or(bad)) {
+    if (tid == 0) {
+      atomicOr(&g_status, 2);
+      int from = 0;
+      for (int e = 0; e < p.groups; ++e) {
+        g[e] = group_at(e, from);
+        from = g[e].row0 + g[e].rows;
+      }
+    }
+    __syncthreads();
+  }
   if (p.sort) {  // at most kSortGroups groups: one thread each
     int place = 0;
+    Group mine = {};
     auto cost = [&](int rows) { return OP == kGradWeights ? rows : tile_rows<C, OP>(rows); };
     if (tid < p.groups) {
+      mine = g[tid];
       const int own = cost(mine.rows);
       for (int e = 0; e < p.groups; ++e) {
         const int other = cost(g[e].rows);

@@ -196,6 +196,18 @@ def test_bad_offsets_are_reported(bad):
     assert np.array_equal(got.cpu().numpy(), want) and ozk.ozk_stream_status() == 0
 
 
+def test_bad_offsets_that_name_rows_many_times():
+    """Every second group all rows again: only the first keeps them, and there are no more tiles than rows allow."""
+    T, N, K, G = 500, 136, 72, 600
+    x, w = whole(T, K, seed=1, dtype=torch.bfloat16), whole(G, N, K, seed=2, dtype=torch.bfloat16)
+    off = device_offsets([0, T] * (G // 2) + [0])
+    y = ozk.grouped_gemm(x, w, off, out_dtype=torch.float32)
+    dw = ozk.grouped_gemm_dw(y.to(torch.bfloat16), x, off, out_dtype=torch.float32)
+    assert ozk.ozk_stream_status() == ozk.OZK_ERR_INVALID_ARG
+    assert torch.equal(y.double(), x.double() @ w[0].double().t())
+    assert bool((dw[1:] == 0).all()) and bool((dw[0] != 0).any())
+
+
 def test_most_groups():
     G, N, K = ozk.OZK_MAX_GROUPS, 32, 64
     counts = [(g * 7) % 5 for g in range(G)]

@@ -245,6 +245,25 @@ def test_grouped_product(fmt, counts, N, K):
     assert ozk.ozk_stream_status() == 0
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_grouped_product_of_some_rows(fmt):
+    """Groups that start after the first row, inside a row block of scales, and end before the last."""
+    starts, T, N, K = [133, 140, 140, 300, 301], 330, 200, 192
+    G, off = 4, torch.tensor(starts, dtype=torch.int32, device="cuda")
+    qx = ozk.mx4_quantize(spread(T, K, 1, torch.bfloat16), fmt, offsets=off)
+    qw = ozk.mx4_quantize(spread(G * N, K, 2, torch.bfloat16).view(G, N, K), fmt)
+    x = torch.zeros(T, K, device="cuda", dtype=torch.float64)
+    ozk.mx4_dequantize(qx, out=x)
+    w = ozk.mx4_dequantize(qw, torch.float64).view(G, N, K)
+    y = torch.full((T, N), 5.0, device="cuda")
+    ozk.mx4_grouped_gemm(qx, qw, out=y)
+    for g in range(G):
+        rows = slice(starts[g], starts[g + 1])
+        check_product(y[rows], x[rows], w[g], 1.0, K)
+    assert bool((y[:133] == 5).all()) and bool((y[301:] == 5).all())
+    assert ozk.ozk_stream_status() == 0
+
+
 def test_results_past_32_bits():
     """An output of more than 2^31 elements, and codes and weights whose last rows lie past 2^31 bytes."""
     M, N, K = 300_000, 7200, 128
