@@ -394,9 +394,18 @@ __device__ __forceinline__ T out_of(float v) {
 
 template <typename T>
 __device__ __forceinline__ void store_block(T* out, int64_t ldo, int rows, bool in_m, const uint32_t (&v)[32], float alpha) {
+  if (!in_m) return;
+  if (rows >= 32) {
 #pragma unroll
-  for (int c = 0; c < 32; ++c)
-    if (c < rows && in_m) out[c * ldo] = out_of<T>(__uint_as_float(v[c]) * alpha);
+    for (int c = 0; c < 32; ++c) {
+      *out = out_of<T>(__uint_as_float(v[c]) * alpha);
+      out += ldo;
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      if (c < rows) out[c * ldo] = out_of<T>(__uint_as_float(v[c]) * alpha);
+  }
 }
 
 // The same block of a 16-bit output with rows that start on 16 bytes.  A lane
