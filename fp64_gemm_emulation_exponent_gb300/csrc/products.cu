@@ -24,7 +24,7 @@
 // measured 1852 TFLOP/s bf16 and 6.68 TB/s):
 //   8 groups of 2048 rows, 4096 x 4096, bf16: 290 us forward, 288 us dx, 281 us
 //     dw, 1.90-1.95 PFLOP/s, bound by the MMAs (516 cycles a stage of 512)
-//   8192^3 NVFP4: 153 us, 7.2 PFLOP/s, 0.97 of four times the bf16 rate; a stage
+//   8192^3 NVFP4: 150 us, 7.3 PFLOP/s, 0.99 of four times the bf16 rate; a stage
 //     of 38 KB an SM takes 525 cycles to arrive, its MMAs 512
 //   8192 rows over 16 groups, 4096 -> 2048, bf16: 96 us, 1.42 PFLOP/s; the
 //     weights are read for two tiles of rows only, HBM and MMAs about even
@@ -35,7 +35,7 @@
 // idle warp 16 stages ahead (no change; 40 ahead 18% slower), scale tiles multicast in
 // the pair, a cluster of two or four CTAs along the terms of a small call (the
 // cluster's launch and barriers cost 1.9 us, the split saves 1.7), weights on
-// the N side in tiles of 64, stores by TMA instead of by the epilogue's warps.
+// the N side in tiles of 64.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -101,8 +101,8 @@ struct Config {
   // full, empty, tail and peer tail per stage (the tails: gradient of w);
   // accumulator full and empty; drain
   static constexpr int BARS = (OP == kGradWeights ? 4 : 2) * STAGES + 5;
-  static constexpr uint32_t OUT_STAGE = 2048;            // one epilogue warp's 32 x 32 block in 16 bits
-  static constexpr uint32_t FIXED = 1024 + STAGES * STAGE + kEpiWarps * OUT_STAGE + 256;
+  static constexpr uint32_t OUT_STAGE = 8192;  // of each side of the epilogue: 32 rows of 128 16-bit columns
+  static constexpr uint32_t FIXED = 1024 + STAGES * STAGE + 2 * OUT_STAGE + 256;
   static_assert(8 * BARS + 8 <= 256, "barriers");
   static_assert(FIXED + 4 * kTableInts <= 232448, "shared memory");
   static_assert(BN % 32 == 0 && B_ROWS % BOX == 0, "copies of whole boxes fill a stage exactly");
@@ -413,9 +413,12 @@ __device__ __forceinline__ void store_block(T* out, int64_t ldo, int rows, bool 
 // that lie a whole row apart in the output; stored from there they take 32
 // two-byte stores.  Read in the 16 x 256-bit form, four lanes share an
 // accumulator row, pairs of output rows pack into a register, and stmatrix
-// writes the 8 x 8 pieces transposed: rows of 32 output columns (64 bytes,
-// 16-byte pieces swizzled by the row), which go out in four 16-byte stores a
-// thread.
+// writes the 8 x 8 pieces transposed.  The four warps that hold the tile's 128
+// output columns of these rows put them together in shared memory (two halves
+// of 64 columns, 128-byte rows, swizzled), and whole blocks leave by TMA
+// stores, full lines that no warp waits for: stored by the warps, in rows of 64
+// bytes, a block took 535 cycles of its 820 (8192^2 x 1024 NVFP4 37.1 -> 35.3
+// us, 8192^3 151.7 -> 149.7; a token's product 0.1 us slower).
 __device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
@@ -441,9 +444,16 @@ __device__ __forceinline__ uint32_t pack16(uint32_t lo, uint32_t hi, float alpha
   else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(h), "f"(l));
   return r;
 }
+// This warp's 32 x 32 values into the block of its four warps (quad: which
+// quarter of the 128 columns).
+constexpr uint32_t kOutHalf = 32 * 128;       // 64 columns of 32 rows
+constexpr uint32_t kOutBlock = 2 * kOutHalf;  // 8 KB
+__device__ __forceinline__ uint32_t out_piece(int n, int chunk) {  // 16-byte piece `chunk` (0..15) of row n
+  return static_cast<uint32_t>((chunk >> 3) * static_cast<int>(kOutHalf) + n * 128 + (((chunk & 7) ^ (n & 7)) * 16));
+}
 template <typename T>
-__device__ __forceinline__ void store_block_vec(T* out, int64_t ldo, int rows, int cols, uint32_t stage, int lane,
-                                                const uint32_t (&lo)[16], const uint32_t (&hi)[16], float alpha) {
+__device__ __forceinline__ void stage_block(uint32_t block, int quad, int lane, const uint32_t (&lo)[16],
+                                            const uint32_t (&hi)[16], float alpha) {
   // lane l gives the address of row l % 8 of piece l / 8: output rows 8 (2 q + l / 16) .. and columns 16 half + 8 (l / 8 % 2) ..
   const int piece = lane >> 3;
 #pragma unroll
@@ -451,44 +461,60 @@ __device__ __forceinline__ void store_block_vec(T* out, int64_t ldo, int rows, i
     const uint32_t(&v)[16] = half ? hi : lo;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const int n = 8 * (2 * q + (piece >> 1)) + (lane & 7);
-      const int chunk = 2 * half + (piece & 1);
-      const uint32_t addr = stage + static_cast<uint32_t>(n * 64 + ((chunk ^ ((n >> 1) & 3)) * 16));
+      const uint32_t addr = block + out_piece(8 * (2 * q + (piece >> 1)) + (lane & 7), 4 * quad + 2 * half + (piece & 1));
       asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
                    "r"(pack16<T>(v[8 * q], v[8 * q + 1], alpha)), "r"(pack16<T>(v[8 * q + 2], v[8 * q + 3], alpha)),
                    "r"(pack16<T>(v[8 * q + 4], v[8 * q + 5], alpha)), "r"(pack16<T>(v[8 * q + 6], v[8 * q + 7], alpha))
                    : "memory");
     }
   }
-  __syncwarp();
-  const int chunk = lane & 3;
+}
+// `rows` rows and `cols` columns of a block by ordinary stores (a group's or
+// the matrix's edge, where a whole box would reach past it): this warp's 8 rows.
+__device__ __forceinline__ void store_edge(uint16_t* out, int64_t ldo, int rows, int cols, uint32_t block, int quad, int lane) {
+  const int chunk = lane & 15;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int n = 8 * i + (lane >> 2);
+    const int n = 8 * quad + 2 * i + (lane >> 4);
+    if (n >= rows || 8 * chunk >= cols) continue;
     uint4 w;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                 : "r"(stage + static_cast<uint32_t>(n * 64 + ((chunk ^ ((n >> 1) & 3)) * 16)))
+                 : "r"(block + out_piece(n, chunk))
                  : "memory");
-    if (n >= rows) continue;
-    T* dst = out + n * ldo + 8 * chunk;
+    uint16_t* dst = out + n * ldo + 8 * chunk;
     if (8 * chunk + 8 <= cols) {
       *reinterpret_cast<uint4*>(dst) = w;
     } else {
-      const T* e = reinterpret_cast<const T*>(&w);
+      const uint32_t e[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (8 * chunk + j < cols) dst[j] = e[j];
+        if (8 * chunk + j < cols) dst[j] = static_cast<uint16_t>(e[j / 2] >> (16 * (j & 1)));
     }
   }
-  __syncwarp();
+}
+
+// Barriers of the four epilogue warps of a side, and their agreement on a
+// wait's outcome (each wait is bounded, so all four get here).
+__device__ __forceinline__ void side_sync(int side) {
+  asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(1 + side) : "memory");
+}
+__device__ __forceinline__ bool side_all(int side, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+      "barrier.cta.red.and.aligned.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(1 + side), "r"(static_cast<uint32_t>(ok))
+      : "memory");
+  return r != 0;
 }
 
 template <ProductOp OP, int FMT, int BN, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmR,
                    const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmSR,
-                   const ProductParams p) {
+                   const __grid_constant__ CUtensorMap tmO, const ProductParams p) {
   using C = Config<OP, FMT, BN, PAIR>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -498,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sSA = sB + C::STAGES * C::B_BYTES;
   const uint32_t sSB = sSA + C::STAGES * C::SFA_BYTES;
   uint8_t* out_stage = smem + C::STAGES * C::STAGE;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(out_stage + kEpiWarps * C::OUT_STAGE);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(out_stage + 2 * C::OUT_STAGE);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   Group* g = reinterpret_cast<Group*>(reinterpret_cast<uint8_t*>(bars) + 256);
@@ -749,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------ epilogue ------------------------------
     if (!p.offsets) grid_dependency_sync();
     const int quad = warp & 3, side = (warp - 4) >> 2;  // TMEM lanes 32 quad..; every other block of 32 columns
-    const uint32_t stage = smem_u32(out_stage) + static_cast<uint32_t>(warp - 4) * C::OUT_STAGE;
+    const uint32_t block = smem_u32(out_stage) + static_cast<uint32_t>(side) * C::OUT_STAGE;
     int e = 0, ab = 0;
     uint32_t aphase = 0;
     for (int wave = 0, u; (u = walk.at(wave)) >= 0; ++wave) {
@@ -761,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       else at += (static_cast<int64_t>(t.row0) + t.n0) * p.ldo;
       const bool has = t.blocks > 0;
       if (has) {
-        if (!warp_wait(accf0 + 8 * ab, aphase, abort_flag, p.timeout_ns)) break;
+        if (!side_all(side, warp_wait(accf0 + 8 * ab, aphase, abort_flag, p.timeout_ns))) break;
         tc_fence_after();
       }
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + (ab ? C::ACC1 : 0u);
@@ -797,11 +823,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (held && (C::SHARED || i == kBlocks - 1)) release();
           if (rows <= 0) continue;
-          const int cols = static_cast<int>(min(static_cast<int64_t>(32), p.M - (m - lane)));
-          if (p.out_type == OZK_F16)
-            store_block_vec(static_cast<__half*>(p.out) + o - lane, p.ldo, rows, cols, stage, lane, lo, hi, p.alpha);
-          else
-            store_block_vec(static_cast<__nv_bfloat16*>(p.out) + o - lane, p.ldo, rows, cols, stage, lane, lo, hi, p.alpha);
+          const int m0 = t.m0 + static_cast<int>(rank) * kTileRows;
+          const bool issuer = quad == 0 && elect_one();
+          if (issuer) bulk_wait_read();  // the block's last stores have read it
+          side_sync(side);
+          if (p.out_type == OZK_F16) stage_block<__half>(block, quad, lane, lo, hi, p.alpha);
+          else stage_block<__nv_bfloat16>(block, quad, lane, lo, hi, p.alpha);
+          fence_proxy_async_smem();
+          side_sync(side);
+          if (rows >= 32) {  // columns past M the map leaves out
+            const int n = OP == kGradWeights ? t.n0 + c : t.row0 + t.n0 + c;
+            if (issuer) {
+              if (m0 < p.M) tma_store_3d(&tmO, block, m0, n, OP == kGradWeights ? t.e : 0);
+              if (m0 + 64 < p.M) tma_store_3d(&tmO, block + kOutHalf, m0 + 64, n, OP == kGradWeights ? t.e : 0);
+            }
+          } else {
+            store_edge(static_cast<uint16_t*>(p.out) + o - (m - m0), p.ldo, rows, p.M - m0, block, quad, lane);
+          }
           continue;
         }
         uint32_t v[32];
@@ -824,6 +862,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         ab ^= 1;
         if (ab == 0) aphase ^= 1u;
       }
+    }
+    // the stores in flight finish before the CTA's shared memory goes
+    if (p.vec && quad == 0) {
+      if (elect_one()) bulk_wait_all();
+      __syncwarp();
     }
   }
 
@@ -922,11 +965,12 @@ cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
     p.idesc |= (1u << 4) | (q.dtype == OZK_BF16 ? (1u << 7) | (1u << 10) : 0u) | (C::A_MN ? 1u << 15 : 0u) |
                (C::B_MN ? 1u << 16 : 0u);
 
-  CUtensorMap tmW, tmR, tmSW, tmSR;
+  CUtensorMap tmW, tmR, tmSW, tmSR, tmO;
   std::memset(&tmW, 0, sizeof tmW);
   std::memset(&tmR, 0, sizeof tmR);
   std::memset(&tmSW, 0, sizeof tmSW);
   std::memset(&tmSR, 0, sizeof tmSR);
+  std::memset(&tmO, 0, sizeof tmO);
   const bool loads = q.T > 0 && q.K != 0;  // otherwise no tile has a term, and nothing is read
   if (loads && !C::MX) {
     const CUtensorMapDataType type = q.dtype == OZK_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
@@ -964,6 +1008,14 @@ cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
         !make_map(&tmSR, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, q.a.scales, dims_sb, strides_s, box_sb, false))
       return cudaErrorInvalidValue;
   }
+  if (p.vec) {
+    const int64_t dims[3] = {q.M, OP == kGradWeights ? q.N : q.T, OP == kGradWeights ? q.groups : 1};
+    const int64_t strides[2] = {2 * q.ldo, OP == kGradWeights && q.groups > 1 ? 2 * q.out_group : 2 * q.ldo * dims[1]};
+    const uint32_t box[3] = {64, 32, 1};
+    if (!make_map(&tmO, q.out_type == OZK_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q.out,
+                  dims, strides, box, true))
+      return cudaErrorInvalidValue;
+  }
   auto kernel = product_kernel<OP, FMT, BN, PAIR>;
   const size_t table = (static_cast<size_t>(q.groups) + 1) * sizeof(Group);
   int resident = 0;
@@ -993,7 +1045,7 @@ cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
     cfg.numAttrs = 2;
   }
   cfg.attrs = attr;
-  return cudaLaunchKernelEx(&cfg, kernel, tmW, tmR, tmSW, tmSR, p);
+  return cudaLaunchKernelEx(&cfg, kernel, tmW, tmR, tmSW, tmSR, tmO, p);
 }
 
 // The form of the tiles, by modelled time: waves of tiles times (stages of a
