@@ -308,6 +308,7 @@ def ozk_crt_lift(M, N, n_moduli, inp, in_kind, ldi, splits, X, stream=None):
 # A small call takes a few microseconds on the GPU, so these wrappers do no
 # more than check and marshal: pointers go as plain integers, the stream comes
 # from the device index, sizes are computed here rather than by another call.
+# Every call runs on the device that holds its operands, whichever is current.
 _FORMATS = {"nvfp4": OZK_NVFP4, "mxfp4": OZK_MXFP4}
 _WORD_COLUMNS = {"nvfp4": 64, "mxfp4": 128}  # columns one word of four scale bytes covers
 _DTYPES = {}
@@ -340,9 +341,24 @@ def _format(fmt):
         raise ValueError(f"unknown 4-bit format {fmt!r} (nvfp4, mxfp4)") from None
 
 
-def _stream_at(index, stream):
-    """Handle of the given stream, or of the current one of a device."""
-    return _torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+def _launch(name, index, stream, *args):
+    """The entry point `name` on the device that holds the operands (its SMs,
+    kernels and status word are the current device's), on the given stream or
+    the device's current one."""
+    if stream is None:
+        handle = _torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device_index == index:
+        handle = stream.cuda_stream
+    else:
+        raise ValueError(f"operands on cuda:{index}, a stream of cuda:{stream.device_index}")
+    entry = getattr(_lib, name)
+    if _torch._C._cuda_getDevice() == index:
+        rc = entry(*args, handle)
+    else:
+        with _torch.cuda.device(index):
+            rc = entry(*args, handle)
+    if rc:
+        raise OzkError(name, rc)
 
 
 def _empty(shape, dtype, device, stream):
@@ -496,10 +512,8 @@ def mx4_quantize(x, fmt: str = "nvfp4", offsets=None, prescale: float = 1.0, str
     else:
         memory = _empty(size, torch.uint8, device, stream)
     codes = memory.data_ptr()
-    rc = _lib.ozk_mx4_quantize(rows, K, x.data_ptr(), ld, _dtype(x.dtype), f, prescale, at, groups, codes,
-                               codes + code_bytes, _stream_at(index, stream))
-    if rc:
-        raise OzkError("ozk_mx4_quantize", rc)
+    _launch("ozk_mx4_quantize", index, stream, rows, K, x.data_ptr(), ld, _dtype(x.dtype), f, prescale, at, groups, codes,
+            codes + code_bytes)
     q = _new_mx4(Mx4)
     q.rows, q.K, q.fmt, q.groups, q.offsets, q.device = rows, K, fmt, groups, offsets, device
     q._memory, q._index, q._codes, q._scales = memory, index, codes, codes + code_bytes
@@ -512,11 +526,8 @@ def mx4_dequantize(q: Mx4, dtype=None, out=None, stream=None):
     if dtype is None and out is None:
         dtype = _torch.float32
     out, ld, kind = _result(out, q.rows, q.K, dtype, q.device, stream)
-    rc = _lib.ozk_mx4_dequantize(q.rows, q.K, q._codes, q._scales, _FORMATS[q.fmt],
-                                 None if q.offsets is None else q.offsets.data_ptr(), q.groups, out.data_ptr(), ld, kind,
-                                 _stream_at(q._index, stream))
-    if rc:
-        raise OzkError("ozk_mx4_dequantize", rc)
+    _launch("ozk_mx4_dequantize", q._index, stream, q.rows, q.K, q._codes, q._scales, _FORMATS[q.fmt],
+            None if q.offsets is None else q.offsets.data_ptr(), q.groups, out.data_ptr(), ld, kind)
     return out
 
 
@@ -536,10 +547,8 @@ def mx4_gemm(a: Mx4, b: Mx4, alpha: float = 1.0, out_dtype=None, out=None, strea
     if out_dtype is None and out is None:
         out_dtype = _torch.bfloat16
     out, ld, kind = _result(out, a.rows, b.rows, out_dtype, a.device, stream)
-    rc = _lib.ozk_mx4_gemm(a.rows, b.rows, a.K, a._codes, a._scales, b._codes, b._scales, _FORMATS[a.fmt], alpha,
-                           out.data_ptr(), ld, kind, _stream_at(a._index, stream))
-    if rc:
-        raise OzkError("ozk_mx4_gemm", rc)
+    _launch("ozk_mx4_gemm", a._index, stream, a.rows, b.rows, a.K, a._codes, a._scales, b._codes, b._scales,
+            _FORMATS[a.fmt], alpha, out.data_ptr(), ld, kind)
     return out
 
 
@@ -554,10 +563,8 @@ def mx4_grouped_gemm(x: Mx4, w: Mx4, alpha: float = 1.0, out_dtype=None, out=Non
         out_dtype = _torch.bfloat16
     N = w.rows // w.groups
     out, ld, kind = _result(out, x.rows, N, out_dtype, x.device, stream)
-    rc = _lib.ozk_mx4_grouped_gemm(x.rows, N, x.K, x.groups, x.offsets.data_ptr(), x._codes, x._scales, w._codes,
-                                   w._scales, _FORMATS[x.fmt], alpha, out.data_ptr(), ld, kind, _stream_at(x._index, stream))
-    if rc:
-        raise OzkError("ozk_mx4_grouped_gemm", rc)
+    _launch("ozk_mx4_grouped_gemm", x._index, stream, x.rows, N, x.K, x.groups, x.offsets.data_ptr(), x._codes, x._scales,
+            w._codes, w._scales, _FORMATS[x.fmt], alpha, out.data_ptr(), ld, kind)
     return out
 
 
@@ -587,10 +594,8 @@ def grouped_gemm(x, w, offsets, out_dtype=None, out=None, stream=None):
     if k != K:
         raise ValueError(f"x is {tuple(x.shape)}, the weights {tuple(w.shape)}")
     out, ld, out_kind = _result(out, T, N, out_dtype or (x.dtype if out is None else None), x.device, stream)
-    rc = _lib.ozk_grouped_gemm(T, N, K, groups, offsets.data_ptr(), x.data_ptr(), ldx, w.data_ptr(), ldw, stride, kind,
-                               out.data_ptr(), ld, out_kind, _stream_at(index, stream))
-    if rc:
-        raise OzkError("ozk_grouped_gemm", rc)
+    _launch("ozk_grouped_gemm", index, stream, T, N, K, groups, offsets.data_ptr(), x.data_ptr(), ldx, w.data_ptr(), ldw,
+            stride, kind, out.data_ptr(), ld, out_kind)
     return out
 
 
@@ -602,10 +607,8 @@ def grouped_gemm_dx(dy, w, offsets, out_dtype=None, out=None, stream=None):
     if n != N:
         raise ValueError(f"dy is {tuple(dy.shape)}, the weights {tuple(w.shape)}")
     out, ld, out_kind = _result(out, T, K, out_dtype or (dy.dtype if out is None else None), dy.device, stream)
-    rc = _lib.ozk_grouped_gemm_dx(T, N, K, groups, offsets.data_ptr(), dy.data_ptr(), lddy, w.data_ptr(), ldw, stride,
-                                  kind, out.data_ptr(), ld, out_kind, _stream_at(index, stream))
-    if rc:
-        raise OzkError("ozk_grouped_gemm_dx", rc)
+    _launch("ozk_grouped_gemm_dx", index, stream, T, N, K, groups, offsets.data_ptr(), dy.data_ptr(), lddy, w.data_ptr(),
+            ldw, stride, kind, out.data_ptr(), ld, out_kind)
     return out
 
 
@@ -626,10 +629,8 @@ def grouped_gemm_dw(dy, x, offsets, out_dtype=None, out=None, stream=None):
             raise TypeError(f"out is {out.dtype}, the result {out_dtype}")
         _same_device(index, out)
         ld, stride = _groups(out)[3:]
-    rc = _lib.ozk_grouped_gemm_dw(T, N, K, groups, offsets.data_ptr(), dy.data_ptr(), lddy, x.data_ptr(), ldx, kind,
-                                  out.data_ptr(), ld, stride, _dtype(out.dtype), _stream_at(index, stream))
-    if rc:
-        raise OzkError("ozk_grouped_gemm_dw", rc)
+    _launch("ozk_grouped_gemm_dw", index, stream, T, N, K, groups, offsets.data_ptr(), dy.data_ptr(), lddy, x.data_ptr(),
+            ldx, kind, out.data_ptr(), ld, stride, _dtype(out.dtype))
     return out
 
 
