@@ -152,6 +152,62 @@ def ozk_workspace_size(M: int, N: int, K: int, n_moduli: int) -> int:
 
 
 # ---------------------------------------------------------------- torch helpers
+_DTYPES = {}
+_torch = None
+
+
+def _load_torch():
+    global _torch
+    import torch
+
+    _DTYPES.update({torch.bfloat16: OZK_BF16, torch.float16: OZK_F16, torch.float32: OZK_F32,
+                    torch.float64: OZK_F64})
+    lib()
+    _torch = torch
+    return torch
+
+
+def _launch(name, index, stream, *args, after=()):
+    """The entry point `name` on the device that holds the operands (its SMs,
+    kernels and status word are the current device's), on the given stream or
+    the device's current one; the handle follows args, `after` the handle."""
+    if stream is None:
+        handle = _torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device_index == index:
+        handle = stream.cuda_stream
+    else:
+        raise ValueError(f"operands on cuda:{index}, a stream of cuda:{stream.device_index}")
+    entry = getattr(_lib, name)
+    if _torch._C._cuda_getDevice() == index:
+        rc = entry(*args, handle, *after)
+    else:
+        with _torch.cuda.device(index):
+            rc = entry(*args, handle, *after)
+    if rc:
+        raise OzkError(name, rc)
+
+
+def _run(name, stream, *args, after=()):
+    """_launch with tensors among args (their addresses are passed) on the
+    device they share; host tensors alone: on the stream's device, or the
+    current one."""
+    torch = _torch or _load_torch()
+    index, values = None, []
+    for a in args:
+        if hasattr(a, "data_ptr"):
+            at = a.get_device()
+            if at >= 0 and index is None:
+                index = at
+            elif at >= 0 and at != index:
+                raise ValueError(f"{name}: operands on cuda:{index} and cuda:{at}")
+            a = a.data_ptr()
+        values.append(a)
+    if index is None:
+        index = torch.cuda.current_device() if stream is None else stream.device_index
+    _launch(name, index, stream, *values, after=after)
+    return OZK_OK
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -174,41 +230,42 @@ def _ld(t):
 # ---------------------------------------------------------------- the GEMM
 def ozk_dgemm(M, N, K, A, lda, B, ldb, C, ldc, n_moduli, stream=None):
     """C-ABI ozk_dgemm on device tensors (A, B, C are torch.float64 CUDA tensors)."""
-    return _call("ozk_dgemm", M, N, K, _ptr(A), lda, _ptr(B), ldb, _ptr(C), ldc, n_moduli, _stream(stream))
+    return _run("ozk_dgemm", stream, M, N, K, A, lda, B, ldb, C, ldc, n_moduli)
 
 
 def ozk_dgemm_ws(M, N, K, A, lda, B, ldb, C, ldc, n_moduli, workspace, workspace_bytes, stream=None):
-    return _call("ozk_dgemm_ws", M, N, K, _ptr(A), lda, _ptr(B), ldb, _ptr(C), ldc, n_moduli,
-                 _ptr(workspace), workspace_bytes, _stream(stream))
+    return _run("ozk_dgemm_ws", stream, M, N, K, A, lda, B, ldb, C, ldc, n_moduli, workspace, workspace_bytes)
 
 
 def ozk_dgemm_ws_timed(M, N, K, A, lda, B, ldb, C, ldc, n_moduli, workspace, workspace_bytes, events,
                        stream=None):
     ev = (ctypes.c_void_p * 5)(*[e.value for e in events]) if events is not None else None
-    return _call("ozk_dgemm_ws_timed", M, N, K, _ptr(A), lda, _ptr(B), ldb, _ptr(C), ldc, n_moduli,
-                 _ptr(workspace), workspace_bytes, _stream(stream), ctypes.cast(ev, _vp) if ev else None)
+    return _run("ozk_dgemm_ws_timed", stream, M, N, K, A, lda, B, ldb, C, ldc, n_moduli, workspace, workspace_bytes,
+                after=(ctypes.cast(ev, _vp) if ev else None,))
 
 
 def ozk_dgemm_norm_ws_timed(M, N, K, A, lda, B, ldb, C, ldc, n_moduli, workspace, workspace_bytes, events,
                             stream=None):
     ev = (ctypes.c_void_p * 5)(*[e.value for e in events]) if events is not None else None
-    return _call("ozk_dgemm_norm_ws_timed", M, N, K, _ptr(A), lda, _ptr(B), ldb, _ptr(C), ldc, n_moduli,
-                 _ptr(workspace), workspace_bytes, _stream(stream), ctypes.cast(ev, _vp) if ev else None)
+    return _run("ozk_dgemm_norm_ws_timed", stream, M, N, K, A, lda, B, ldb, C, ldc, n_moduli, workspace, workspace_bytes,
+                after=(ctypes.cast(ev, _vp) if ev else None,))
 
 
 def ozk_dgemm_host(M, N, K, A, lda, B, ldb, C, ldc, n_moduli, stream=None):
     """Host (CPU, ideally pinned) float64 tensors in and out; synchronous."""
-    return _call("ozk_dgemm_host", M, N, K, _ptr(A), lda, _ptr(B), ldb, _ptr(C), ldc, n_moduli, _stream(stream))
+    return _run("ozk_dgemm_host", stream, M, N, K, A, lda, B, ldb, C, ldc, n_moduli)
 
 
 def ozk_dgemm_host_async(M, N, K, A, lda, B, ldb, C, ldc, n_moduli, stream=None):
     """Host (pinned) float64 tensors; returns once enqueued, C is complete when the stream gets there."""
-    return _call("ozk_dgemm_host_async", M, N, K, _ptr(A), lda, _ptr(B), ldb, _ptr(C), ldc, n_moduli,
-                 _stream(stream))
+    return _run("ozk_dgemm_host_async", stream, M, N, K, A, lda, B, ldb, C, ldc, n_moduli)
 
 
 def ozk_stream_status(stream=None):
-    return lib().ozk_stream_status(_stream(stream))
+    """Status of the given stream and its device, or of the current ones."""
+    torch = _torch or _load_torch()
+    with torch.cuda.device(None if stream is None else stream.device_index):
+        return lib().ozk_stream_status(_stream(stream))
 
 
 def ozk_release_cached():
@@ -219,8 +276,7 @@ def dgemm(A, B, n_moduli: int = 14, out=None, stream=None, target_bits=None, sca
     """C = A @ B for float64 CUDA tensors through ozk_dgemm (or ozk_dgemm_bits
     when target_bits is given: the moduli count then follows from K; or
     ozk_dgemm_norm with scaling="norm": scales from the rows' 2-norms)."""
-    import torch
-
+    torch = _torch or _load_torch()
     M, K = A.shape
     K2, N = B.shape
     if K != K2:
@@ -236,15 +292,13 @@ def dgemm(A, B, n_moduli: int = 14, out=None, stream=None, target_bits=None, sca
     elif target_bits is None:
         ozk_dgemm(M, N, K, A, _ld(A), B, _ld(B), out, _ld(out), n_moduli, stream)
     else:
-        _call("ozk_dgemm_bits", M, N, K, _ptr(A), _ld(A), _ptr(B), _ld(B), _ptr(out), _ld(out), target_bits,
-              _stream(stream))
+        _run("ozk_dgemm_bits", stream, M, N, K, A, _ld(A), B, _ld(B), out, _ld(out), target_bits)
     return out
 
 
 # ---------------------------------------------------------------- stages
 def ozk_scale(M, N, K, A, lda, B, ldb, n_moduli, s, t, scratch, stream=None):
-    return _call("ozk_scale", M, N, K, _ptr(A), lda, _ptr(B), ldb, n_moduli, _ptr(s), _ptr(t), _ptr(scratch),
-                 _stream(stream))
+    return _run("ozk_scale", stream, M, N, K, A, lda, B, ldb, n_moduli, s, t, scratch)
 
 
 def ozk_workspace_layout(M: int, N: int, K: int, n_moduli: int) -> WorkspaceInfo:
@@ -258,50 +312,45 @@ def ozk_gamma(K: int, n_moduli: int) -> int:
 
 
 def ozk_dgemm_norm(M, N, K, A, lda, B, ldb, C, ldc, n_moduli, stream=None):
-    return _call("ozk_dgemm_norm", M, N, K, _ptr(A), lda, _ptr(B), ldb, _ptr(C), ldc, n_moduli, _stream(stream))
+    return _run("ozk_dgemm_norm", stream, M, N, K, A, lda, B, ldb, C, ldc, n_moduli)
 
 
 def ozk_dgemm_norm_ws(M, N, K, A, lda, B, ldb, C, ldc, n_moduli, workspace, workspace_bytes, stream=None):
-    return _call("ozk_dgemm_norm_ws", M, N, K, _ptr(A), lda, _ptr(B), ldb, _ptr(C), ldc, n_moduli, _ptr(workspace),
-                 workspace_bytes, _stream(stream))
+    return _run("ozk_dgemm_norm_ws", stream, M, N, K, A, lda, B, ldb, C, ldc, n_moduli, workspace, workspace_bytes)
 
 
 def ozk_scale_norm(M, N, K, A, lda, B, ldb, n_moduli, s, t, scratch, stream=None):
-    return _call("ozk_scale_norm", M, N, K, _ptr(A), lda, _ptr(B), ldb, n_moduli, _ptr(s), _ptr(t), _ptr(scratch),
-                 _stream(stream))
+    return _run("ozk_scale_norm", stream, M, N, K, A, lda, B, ldb, n_moduli, s, t, scratch)
 
 
 def ozk_scale_noalloc(M, N, K, A, lda, B, ldb, n_moduli, s, t, stream=None):
-    return _call("ozk_scale_noalloc", M, N, K, _ptr(A), lda, _ptr(B), ldb, n_moduli, _ptr(s), _ptr(t),
-                 _stream(stream))
+    return _run("ozk_scale_noalloc", stream, M, N, K, A, lda, B, ldb, n_moduli, s, t)
 
 
 def ozk_quantize_a(M, K, A, lda, s, n_moduli, a_slices, stream=None):
-    return _call("ozk_quantize_a", M, K, _ptr(A), lda, _ptr(s), n_moduli, _ptr(a_slices), _stream(stream))
+    return _run("ozk_quantize_a", stream, M, K, A, lda, s, n_moduli, a_slices)
 
 
 def ozk_quantize_b(K, N, B, ldb, t, n_moduli, b_slices, stream=None):
-    return _call("ozk_quantize_b", K, N, _ptr(B), ldb, _ptr(t), n_moduli, _ptr(b_slices), _stream(stream))
+    return _run("ozk_quantize_b", stream, K, N, B, ldb, t, n_moduli, b_slices)
 
 
 def ozk_residue_gemm(M, N, K, a_slices, b_slices, n_moduli, out_kind, out, ldo, splits, stream=None):
-    return _call("ozk_residue_gemm", M, N, K, _ptr(a_slices), _ptr(b_slices), n_moduli, out_kind, _ptr(out), ldo,
-                 splits, _stream(stream))
+    return _run("ozk_residue_gemm", stream, M, N, K, a_slices, b_slices, n_moduli, out_kind, out, ldo, splits)
 
 
 def ozk_residue_gemm_withheld(M, N, K, a_slices, b_slices, n_moduli, out, ldo, withhold_kb, timeout_us,
                               stream=None):
-    return _call("ozk_residue_gemm_withheld", M, N, K, _ptr(a_slices), _ptr(b_slices), n_moduli, _ptr(out), ldo,
-                 withhold_kb, timeout_us, _stream(stream))
+    return _run("ozk_residue_gemm_withheld", stream, M, N, K, a_slices, b_slices, n_moduli, out, ldo, withhold_kb,
+                timeout_us)
 
 
 def ozk_crt_combine(M, N, n_moduli, inp, in_kind, ldi, splits, s, t, C, ldc, stream=None):
-    return _call("ozk_crt_combine", M, N, n_moduli, _ptr(inp), in_kind, ldi, splits, _ptr(s), _ptr(t), _ptr(C), ldc,
-                 _stream(stream))
+    return _run("ozk_crt_combine", stream, M, N, n_moduli, inp, in_kind, ldi, splits, s, t, C, ldc)
 
 
 def ozk_crt_lift(M, N, n_moduli, inp, in_kind, ldi, splits, X, stream=None):
-    return _call("ozk_crt_lift", M, N, n_moduli, _ptr(inp), in_kind, ldi, splits, _ptr(X), _stream(stream))
+    return _run("ozk_crt_lift", stream, M, N, n_moduli, inp, in_kind, ldi, splits, X)
 
 
 # ---------------------------------------------------------------- 4-bit matrices and grouped products
@@ -311,19 +360,6 @@ def ozk_crt_lift(M, N, n_moduli, inp, in_kind, ldi, splits, X, stream=None):
 # Every call runs on the device that holds its operands, whichever is current.
 _FORMATS = {"nvfp4": OZK_NVFP4, "mxfp4": OZK_MXFP4}
 _WORD_COLUMNS = {"nvfp4": 64, "mxfp4": 128}  # columns one word of four scale bytes covers
-_DTYPES = {}
-_torch = None
-
-
-def _load_torch():
-    global _torch
-    import torch
-
-    _DTYPES.update({torch.bfloat16: OZK_BF16, torch.float16: OZK_F16, torch.float32: OZK_F32,
-                    torch.float64: OZK_F64})
-    lib()
-    _torch = torch
-    return torch
 
 
 def _dtype(t):
@@ -339,26 +375,6 @@ def _format(fmt):
         return _FORMATS[fmt]
     except KeyError:
         raise ValueError(f"unknown 4-bit format {fmt!r} (nvfp4, mxfp4)") from None
-
-
-def _launch(name, index, stream, *args):
-    """The entry point `name` on the device that holds the operands (its SMs,
-    kernels and status word are the current device's), on the given stream or
-    the device's current one."""
-    if stream is None:
-        handle = _torch._C._cuda_getCurrentRawStream(index)
-    elif stream.device_index == index:
-        handle = stream.cuda_stream
-    else:
-        raise ValueError(f"operands on cuda:{index}, a stream of cuda:{stream.device_index}")
-    entry = getattr(_lib, name)
-    if _torch._C._cuda_getDevice() == index:
-        rc = entry(*args, handle)
-    else:
-        with _torch.cuda.device(index):
-            rc = entry(*args, handle)
-    if rc:
-        raise OzkError(name, rc)
 
 
 def _empty(shape, dtype, device, stream):
@@ -647,7 +663,7 @@ class Event:
         return self.handle.value
 
     def record(self, stream=None):
-        _call("ozk_event_record", self.handle, _stream(stream))
+        _run("ozk_event_record", stream, self.handle)
 
     def elapsed_ms(self, end: "Event") -> float:
         ms = ctypes.c_float()

@@ -66,7 +66,7 @@ class FakeTorch:
 
     @contextlib.contextmanager
     def device(self, index):
-        before, self.current = self.current, index
+        before, self.current = self.current, self.current if index is None else index
         try:
             yield
         finally:
@@ -153,3 +153,42 @@ def test_low_precision_calls_refuse_another_devices_stream(machine, name):
     with pytest.raises(ValueError):
         LOWP[name](1, FakeStream(0))
     assert machine.calls == []
+
+
+FP64 = {
+    "ozk_dgemm": lambda i, s: ozk.dgemm(wide(8, 16, i), wide(16, 4, i), 14, stream=s),
+    "ozk_dgemm_norm": lambda i, s: ozk.dgemm(wide(8, 16, i), wide(16, 4, i), 13, scaling="norm", stream=s),
+    "ozk_dgemm_bits": lambda i, s: ozk.dgemm(wide(8, 16, i), wide(16, 4, i), target_bits=40, stream=s),
+    "ozk_dgemm_ws_timed": lambda i, s: ozk.ozk_dgemm_ws_timed(
+        8, 4, 16, wide(8, 16, i), 16, wide(16, 4, i), 4, wide(8, 4, i), 4, 14, wide(1, 1, i), 8, None, stream=s),
+    "ozk_quantize_a": lambda i, s: ozk.ozk_quantize_a(8, 16, wide(8, 16, i), 16, wide(8, 1, i), 14, wide(8, 64, i), stream=s),
+}
+
+
+def wide(rows, cols, index):
+    return tensor(rows, cols, dtype=torch.float64, index=index)
+
+
+@pytest.mark.parametrize("name", FP64)
+@pytest.mark.parametrize("index", [0, 2])
+def test_fp64_calls_run_on_their_operands_device(machine, name, index):
+    FP64[name](index, None)
+    FP64[name](index, FakeStream(index))
+    assert machine.calls == [(name, index, 0x1000 + index), (name, index, 0x5000 + index)]
+    with pytest.raises(ValueError):
+        FP64[name](index, FakeStream(index + 1))
+    with pytest.raises(ValueError):
+        ozk.dgemm(wide(8, 16, index), wide(16, 4, index + 1), 14)
+    assert machine.fake.current == 0 and len(machine.calls) == 2
+
+
+def test_host_operands_run_on_the_streams_device(machine):
+    host = [wide(8, 8, -1) for _ in range(3)]
+    ozk.ozk_dgemm_host(8, 8, 8, host[0], 8, host[1], 8, host[2], 8, 14)
+    ozk.ozk_dgemm_host_async(8, 8, 8, host[0], 8, host[1], 8, host[2], 8, 14, stream=FakeStream(2))
+    assert machine.calls == [("ozk_dgemm_host", 0, 0x1000), ("ozk_dgemm_host_async", 2, 0x5002)]
+
+
+def test_status_is_that_of_the_streams_device(machine):
+    ozk.ozk_stream_status(FakeStream(3))
+    assert machine.calls == [("ozk_stream_status", 3, 0x5003)]
