@@ -423,6 +423,12 @@ def _offsets(offsets, index):
     return shape[0] - 1
 
 
+def _one_row(columns):
+    """Leading dimension of a single row: nothing is addressed by it, whatever
+    the tensor's own stride, and bulk copies want it a multiple of 8."""
+    return -(-columns // 8) * 8 or 8
+
+
 def _rows(t):
     """(rows, columns, leading dimension) of a matrix with unit column stride and rows that do not overlap."""
     shape, stride = t.shape, t.stride()
@@ -431,6 +437,8 @@ def _rows(t):
     (r, c), (sr, sc) = shape, stride
     if sc != 1 and c > 1 or r > 1 and sr < c:
         raise ValueError("expected a 2-D row-major tensor with unit column stride, its rows apart (not an expanded one)")
+    if r == 1:
+        return r, c, _one_row(c)
     return r, c, sr if r > 1 and sr > c else c or 1
 
 
@@ -443,7 +451,7 @@ def _groups(t):
     (g, r, c), (sg, sr, sc) = shape, stride
     if sc != 1 and c > 1:
         raise ValueError("expected a [groups, rows, columns] tensor with unit column stride")
-    ld = sr if r > 1 and sr > c else c or 1
+    ld = _one_row(c) if r == 1 else sr if r > 1 and sr > c else c or 1
     if r > 1 and sr < c or g > 1 and sg < (r - 1) * ld + c:
         raise ValueError("rows or groups that overlap")
     return g, r, c, ld, sg if g > 1 else r * ld
