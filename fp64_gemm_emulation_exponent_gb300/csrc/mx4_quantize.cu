@@ -120,10 +120,13 @@ __device__ __forceinline__ float element(const Raw<T>& r, int i) {
 }
 
 // 32 bytes at once (32-byte aligned): a lane's whole sector in one access.
+// Volatile and coherent, as are the other loads (plain ones, which no memory
+// clobber lets over it): the kernel before this one may still be writing until
+// the wait at the kernel's start is through.
 __device__ __forceinline__ void load32(const void* src, uint32_t* d) {
-  asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]), "=r"(d[4]), "=r"(d[5]), "=r"(d[6]), "=r"(d[7])
-      : "l"(src));
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]), "=r"(d[4]), "=r"(d[5]), "=r"(d[6]), "=r"(d[7])
+               : "l"(src));
 }
 __device__ __forceinline__ void store32(void* dst, const uint32_t* d) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(d[0]), "r"(d[1]), "r"(d[2]),
@@ -135,7 +138,7 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t* d) {
 template <typename T>
 __device__ __forceinline__ uint32_t load_word(const T* row, int64_t k, int64_t K) {
   const uint16_t* h = reinterpret_cast<const uint16_t*>(row + k);
-  return k + 1 < K ? __ldg(reinterpret_cast<const uint32_t*>(h)) : k < K ? *h : 0u;
+  return k + 1 < K ? *reinterpret_cast<const uint32_t*>(h) : k < K ? *h : 0u;
 }
 
 template <typename T, int ALIGN>
@@ -151,7 +154,7 @@ __device__ __forceinline__ void load_raw(const T* row, int k0, int64_t K, int la
       } else {
 #pragma unroll
         for (int i = 0; i < kWords / 4; ++i) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i);
+          const uint4 v = reinterpret_cast<const uint4*>(src)[i];
           r.w[4 * i] = v.x;
           r.w[4 * i + 1] = v.y;
           r.w[4 * i + 2] = v.z;
@@ -164,7 +167,7 @@ __device__ __forceinline__ void load_raw(const T* row, int k0, int64_t K, int la
     } else {
 #pragma unroll
       for (int i = 0; i < kWords; ++i)
-        r.w[i] = k + i / (kWords / kLaneElems) < K ? __ldg(reinterpret_cast<const uint32_t*>(row + k) + i) : 0u;
+        r.w[i] = k + i / (kWords / kLaneElems) < K ? reinterpret_cast<const uint32_t*>(row + k)[i] : 0u;
     }
   } else {
     if constexpr (ALIGN == 4 && sizeof(T) == 2) {
@@ -406,9 +409,9 @@ __global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(const Mx4Param
       run_codes[i] = make_uint2(0, 0);
       run_bytes[i] = 0;
       if (c + i < c1 && k < p.K) {
-        run_codes[i] = __ldg(reinterpret_cast<const uint2*>(codes + k / 2));
+        run_codes[i] = *reinterpret_cast<const uint2*>(codes + k / 2);
         const int b = k / (FMT == OZK_MXFP4 ? 32 : 16);
-        run_bytes[i] = __ldg(p.scales + at + static_cast<int64_t>(b / 4) * 512 + b % 4);
+        run_bytes[i] = p.scales[at + static_cast<int64_t>(b / 4) * 512 + b % 4];
       }
     }
 #pragma unroll
