@@ -29,6 +29,7 @@ cudaError_t launch_mx4_quantize(const Mx4Matrix& m, const void* x, int64_t ldx, 
                                 int num_sms, cudaStream_t stream);
 cudaError_t launch_mx4_dequantize(const Mx4Matrix& m, void* out, int64_t ldo, int dtype, int num_sms,
                                   cudaStream_t stream);
+int take_mx4_status(int* status);  // the stream is idle; bit 1: bad group offsets
 
 // The products.  kForward: out[t, m] = sum_k x[t, k] w[e][m, k]; kGradRows:
 // out[t, m] = sum_k dy[t, k] w[e][k, m]; kGradWeights: out[e][n, m] =

@@ -33,6 +33,7 @@
 #include <cstdint>
 
 #include "lowp.h"
+#include "tc_ptx.cuh"
 
 namespace ozk {
 namespace {
@@ -71,13 +72,36 @@ __device__ __forceinline__ int64_t row_of(const Mx4Params& p, int64_t u, int* ch
   return row;
 }
 
+// Whether any offset lies outside [0, rows] or runs backwards (every thread of
+// the block), which one block reports.
+__device__ __forceinline__ bool bad_offsets(const Mx4Params& p) {
+  bool bad = false;
+  for (int i = threadIdx.x; i <= p.groups; i += kThreads) {
+    const int at = p.offsets[i], before = i ? p.offsets[i - 1] : 0;
+    bad |= at < before || at > p.rows;
+  }
+  bad = __syncthreads_or(bad);
+  if (bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_status, 2);
+  return bad;
+}
+
 // Byte offset of the scale word (4 blocks) kg = 0 of `row`, or -1 for a row
-// outside every group.  Groups that overlap or run backwards cannot take it
-// out of the buffer: o_g <= row gives a row block of at most row / 128 + g.
-__device__ __forceinline__ int64_t scale_row(const Mx4Params& p, int64_t row64) {
+// outside every group.  Bad offsets (`cut`) are taken as the products take
+// them, each group's start at least the end of the one before it: the row is in
+// the first group that ends past it, if none of the starts up to there does.
+__device__ __forceinline__ int64_t scale_row(const Mx4Params& p, int64_t row64, bool cut) {
   const int row = static_cast<int>(row64);  // below 2^30
   int g = 0, o = 0;
-  if (p.offsets != nullptr) {
+  if (cut) {
+    o = max(p.offsets[0], 0);
+    if (o > row) return -1;
+    for (;; ++g) {
+      if (g == p.groups) return -1;
+      const int end = p.offsets[g + 1];
+      if (end > row) break;
+      o = max(o, end);
+    }
+  } else if (p.offsets != nullptr) {
     int lo = 0, hi = p.groups;  // the last group that starts at or before the row
     while (lo + 1 < hi) {
       const int mid = (lo + hi) / 2;
@@ -86,7 +110,7 @@ __device__ __forceinline__ int64_t scale_row(const Mx4Params& p, int64_t row64) 
     }
     g = lo;
     o = p.offsets[lo];
-    if (o < 0 || o > row || row >= p.offsets[lo + 1]) return -1;
+    if (o > row || row >= p.offsets[lo + 1]) return -1;
   } else if (p.groups > 1) {
     const int per = static_cast<int>(p.rows_per_group);
     g = row / per;
@@ -364,14 +388,20 @@ __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const Mx4Params 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint8_t* stage = ALIGN >= 16 ? stages : stages + warp * kWarpElems * sizeof(T);
   const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < p.units; u += warps) {
-    int c;
-    const int64_t row = row_of(p, u, &c);
+  int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp, row = 0;
+  int c = 0;
+  Raw<T> r;
+  auto load_first = [&]() {
+    row = row_of(p, u, &c);
+    load_raw<T, ALIGN>(static_cast<const T*>(p.x) + row * p.ld, c * kWarpElems, p.K, lane, stage, r);
+  };
+  if (u < p.units) load_first();  // on its way while the offsets are checked
+  const bool cut = p.offsets != nullptr && bad_offsets(p);
+  for (bool first = true; u < p.units; u += warps, first = false) {
+    if (!first) load_first();
     const T* src = static_cast<const T*>(p.x) + row * p.ld;
     const int c1 = min(c + p.run, p.chunks);
-    Raw<T> r;
-    load_raw<T, ALIGN>(src, c * kWarpElems, p.K, lane, stage, r);
-    const int64_t at = scale_row(p, row);
+    const int64_t at = scale_row(p, row, cut);
     if (at < 0) continue;
 #pragma unroll 2
     for (;;) {  // the next chunk is on its way while this one is quantised
@@ -393,10 +423,11 @@ __global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(const Mx4Param
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   T* stage = reinterpret_cast<T*>(ALIGN >= 16 ? stages : stages + warp * kWarpElems * sizeof(T));
   const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
+  const bool cut = p.offsets != nullptr && bad_offsets(p);
   for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < p.units; u += warps) {
     int c;
     const int64_t row = row_of(p, u, &c);
-    const int64_t at = scale_row(p, row);
+    const int64_t at = scale_row(p, row, cut);
     if (at < 0) continue;
     const int c1 = min(c + p.run, p.chunks);
     const uint8_t* codes = p.codes + row * (p.kpad / 2);
@@ -559,5 +590,7 @@ cudaError_t launch_mx4_dequantize(const Mx4Matrix& m, void* out, int64_t ldo, in
                             dim3(kThreads), 0, stream, p);
   });
 }
+
+int take_mx4_status(int* status) { return take_status(status); }
 
 }  // namespace ozk

@@ -784,11 +784,10 @@ int ozk_stream_status(ozk_stream_t stream) {
   int status = 0;
   int rc = take_device_status(reinterpret_cast<cudaStream_t>(stream), &status);
   if (rc) return rc;
-  int products = 0;
-  rc = take_product_status(&products);
-  if (rc) return rc;
+  int products = 0, matrices = 0;
+  if ((rc = take_product_status(&products)) || (rc = take_mx4_status(&matrices))) return rc;
   if (status || (products & 1)) return OZK_ERR_TIMEOUT;
-  return products ? OZK_ERR_INVALID_ARG : OZK_OK;
+  return products || matrices ? OZK_ERR_INVALID_ARG : OZK_OK;
 }
 
 int ozk_release_cached(void) {

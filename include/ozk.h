@@ -26,8 +26,8 @@
  *    events are ordered as usual.
  *  - Argument errors are returned synchronously before anything is launched.
  *    Launch failures return OZK_ERR_CUDA.  Faults detected inside a kernel
- *    (a pipeline wait that ran out) are latched on the device and reported by
- *    ozk_stream_status().
+ *    (a pipeline wait that ran out, bad group offsets) are latched on the
+ *    device and reported by ozk_stream_status().
  *  - Sizes M, N or K equal to 0 are valid: nothing is computed, and for K = 0
  *    (with M, N > 0) C is filled with zeros.
  *  - Requires a GB300-class GPU (sm_103a); other devices give OZK_ERR_DEVICE.
@@ -238,8 +238,10 @@ int ozk_dgemm_host_async(int64_t M, int64_t N, int64_t K, const double* A,
                          int64_t lda, const double* B, int64_t ldb, double* C,
                          int64_t ldc, int n_moduli, ozk_stream_t stream);
 
-/* Synchronises the stream, then reports and clears a fault latched by a
- * kernel (OZK_ERR_TIMEOUT), or OZK_ERR_CUDA if the stream reported an error. */
+/* Synchronises the stream, then reports and clears what the device's kernels
+ * have latched: OZK_ERR_TIMEOUT (a pipeline wait that ran out), else
+ * OZK_ERR_INVALID_ARG (group offsets that lie outside the rows or run
+ * backwards).  OZK_ERR_CUDA if the stream reported an error. */
 int ozk_stream_status(ozk_stream_t stream);
 
 /* Releases the cached workspaces and host-copy buffers of the current device. */
@@ -361,8 +363,9 @@ int ozk_crt_lift(int64_t M, int64_t N, int n_moduli, const void* in, int in_kind
  *    router's result needs no copy to the host and a captured graph may be
  *    replayed with other offsets.  Rows before offsets[0] and from
  *    offsets[groups] on belong to no group: no result is written for them.
- *    Offsets outside [0, T] or running backwards are cut to shorter groups
- *    and reported by ozk_stream_status as OZK_ERR_INVALID_ARG.  At most
+ *    Offsets outside [0, T] or running backwards are cut, each to the range
+ *    from the one before it (as cut) to T, by every call that takes them, and
+ *    reported by ozk_stream_status as OZK_ERR_INVALID_ARG.  At most
  *    OZK_MAX_GROUPS groups.
  *  - Sums are formed in fp32 on the tensor cores and rounded once, to the
  *    output's type.  The order of a sum depends on the sizes alone: the same
