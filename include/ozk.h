@@ -413,8 +413,10 @@ size_t ozk_mx4_scale_bytes(int64_t rows, int64_t K, int format, int groups);
 int ozk_mx4_quantize(int64_t rows, int64_t K, const void* X, int64_t ldx, int dtype, int format, float prescale,
                      const int32_t* offsets, int groups, uint8_t* codes, uint8_t* scales, ozk_stream_t stream);
 
-/* The values stored codes and scales stand for, rounded to dtype (exact in
- * fp32 and FP64; in bf16 too; fp16 only within its range). */
+/* The values stored codes and scales stand for, rounded to dtype: exact in
+ * FP64; in fp32 and bf16 too but for MXFP4 scale bytes 253 and 254 (which
+ * quantisation never gives), whose larger values lie past their range; in
+ * fp16 within its range. */
 int ozk_mx4_dequantize(int64_t rows, int64_t K, const uint8_t* codes, const uint8_t* scales, int format,
                        const int32_t* offsets, int groups, void* X, int64_t ldx, int dtype, ozk_stream_t stream);
 

@@ -1,0 +1,50 @@
+"""Every code under every scale byte, dequantised: what a stored pair stands for, rounded once to the output's type."""
+import numpy as np
+import pytest
+import torch
+
+import lowp_reference as ref
+from fp64_gemm_emulation_exponent_gb300 import ozk
+
+pytestmark = pytest.mark.gpu
+
+
+def every_pair(fmt):
+    """(matrix, its values in 64 bits): row r holds the 16 codes under scale byte r."""
+    rows, K = (256, 32) if fmt == "mxfp4" else (128, 16)  # a sign bit in an E4M3 scale byte is never stored
+    code = np.tile(np.arange(16, dtype=np.uint8), K // 16)
+    codes = np.zeros((rows, 32), dtype=np.uint8)
+    codes[:, : K // 2] = code[0::2] | code[1::2] << 4
+    scales = np.zeros(ozk.mx4_scale_bytes(rows, K, fmt), dtype=np.uint8)
+    r = np.arange(rows)
+    scales[r // 128 * 512 + r % 32 * 16 + r // 32 % 4 * 4] = r
+    q = ozk.Mx4(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), rows, K, fmt)
+    c = np.broadcast_to(code, (rows, K))
+    return q, ref.values(c & 7, c >= 8, r[:, None].astype(np.uint8), fmt, K)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_every_pair_in_64_bits(fmt):
+    q, want = every_pair(fmt)
+    got = ozk.mx4_dequantize(q, torch.float64).cpu().numpy()
+    assert np.array_equal(got, want, equal_nan=True)
+    assert np.isfinite(got[-2]).all()  # the largest scale
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_every_pair_rounded(fmt, dtype):
+    """Values beyond a type's range become infinite, as its rounding has it."""
+    q, want = every_pair(fmt)
+    got = ozk.mx4_dequantize(q, dtype).double().cpu().numpy()
+    rounded = torch.from_numpy(want).float().to(dtype).double().numpy()  # 64 to 32 bits is exact or infinite here
+    assert np.array_equal(got, rounded, equal_nan=True)
+
+
+@pytest.mark.parametrize("offset,pad", [(0, 0), (1, 1), (2, 0), (4, 4)])
+def test_every_pair_at_any_alignment(offset, pad):
+    q, want = every_pair("mxfp4")
+    buf = torch.zeros(offset + 256 * (32 + pad), device="cuda", dtype=torch.float64)
+    out = buf[offset:].view(256, 32 + pad)[:, :32]
+    ozk.mx4_dequantize(q, out=out)
+    assert np.array_equal(out.cpu().numpy(), want, equal_nan=True)
