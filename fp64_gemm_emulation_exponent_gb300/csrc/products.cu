@@ -950,7 +950,7 @@ cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
   p.out_type = q.out_type;
   p.ldo = q.ldo;
   p.out_group = q.out_group;
-  p.alpha = q.alpha;
+  p.alpha = q.K ? q.alpha : 1.0f;  // a sum of no terms is zero, whatever alpha
   p.vec = q.out_type != OZK_F32 && reinterpret_cast<uintptr_t>(q.out) % 16 == 0 && q.ldo % 8 == 0 &&
           (OP != kGradWeights || q.groups == 1 || q.out_group % 8 == 0);
   const int64_t terms = OP == kGradWeights ? q.T : q.K;

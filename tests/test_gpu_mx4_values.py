@@ -48,3 +48,16 @@ def test_every_pair_at_any_alignment(offset, pad):
     out = buf[offset:].view(256, 32 + pad)[:, :32]
     ozk.mx4_dequantize(q, out=out)
     assert np.array_equal(out.cpu().numpy(), want, equal_nan=True)
+
+
+@pytest.mark.parametrize("alpha", [float("inf"), float("nan"), -1.0])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_products_of_no_terms_are_zero(alpha, dtype):
+    """An empty sum is zero whatever alpha is: nothing is multiplied."""
+    e, w = ozk.mx4_quantize(torch.empty(5, 0, device="cuda")), ozk.mx4_quantize(torch.empty(3, 7, 0, device="cuda"))
+    out = ozk.mx4_gemm(e, e, alpha=alpha, out_dtype=dtype)
+    assert torch.equal(out, torch.zeros(5, 5, device="cuda", dtype=dtype)) and not bool(out.signbit().any())
+    x = ozk.mx4_quantize(torch.empty(5, 0, device="cuda"), offsets=torch.tensor([0, 2, 2, 5], dtype=torch.int32, device="cuda"))
+    out = torch.full((5, 7), 9.0, device="cuda", dtype=dtype)
+    ozk.mx4_grouped_gemm(x, w, alpha=alpha, out=out)
+    assert torch.equal(out, torch.zeros_like(out))
