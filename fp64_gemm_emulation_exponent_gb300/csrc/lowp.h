@@ -54,6 +54,7 @@ struct Product {
   float alpha;
 };
 cudaError_t launch_product(const Product& q, int num_sms, cudaStream_t stream);
+void withhold_next_product(int pairs, int cta, int kblock, uint32_t timeout_us);  // test hook, see ozk.h
 int take_product_status(int* status);  // the stream is idle; bit 0: a wait ran out, bit 1: bad group offsets
 
 }  // namespace ozk

@@ -282,4 +282,11 @@ int ozk_grouped_gemm_dw(int64_t T, int64_t N, int64_t K, int groups, const int32
   return rc ? rc : run(q, stream, sms);
 }
 
+int ozk_withhold_next_product(int pairs, int cta, int kblock, uint32_t timeout_us) {
+  if (pairs < 0 || pairs > 1 || cta < 0 || cta > pairs || kblock < -1 || timeout_us > 1000000u)
+    return OZK_ERR_INVALID_ARG;
+  withhold_next_product(pairs, cta, kblock, timeout_us);
+  return OZK_OK;
+}
+
 }  // extern "C"

@@ -18,7 +18,9 @@
 // Roles of a CTA (12 warps): warps 0 and 3 issue the TMA loads, warp 1 the
 // MMAs, warp 2 (gradient of w) clears the rows past a group's end in its last
 // block, warps 4..11 the epilogue.  Every mbarrier wait is bounded; a wait
-// that runs out latches the fault, stops the CTA's roles, drains and returns.
+// that runs out latches the fault and stops the roles of the CTA and its peer;
+// once all have stopped, the copies in flight are waited for, each on the
+// barrier that it was issued on, and the kernel returns.
 //
 // Measured on a GB300 (CUDA events around graph replays; rates against the
 // measured 1852 TFLOP/s bf16 and 6.68 TB/s):
@@ -102,8 +104,9 @@ struct Config {
   // accumulator full and empty; drain
   static constexpr int BARS = (OP == kGradWeights ? 4 : 2) * STAGES + 5;
   static constexpr uint32_t OUT_STAGE = 8192;  // of each side of the epilogue: 32 rows of 128 16-bit columns
-  static constexpr uint32_t FIXED = 1024 + STAGES * STAGE + 2 * OUT_STAGE + 256;
-  static_assert(8 * BARS + 8 <= 256, "barriers");
+  static constexpr uint32_t CTRL = 320;  // barriers, TMEM address, abort flag; from 256 on an Issue per stage
+  static constexpr uint32_t FIXED = 1024 + STAGES * STAGE + 2 * OUT_STAGE + CTRL;
+  static_assert(8 * BARS + 8 <= 256 && 256 + 8 * STAGES <= CTRL, "control words");
   static_assert(FIXED + 4 * kTableInts <= 232448, "shared memory");
   static_assert(BN % 32 == 0 && B_ROWS % BOX == 0, "copies of whole boxes fill a stage exactly");
 };
@@ -120,6 +123,7 @@ struct ProductParams {
   float alpha;
   bool vec;        // 16-byte stores: a 16-bit output whose rows are 16-byte aligned
   uint64_t timeout_ns;  // limit of a pipeline wait: what a whole tile's stages may take, and 2 s
+  int withhold_kb, withhold_cta;  // the stage that test runs withhold (of that CTA's first tile), or -1
   uint32_t idesc;  // types, majorness, M; N is filled in per tile
 };
 
@@ -494,6 +498,57 @@ __device__ __forceinline__ void store_edge(uint16_t* out, int64_t ldo, int rows,
   }
 }
 
+// ---------------------------------------------------------------------------
+// The abort path
+// ---------------------------------------------------------------------------
+// The last issue of a stage's copies: its number (from 1; 0: none yet), the
+// bytes of this CTA, and for a group's last block, which arrives on the tail
+// barrier, bit 31 and the parity of that barrier's phase in bit 30.
+struct alignas(8) Issue {
+  uint32_t number, word;
+};
+__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_shared_cluster(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_shared_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// Waits (each wait bounded) until every copy issued into this CTA's stages is
+// in; one thread, once every role of the CTA and its peer has stopped.  A
+// stage's earlier uses are over, or it would not have been issued again.  On a
+// pair the copies of both CTAs arrive on the leader's barrier, armed by the
+// leader for both: where only one of the two issued the stage's last use, the
+// leader stands in for the other.
+template <typename C>
+__device__ __forceinline__ void drain_copies(const Issue* issues, uint32_t full0, uint32_t tail0, bool leader) {
+  for (int s = 0; s < C::STAGES; ++s) {
+    const Issue own = issues[s];
+    const bool tail = own.word >> 31;
+    if (tail) mbar_wait_drain(tail0 + 8 * s, (own.word >> 30) & 1u);
+    bool full = own.number != 0 && !tail;
+    uint32_t number = own.number;
+    if (C::PAIR) {
+      if (!leader) continue;
+      const uint32_t remote = cluster_addr(smem_u32(issues + s), 1);
+      const Issue peer{ld_shared_cluster(remote), ld_shared_cluster(remote + 4)};
+      if (peer.number > own.number) {
+        full = !(peer.word >> 31);
+        number = peer.number;
+        if (full) mbar_expect_tx(full0 + 8 * s, peer.word & 0xFFFFFu);
+      } else if (peer.number < own.number && full) {
+        mbar_complete_tx(full0 + 8 * s, own.word & 0xFFFFFu);
+      }
+    }
+    if (full) mbar_wait_drain(full0 + 8 * s, ((number - 1) / C::STAGES) & 1u);
+  }
+}
+
 // Barriers of the four epilogue warps of a side, and their agreement on a
 // wait's outcome (each wait is bounded, so all four get here).
 __device__ __forceinline__ void side_sync(int side) {
@@ -527,7 +582,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(out_stage + 2 * C::OUT_STAGE);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  Group* g = reinterpret_cast<Group*>(reinterpret_cast<uint8_t*>(bars) + 256);
+  Issue* issues = reinterpret_cast<Issue*>(reinterpret_cast<uint8_t*>(bars) + 256);
+  Group* g = reinterpret_cast<Group*>(reinterpret_cast<uint8_t*>(bars) + C::CTRL);
 
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_rank() : 0;               // in a pair
@@ -544,6 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
+      issues[s] = {0, 0};
       if (OP == kGradWeights) {
         mbar_init(tail0 + 8 * s, 1);
         mbar_init(peer0 + 8 * s, 1);
@@ -587,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // small tile takes to arrive or to be used.
     int stage = 0, e = 0, issued = 0;
     const int turn = warp == 3;
-    uint32_t phase = 0;
+    uint32_t phase = 0, tails = 0;
     bool ok = true, waited = p.offsets != nullptr;
     for (int wave = 0, u; ok && (u = walk.at(wave)) >= 0; ++wave) {
       const Tile t = tile_at<C, OP>(p, g, u, e);
@@ -604,7 +661,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!waited) grid_dependency_sync();  // the first tile is laid out by now
         waited = true;
         const bool clear = has_tail<OP>(t) && kb == t.blocks - 1;
-        if (mine && elect_one()) {
+        const bool withheld = kb == p.withhold_kb && wave == 0 && static_cast<int>(blockIdx.x) == p.withhold_cta;
+        if (mine && !withheld && elect_one()) {
           uint32_t bar = full0 + 8 * stage;
           if (clear) {  // warp 2 passes the stage on once it has cleared the rows
             bar = tail0 + 8 * stage;
@@ -645,7 +703,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             load3(sSA + stage * C::SFA_BYTES, &tmSW, 0, kb * C::KG, wrow + t.e + m0 / 128);
             load3(sSB + stage * C::SFB_BYTES, &tmSR, 0, kb * C::KG, t.row0 / 128 + t.e + t.n0 / 128);
           }
+          issues[stage] = {static_cast<uint32_t>(issued) + 1u,
+                           bytes | (clear ? 0x80000000u | ((tails >> stage) & 1u) << 30 : 0u)};
         }
+        if (clear) tails ^= 1u << stage;
         ++issued;
         if (++stage == C::STAGES) {
           stage = 0;
@@ -653,9 +714,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (!ok && leader && lane == 0)  // let copies still in flight land before the CTA exits
-      for (int i = max(issued - C::STAGES, 0); i < issued; ++i)
-        if ((i & 1) == turn) mbar_wait_drain(full0 + 8 * (i % C::STAGES), static_cast<uint32_t>(i / C::STAGES) & 1u);
     __syncwarp();
   } else if (warp == 1 && leader) {
     // ------------------------------ MMA issuer ------------------------------
@@ -872,7 +930,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (C::CTAS > 1) cluster_sync();
+  if (C::CTAS > 1) {
+    if (threadIdx.x == 0 && *abort_flag)  // the peer stops too, its own limit aside
+      st_shared_cluster(cluster_addr(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u), 1u);
+    __syncwarp();
+    cluster_sync();
+  }
+  if (*abort_flag) {  // of either CTA of a pair; nothing is issued any more
+    if (threadIdx.x == 0) drain_copies<C>(issues, full0, tail0, leader);
+    __syncthreads();
+    if (C::CTAS > 1) cluster_sync();
+  }
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
@@ -936,6 +1004,13 @@ cudaError_t setup(const void* kernel, size_t smem, int cluster, int* resident) {
   return it->second.err;
 }
 
+// What ozk_withhold_next_product asked of this host thread's next product.
+struct Withhold {
+  int pairs, cta, kblock;
+  uint32_t timeout_us;  // 0: nothing asked
+};
+thread_local Withhold g_withhold = {};
+
 template <ProductOp OP, int FMT, int BN, bool PAIR>
 cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
   using C = Config<OP, FMT, BN, PAIR>;
@@ -955,6 +1030,13 @@ cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
           (OP != kGradWeights || q.groups == 1 || q.out_group % 8 == 0);
   const int64_t terms = OP == kGradWeights ? q.T : q.K;
   p.timeout_ns = kTimeoutNs + 4000ull * static_cast<uint64_t>(terms / C::BLOCK_K);
+  p.withhold_kb = -1;
+  if (g_withhold.timeout_us != 0) {
+    p.timeout_ns = 1000ull * g_withhold.timeout_us;
+    p.withhold_kb = g_withhold.kblock;
+    p.withhold_cta = g_withhold.cta;
+    g_withhold.timeout_us = 0;
+  }
   p.tiles_m = static_cast<int>((q.M + (kTileRows * C::CTAS) - 1) / (kTileRows * C::CTAS));
   p.tiles_n = static_cast<int>((q.N + C::BN - 1) / C::BN);
   p.div_tail = fast_div(p.tiles_m % kSuper);
@@ -1075,8 +1157,9 @@ cudaError_t choose(const Product& q, int num_sms, cudaStream_t stream) {
   };
   const double pair = cost(256, 256, num_sms / 2, mx ? 2.15 : 2.1, 3000, 2000);
   const double single = cost(128, 128, num_sms, mx ? 4.0 : 3.5, 2000, 0);
-  return pair < single ? launch<OP, FMT, 256, true>(q, num_sms, stream)
-                       : launch<OP, FMT, 128, false>(q, num_sms, stream);
+  const bool pairs = g_withhold.timeout_us ? g_withhold.pairs != 0 : pair < single;
+  return pairs ? launch<OP, FMT, 256, true>(q, num_sms, stream)
+               : launch<OP, FMT, 128, false>(q, num_sms, stream);
 }
 
 }  // namespace
@@ -1092,5 +1175,9 @@ cudaError_t launch_product(const Product& q, int num_sms, cudaStream_t stream) {
 }
 
 int take_product_status(int* status) { return take_status(status); }
+
+void withhold_next_product(int pairs, int cta, int kblock, uint32_t timeout_us) {
+  g_withhold = {pairs, cta, kblock, timeout_us};
+}
 
 }  // namespace ozk

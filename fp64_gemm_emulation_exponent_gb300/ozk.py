@@ -74,6 +74,7 @@ SIGNATURES = {
                                    _vp]),
     "ozk_grouped_gemm_dw": (_i32, [_i64, _i64, _i64, _i32, _vp, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _i64, _i32,
                                    _vp]),
+    "ozk_withhold_next_product": (_i32, [_i32, _i32, _i32, ctypes.c_uint32]),
     "ozk_event_create": (_i32, [_vp]),
     "ozk_event_destroy": (_i32, [_vp]),
     "ozk_event_record": (_i32, [_vp, _vp]),
@@ -343,6 +344,10 @@ def ozk_residue_gemm_withheld(M, N, K, a_slices, b_slices, n_moduli, out, ldo, w
                               stream=None):
     return _run("ozk_residue_gemm_withheld", stream, M, N, K, a_slices, b_slices, n_moduli, out, ldo, withhold_kb,
                 timeout_us)
+
+
+def ozk_withhold_next_product(pairs, cta, kblock, timeout_us):
+    return _call("ozk_withhold_next_product", pairs, cta, kblock, timeout_us)
 
 
 def ozk_crt_combine(M, N, n_moduli, inp, in_kind, ldi, splits, s, t, C, ldc, stream=None):

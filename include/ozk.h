@@ -458,7 +458,7 @@ int ozk_grouped_gemm_dw(int64_t T, int64_t N, int64_t K, int groups, const int32
                         int out_dtype, ozk_stream_t stream);
 
 /* ------------------------------------------------------------------ */
-/* Test hook of the failure path.                                      */
+/* Test hooks of the failure path.                                     */
 /* ------------------------------------------------------------------ */
 
 /* ozk_residue_gemm (out_kind 0, one split) on the single-CTA kernel with
@@ -479,6 +479,17 @@ int ozk_grouped_gemm_dw(int64_t T, int64_t N, int64_t K, int groups, const int32
 int ozk_residue_gemm_withheld(int64_t M, int64_t N, int64_t K, const uint16_t* a_slices,
                               const uint16_t* b_slices, int n_moduli, uint8_t* out, int64_t ldo,
                               int withhold_kb, uint32_t timeout_us, ozk_stream_t stream);
+
+/* The next product (ozk_mx4_gemm, ozk_mx4_grouped_gemm, ozk_grouped_gemm and
+ * its gradients) that this host thread launches runs on CTA pairs (pairs 1) or
+ * single CTAs (0), with every pipeline wait limited to timeout_us microseconds
+ * (up to 10^6; 0 takes the request back) and the copies of k-block `kblock`
+ * (64 terms, 256 for 4-bit operands) of the first tile of CTA `cta` (0; on
+ * pairs 0 or 1: one CTA's half of the copies) never issued; -1 or a block that
+ * the tile does not have: none withheld.  What follows is as for
+ * ozk_residue_gemm_withheld; the results of the tiles of that CTA (pair) are
+ * not written.  OZK_ERR_INVALID_ARG for values out of range. */
+int ozk_withhold_next_product(int pairs, int cta, int kblock, uint32_t timeout_us);
 
 /* ------------------------------------------------------------------ */
 /* Timing helpers (thin wrappers of the CUDA runtime).                 */
