@@ -154,44 +154,36 @@ def ozk_workspace_size(M: int, N: int, K: int, n_moduli: int) -> int:
 
 # ---------------------------------------------------------------- torch helpers
 _DTYPES = {}
-_torch = None
+_torch = _current_device = _current_stream = None
 
 
 def _load_torch():
-    global _torch
+    global _torch, _current_device, _current_stream
     import torch
 
     _DTYPES.update({torch.bfloat16: OZK_BF16, torch.float16: OZK_F16, torch.float32: OZK_F32,
                     torch.float64: OZK_F64})
     lib()
+    _current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     _torch = torch
     return torch
 
 
-def _launch(name, index, stream, *args, after=()):
-    """The entry point `name` on the device that holds the operands (its SMs,
-    kernels and status word are the current device's), on the given stream or
-    the device's current one; the handle follows args, `after` the handle."""
+def _stream_at(index, stream):
+    """Handle of the given stream, or of the current one, of a device."""
     if stream is None:
-        handle = _torch._C._cuda_getCurrentRawStream(index)
-    elif stream.device_index == index:
-        handle = stream.cuda_stream
-    else:
+        return _current_stream(index)
+    if stream.device_index != index:
         raise ValueError(f"operands on cuda:{index}, a stream of cuda:{stream.device_index}")
-    entry = getattr(_lib, name)
-    if _torch._C._cuda_getDevice() == index:
-        rc = entry(*args, handle, *after)
-    else:
-        with _torch.cuda.device(index):
-            rc = entry(*args, handle, *after)
-    if rc:
-        raise OzkError(name, rc)
+    return stream.cuda_stream
 
 
 def _run(name, stream, *args, after=()):
-    """_launch with tensors among args (their addresses are passed) on the
-    device they share; host tensors alone: on the stream's device, or the
-    current one."""
+    """The entry point `name` on the device that the tensors among args share
+    (its SMs, kernels and status word are the current device's; their addresses
+    are passed) and on the given stream or that device's current one; host
+    tensors alone: on the stream's device, or the current one.  The stream's
+    handle follows args, `after` the handle."""
     torch = _torch or _load_torch()
     index, values = None, []
     for a in args:
@@ -205,8 +197,11 @@ def _run(name, stream, *args, after=()):
         values.append(a)
     if index is None:
         index = torch.cuda.current_device() if stream is None else stream.device_index
-    _launch(name, index, stream, *values, after=after)
-    return OZK_OK
+    handle = _stream_at(index, stream)
+    if _current_device() == index:
+        return _call(name, *values, handle, *after)
+    with torch.cuda.device(index):
+        return _call(name, *values, handle, *after)
 
 
 def _ptr(t):
@@ -521,6 +516,9 @@ def mx4_quantize(x, fmt: str = "nvfp4", offsets=None, prescale: float = 1.0, str
     if offsets is not None:
         groups = _offsets(offsets, index)
         at = offsets.data_ptr()
+    if index != _current_device():
+        with _torch.cuda.device(index):
+            return mx4_quantize(x, fmt, offsets, prescale, stream)
     if len(x.shape) == 3:
         if offsets is not None:
             raise ValueError("offsets are for the rows of a 2-D matrix")
@@ -541,8 +539,10 @@ def mx4_quantize(x, fmt: str = "nvfp4", offsets=None, prescale: float = 1.0, str
     else:
         memory = _empty(size, torch.uint8, device, stream)
     codes = memory.data_ptr()
-    _launch("ozk_mx4_quantize", index, stream, rows, K, x.data_ptr(), ld, _dtype(x.dtype), f, prescale, at, groups, codes,
-            codes + code_bytes)
+    rc = _lib.ozk_mx4_quantize(rows, K, x.data_ptr(), ld, _dtype(x.dtype), f, prescale, at, groups, codes,
+                               codes + code_bytes, _stream_at(index, stream))
+    if rc:
+        raise OzkError("ozk_mx4_quantize", rc)
     q = _new_mx4(Mx4)
     q.rows, q.K, q.fmt, q.groups, q.offsets, q.device = rows, K, fmt, groups, offsets, device
     q._memory, q._index, q._codes, q._scales = memory, index, codes, codes + code_bytes
@@ -552,11 +552,17 @@ def mx4_quantize(x, fmt: str = "nvfp4", offsets=None, prescale: float = 1.0, str
 def mx4_dequantize(q: Mx4, dtype=None, out=None, stream=None):
     """The values q stands for, [rows, K] of dtype (default float32).  Rows in
     no group are not written."""
+    if q._index != _current_device():
+        with _torch.cuda.device(q._index):
+            return mx4_dequantize(q, dtype, out, stream)
     if dtype is None and out is None:
         dtype = _torch.float32
     out, ld, kind = _result(out, q.rows, q.K, dtype, q.device, stream)
-    _launch("ozk_mx4_dequantize", q._index, stream, q.rows, q.K, q._codes, q._scales, _FORMATS[q.fmt],
-            None if q.offsets is None else q.offsets.data_ptr(), q.groups, out.data_ptr(), ld, kind)
+    rc = _lib.ozk_mx4_dequantize(q.rows, q.K, q._codes, q._scales, _FORMATS[q.fmt],
+                                 None if q.offsets is None else q.offsets.data_ptr(), q.groups, out.data_ptr(), ld,
+                                 kind, _stream_at(q._index, stream))
+    if rc:
+        raise OzkError("ozk_mx4_dequantize", rc)
     return out
 
 
@@ -571,13 +577,18 @@ def mx4_gemm(a: Mx4, b: Mx4, alpha: float = 1.0, out_dtype=None, out=None, strea
     """alpha * A @ B^T of two 4-bit matrices of one group each (ozk_mx4_gemm):
     [a.rows, b.rows] of out_dtype (default bfloat16)."""
     _pair_of(a, b)
+    if a._index != _current_device():
+        with _torch.cuda.device(a._index):
+            return mx4_gemm(a, b, alpha, out_dtype, out, stream)
     if a.groups != 1 or b.groups != 1 or a.offsets is not None or b.offsets is not None:
         raise ValueError("matrices of one group are expected; mx4_grouped_gemm takes grouped ones")
     if out_dtype is None and out is None:
         out_dtype = _torch.bfloat16
     out, ld, kind = _result(out, a.rows, b.rows, out_dtype, a.device, stream)
-    _launch("ozk_mx4_gemm", a._index, stream, a.rows, b.rows, a.K, a._codes, a._scales, b._codes, b._scales,
-            _FORMATS[a.fmt], alpha, out.data_ptr(), ld, kind)
+    rc = _lib.ozk_mx4_gemm(a.rows, b.rows, a.K, a._codes, a._scales, b._codes, b._scales, _FORMATS[a.fmt], alpha,
+                           out.data_ptr(), ld, kind, _stream_at(a._index, stream))
+    if rc:
+        raise OzkError("ozk_mx4_gemm", rc)
     return out
 
 
@@ -586,14 +597,20 @@ def mx4_grouped_gemm(x: Mx4, w: Mx4, alpha: float = 1.0, out_dtype=None, out=Non
     w from a [groups, N, K] tensor; [x.rows, N] of out_dtype (default
     bfloat16).  Rows in no group are not written."""
     _pair_of(x, w)
+    if x._index != _current_device():
+        with _torch.cuda.device(x._index):
+            return mx4_grouped_gemm(x, w, alpha, out_dtype, out, stream)
     if x.offsets is None or w.offsets is not None or x.groups != w.groups:
         raise ValueError("rows quantised with offsets and weights of as many equal groups are expected")
     if out_dtype is None and out is None:
         out_dtype = _torch.bfloat16
     N = w.rows // w.groups
     out, ld, kind = _result(out, x.rows, N, out_dtype, x.device, stream)
-    _launch("ozk_mx4_grouped_gemm", x._index, stream, x.rows, N, x.K, x.groups, x.offsets.data_ptr(), x._codes, x._scales,
-            w._codes, w._scales, _FORMATS[x.fmt], alpha, out.data_ptr(), ld, kind)
+    rc = _lib.ozk_mx4_grouped_gemm(x.rows, N, x.K, x.groups, x.offsets.data_ptr(), x._codes, x._scales, w._codes,
+                                   w._scales, _FORMATS[x.fmt], alpha, out.data_ptr(), ld, kind,
+                                   _stream_at(x._index, stream))
+    if rc:
+        raise OzkError("ozk_mx4_grouped_gemm", rc)
     return out
 
 
@@ -619,12 +636,17 @@ def grouped_gemm(x, w, offsets, out_dtype=None, out=None, stream=None):
     type or float32.  Rows in no group are not written."""
     groups, N, K, ldw, stride = _groups(w)
     _, kind, index = _grouped(x, w, offsets, groups)
+    if index != _current_device():
+        with _torch.cuda.device(index):
+            return grouped_gemm(x, w, offsets, out_dtype, out, stream)
     T, k, ldx = _rows(x)
     if k != K:
         raise ValueError(f"x is {tuple(x.shape)}, the weights {tuple(w.shape)}")
     out, ld, out_kind = _result(out, T, N, out_dtype or (x.dtype if out is None else None), x.device, stream)
-    _launch("ozk_grouped_gemm", index, stream, T, N, K, groups, offsets.data_ptr(), x.data_ptr(), ldx, w.data_ptr(), ldw,
-            stride, kind, out.data_ptr(), ld, out_kind)
+    rc = _lib.ozk_grouped_gemm(T, N, K, groups, offsets.data_ptr(), x.data_ptr(), ldx, w.data_ptr(), ldw, stride,
+                               kind, out.data_ptr(), ld, out_kind, _stream_at(index, stream))
+    if rc:
+        raise OzkError("ozk_grouped_gemm", rc)
     return out
 
 
@@ -632,12 +654,17 @@ def grouped_gemm_dx(dy, w, offsets, out_dtype=None, out=None, stream=None):
     """The gradient of grouped_gemm with respect to x: dx[t] = dy[t] @ w[g(t)], [T, K]."""
     groups, N, K, ldw, stride = _groups(w)
     _, kind, index = _grouped(dy, w, offsets, groups)
+    if index != _current_device():
+        with _torch.cuda.device(index):
+            return grouped_gemm_dx(dy, w, offsets, out_dtype, out, stream)
     T, n, lddy = _rows(dy)
     if n != N:
         raise ValueError(f"dy is {tuple(dy.shape)}, the weights {tuple(w.shape)}")
     out, ld, out_kind = _result(out, T, K, out_dtype or (dy.dtype if out is None else None), dy.device, stream)
-    _launch("ozk_grouped_gemm_dx", index, stream, T, N, K, groups, offsets.data_ptr(), dy.data_ptr(), lddy, w.data_ptr(),
-            ldw, stride, kind, out.data_ptr(), ld, out_kind)
+    rc = _lib.ozk_grouped_gemm_dx(T, N, K, groups, offsets.data_ptr(), dy.data_ptr(), lddy, w.data_ptr(), ldw,
+                                  stride, kind, out.data_ptr(), ld, out_kind, _stream_at(index, stream))
+    if rc:
+        raise OzkError("ozk_grouped_gemm_dx", rc)
     return out
 
 
@@ -645,6 +672,9 @@ def grouped_gemm_dw(dy, x, offsets, out_dtype=None, out=None, stream=None):
     """The gradient with respect to w: dw[g] = the sum of dy[t]^T x[t] over the
     rows of group g, [groups, N, K] (zeros for a group without rows)."""
     groups, kind, index = _grouped(dy, x, offsets, None)
+    if index != _current_device():
+        with _torch.cuda.device(index):
+            return grouped_gemm_dw(dy, x, offsets, out_dtype, out, stream)
     (T, N, lddy), (t, K, ldx) = _rows(dy), _rows(x)
     if t != T:
         raise ValueError(f"dy is {tuple(dy.shape)}, x {tuple(x.shape)}")
@@ -658,8 +688,10 @@ def grouped_gemm_dw(dy, x, offsets, out_dtype=None, out=None, stream=None):
             raise TypeError(f"out is {out.dtype}, the result {out_dtype}")
         _same_device(index, out)
         ld, stride = _groups(out)[3:]
-    _launch("ozk_grouped_gemm_dw", index, stream, T, N, K, groups, offsets.data_ptr(), dy.data_ptr(), lddy, x.data_ptr(),
-            ldx, kind, out.data_ptr(), ld, stride, _dtype(out.dtype))
+    rc = _lib.ozk_grouped_gemm_dw(T, N, K, groups, offsets.data_ptr(), dy.data_ptr(), lddy, x.data_ptr(), ldx, kind,
+                                  out.data_ptr(), ld, stride, _dtype(out.dtype), _stream_at(index, stream))
+    if rc:
+        raise OzkError("ozk_grouped_gemm_dw", rc)
     return out
 
 

@@ -105,6 +105,8 @@ def machine(monkeypatch):
     fake = FakeTorch()
     library = FakeLibrary(fake)
     monkeypatch.setattr(ozk, "_torch", fake)
+    monkeypatch.setattr(ozk, "_current_device", fake._cuda_getDevice)
+    monkeypatch.setattr(ozk, "_current_stream", fake._cuda_getCurrentRawStream)
     monkeypatch.setattr(ozk, "_lib", library)
     monkeypatch.setattr(ozk, "_DTYPES", {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.float64: 3})
     return library
