@@ -59,6 +59,7 @@ constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr uint32_t kRowBytes = 128;                       // K bytes of a stage: one swizzle row
 constexpr uint32_t kABytes = kTileRows * kRowBytes;       // 16 KB
 constexpr uint32_t kScaleTile = 512;                      // 128 rows x 4 scale bytes
+constexpr uint64_t kStageNs = 4000;  // what a stage may take, for the limits of the waits (0.3 us is usual)
 constexpr int kSuper = 16;       // tiles of the M side that run together (L2 reuse)
 
 constexpr int kTableInts = 4 * (kMaxGroups + 1);  // group table: see Group
@@ -797,13 +798,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 2 && OP == kGradWeights) {
     // ------------------------------ tails ------------------------------
     int e = 0;
-    unsigned pos = 0;  // stages the producer has filled before this tile
+    unsigned pos = 0;     // stages the producer has filled before this tile
+    unsigned waited = 0;  // of them, before the last tile with a tail
     uint32_t tails = 0;
     for (int wave = 0, u; (u = walk.at(wave)) >= 0; ++wave) {
       const Tile t = tile_at<C, OP>(p, g, u, e);
       if (t.blocks > 0 && has_tail<OP>(t)) {
         const int stage = static_cast<int>((pos + t.blocks - 1) % C::STAGES);
-        if (!warp_wait(tail0 + 8 * stage, (tails >> stage) & 1u, abort_flag, p.timeout_ns)) break;
+        // this warp is ahead of the others by the tiles without a tail since the last one
+        const uint64_t limit = p.timeout_ns + kStageNs * (pos + static_cast<unsigned>(t.blocks) - waited);
+        if (!warp_wait(tail0 + 8 * stage, (tails >> stage) & 1u, abort_flag, limit)) break;
+        waited = pos + static_cast<unsigned>(t.blocks);
         tails ^= 1u << stage;
         const int r0 = t.k % 64;                 // first row past the group's end; the MMAs stop at the next 16
         const int r1 = (r0 + 15) / 16 * 16;
@@ -1029,7 +1034,7 @@ cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
   p.vec = q.out_type != OZK_F32 && reinterpret_cast<uintptr_t>(q.out) % 16 == 0 && q.ldo % 8 == 0 &&
           (OP != kGradWeights || q.groups == 1 || q.out_group % 8 == 0);
   const int64_t terms = OP == kGradWeights ? q.T : q.K;
-  p.timeout_ns = kTimeoutNs + 4000ull * static_cast<uint64_t>(terms / C::BLOCK_K);
+  p.timeout_ns = kTimeoutNs + kStageNs * static_cast<uint64_t>(terms / C::BLOCK_K);
   p.withhold_kb = -1;
   if (g_withhold.timeout_us != 0) {
     p.timeout_ns = 1000ull * g_withhold.timeout_us;
