@@ -721,6 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // first TMEM column of a stage's scale word: of the M side, and of the N side
     auto sfa_of = [&](int word) { return tmem_base + C::SF_BASE + 4u * word; };
     auto sfb_of = [&](int word) { return tmem_base + C::SF_BASE + 4u * C::KG + 4u * C::NB * word; };
+    if (!p.offsets) grid_dependency_sync();  // reads nothing, but its waits are for this kernel's copies alone
     int stage = 0, e = 0, ab = 0;
     uint32_t phase = 0, aphase = 0;
     bool ok = true, first = true;

@@ -104,3 +104,22 @@ def test_waits_for_a_tail_behind_many_tiles():
     got = ozk.grouped_gemm_dw(dy, x, off)
     assert ozk.ozk_stream_status() == 0
     assert torch.equal(got, want)
+
+
+@pytest.mark.gpu
+def test_waits_do_not_count_the_kernel_before():
+    """A product without offsets may start while the kernel before it still runs (here 10 ms, on one SM): its limit of 2 ms
+    is for its own work."""
+    rows = 1 << 22
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    dy, x = whole(rows, 128, seed=1), whole(rows, 128, seed=2)
+    a, b = ozk.mx4_quantize(whole(300, 640, seed=3)), ozk.mx4_quantize(whole(300, 640, seed=4))
+    want = ozk.mx4_gemm(a, b)
+    ozk.grouped_gemm_dw(dy, x, off)
+    assert ozk.ozk_stream_status() == 0
+    for pairs in (0, 1):
+        ozk.grouped_gemm_dw(dy, x, off)
+        ozk.ozk_withhold_next_product(pairs, 0, -1, 2000)
+        got = ozk.mx4_gemm(a, b)
+        assert ozk.ozk_stream_status() == 0
+        assert torch.equal(got, want)
