@@ -105,9 +105,9 @@ struct Config {
   // accumulator full and empty; drain
   static constexpr int BARS = (OP == kGradWeights ? 4 : 2) * STAGES + 5;
   static constexpr uint32_t OUT_STAGE = 8192;  // of each side of the epilogue: 32 rows of 128 16-bit columns
-  static constexpr uint32_t CTRL = 320;  // barriers, TMEM address, abort flag; from 256 on an Issue per stage
+  static constexpr uint32_t CTRL = 384;  // barriers, TMEM address, abort flag; from 256 on the loaders' last issues
   static constexpr uint32_t FIXED = 1024 + STAGES * STAGE + 2 * OUT_STAGE + CTRL;
-  static_assert(8 * BARS + 8 <= 256 && 256 + 8 * STAGES <= CTRL, "control words");
+  static_assert(8 * BARS + 8 <= 256 && 256 + 2 * 8 * STAGES <= CTRL, "control words");
   static_assert(FIXED + 4 * kTableInts <= 232448, "shared memory");
   static_assert(BN % 32 == 0 && B_ROWS % BOX == 0, "copies of whole boxes fill a stage exactly");
 };
@@ -502,9 +502,11 @@ __device__ __forceinline__ void store_edge(uint16_t* out, int64_t ldo, int rows,
 // ---------------------------------------------------------------------------
 // The abort path
 // ---------------------------------------------------------------------------
-// The last issue of a stage's copies: its number (from 1; 0: none yet), the
+// A loader's last issue of a stage's copies: its number (from 1; 0: none), the
 // bytes of this CTA, and for a group's last block, which arrives on the tail
-// barrier, bit 31 and the parity of that barrier's phase in bit 30.
+// barrier, bit 31 and the parity of that barrier's phase in bit 30.  Lane s of
+// each loader warp holds that of stage s until the roles end, so that a stage
+// costs the loaders no store.
 struct alignas(8) Issue {
   uint32_t number, word;
 };
@@ -526,18 +528,20 @@ __device__ __forceinline__ void st_shared_cluster(uint32_t addr, uint32_t v) {
 // pair the copies of both CTAs arrive on the leader's barrier, armed by the
 // leader for both: where only one of the two issued the stage's last use, the
 // leader stands in for the other.
+__device__ __forceinline__ Issue later(const Issue& a, const Issue& b) { return a.number > b.number ? a : b; }
 template <typename C>
 __device__ __forceinline__ void drain_copies(const Issue* issues, uint32_t full0, uint32_t tail0, bool leader) {
   for (int s = 0; s < C::STAGES; ++s) {
-    const Issue own = issues[s];
+    const Issue own = later(issues[s], issues[C::STAGES + s]);
     const bool tail = own.word >> 31;
     if (tail) mbar_wait_drain(tail0 + 8 * s, (own.word >> 30) & 1u);
     bool full = own.number != 0 && !tail;
     uint32_t number = own.number;
     if (C::PAIR) {
       if (!leader) continue;
-      const uint32_t remote = cluster_addr(smem_u32(issues + s), 1);
-      const Issue peer{ld_shared_cluster(remote), ld_shared_cluster(remote + 4)};
+      const uint32_t remote = cluster_addr(smem_u32(issues + s), 1), other = remote + 8 * C::STAGES;
+      const Issue peer = later({ld_shared_cluster(remote), ld_shared_cluster(remote + 4)},
+                               {ld_shared_cluster(other), ld_shared_cluster(other + 4)});
       if (peer.number > own.number) {
         full = !(peer.word >> 31);
         number = peer.number;
@@ -601,7 +605,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
-      issues[s] = {0, 0};
       if (OP == kGradWeights) {
         mbar_init(tail0 + 8 * s, 1);
         mbar_init(peer0 + 8 * s, 1);
@@ -646,6 +649,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int stage = 0, e = 0, issued = 0;
     const int turn = warp == 3;
     uint32_t phase = 0, tails = 0;
+    Issue last = {0, 0};  // of stage `lane`
+    int withheld = static_cast<int>(blockIdx.x) == p.withhold_cta ? p.withhold_kb : -1;  // block of the first tile
     bool ok = true, waited = p.offsets != nullptr;
     for (int wave = 0, u; ok && (u = walk.at(wave)) >= 0; ++wave) {
       const Tile t = tile_at<C, OP>(p, g, u, e);
@@ -662,8 +667,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!waited) grid_dependency_sync();  // the first tile is laid out by now
         waited = true;
         const bool clear = has_tail<OP>(t) && kb == t.blocks - 1;
-        const bool withheld = kb == p.withhold_kb && wave == 0 && static_cast<int>(blockIdx.x) == p.withhold_cta;
-        if (mine && !withheld && elect_one()) {
+        const bool issue = mine && kb != withheld;
+        if (issue && elect_one()) {
           uint32_t bar = full0 + 8 * stage;
           if (clear) {  // warp 2 passes the stage on once it has cleared the rows
             bar = tail0 + 8 * stage;
@@ -704,9 +709,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             load3(sSA + stage * C::SFA_BYTES, &tmSW, 0, kb * C::KG, wrow + t.e + m0 / 128);
             load3(sSB + stage * C::SFB_BYTES, &tmSR, 0, kb * C::KG, t.row0 / 128 + t.e + t.n0 / 128);
           }
-          issues[stage] = {static_cast<uint32_t>(issued) + 1u,
-                           bytes | (clear ? 0x80000000u | ((tails >> stage) & 1u) << 30 : 0u)};
         }
+        if (issue && lane == stage)
+          last = {static_cast<uint32_t>(issued) + 1u, bytes | (clear ? 0x80000000u | ((tails >> stage) & 1u) << 30 : 0u)};
         if (clear) tails ^= 1u << stage;
         ++issued;
         if (++stage == C::STAGES) {
@@ -714,7 +719,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           phase ^= 1u;
         }
       }
+      withheld = -1;
     }
+    if (lane < C::STAGES) issues[turn * C::STAGES + lane] = last;
     __syncwarp();
   } else if (warp == 1 && leader) {
     // ------------------------------ MMA issuer ------------------------------
