@@ -7,8 +7,8 @@ matrices are applied to its own rows:
 
     h = relu(x W1_e^T)        y = sum over the row's experts of p_e (h W2_e^T)
 
-Training runs ozk.grouped_gemm and its gradients ozk.grouped_gemm_dx and
-ozk.grouped_gemm_dw; serving quantises the weights once (ozk.mx4_quantize) and
+Training runs ozk.grouped_gemm, whose gradients autograd takes from
+ozk.grouped_gemm_dx and ozk.grouped_gemm_dw; serving quantises the weights once (ozk.mx4_quantize) and
 each call's rows as they come, and multiplies them with ozk.mx4_grouped_gemm.
 
     python examples/expert_layer.py [--rows 4096] [--experts 8] [--steps 30]
@@ -21,21 +21,6 @@ import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 from fp64_gemm_emulation_exponent_gb300 import ozk  # noqa: E402
-
-
-class GroupedLinear(torch.autograd.Function):
-    """y[t] = x[t] @ w[g(t)]^T for rows sorted by group."""
-
-    @staticmethod
-    def forward(ctx, x, w, offsets):
-        ctx.save_for_backward(x, w, offsets)
-        return ozk.grouped_gemm(x, w, offsets)
-
-    @staticmethod
-    def backward(ctx, dy):
-        x, w, offsets = ctx.saved_tensors
-        dy = dy.contiguous()
-        return ozk.grouped_gemm_dx(dy, w, offsets), ozk.grouped_gemm_dw(dy, x, offsets), None
 
 
 def route(x, router, top):
@@ -57,8 +42,8 @@ class ExpertLayer:
 
     def train_forward(self, x):
         rows, offsets, p = route(x, self.router, self.top)
-        h = torch.relu(GroupedLinear.apply(x[rows], self.w1, offsets))
-        y = GroupedLinear.apply(h, self.w2, offsets)
+        h = torch.relu(ozk.grouped_gemm(x[rows], self.w1, offsets))
+        y = ozk.grouped_gemm(h, self.w2, offsets)
         return torch.zeros_like(x, dtype=torch.float32).index_add(0, rows, y.float() * p[:, None])
 
     def quantize(self, fmt="nvfp4"):

@@ -633,12 +633,21 @@ def _grouped(first, second, offsets, groups):
 def grouped_gemm(x, w, offsets, out_dtype=None, out=None, stream=None):
     """y[t] = x[t] @ w[g(t)]^T (ozk_grouped_gemm): x [T, K], w [groups, N, K] of
     one 16-bit type, offsets int32 [groups + 1] on the device; [T, N] of their
-    type or float32.  Rows in no group are not written."""
+    type or float32.  Rows in no group are not written.
+
+    Autograd records it where x or w asks for a gradient (grouped_gemm_dx and
+    grouped_gemm_dw, each only where asked for; zeros for rows in no group; a
+    float32 result's gradient is rounded to the operands' type), once: there is
+    no second derivative.  With out given, and in every other call here, no
+    graph is recorded."""
     groups, N, K, ldw, stride = _groups(w)
     _, kind, index = _grouped(x, w, offsets, groups)
     if index != _current_device():
         with _torch.cuda.device(index):
             return grouped_gemm(x, w, offsets, out_dtype, out, stream)
+    if out is None and (x.requires_grad or w.requires_grad) and _torch.is_grad_enabled():
+        with _torch.cuda.stream(stream):
+            return (_GroupedGemm or _load_function()).apply(x, w, offsets, out_dtype)
     T, k, ldx = _rows(x)
     if k != K:
         raise ValueError(f"x is {tuple(x.shape)}, the weights {tuple(w.shape)}")
@@ -648,6 +657,44 @@ def grouped_gemm(x, w, offsets, out_dtype=None, out=None, stream=None):
     if rc:
         raise OzkError("ozk_grouped_gemm", rc)
     return out
+
+
+def _bulk_rows(t):
+    """t, or a copy of it, with rows that bulk copies can read."""
+    rows, cols = t.shape
+    if t.stride(1) == 1 and t.stride(0) >= cols and t.stride(0) % 8 == 0 and t.data_ptr() % 16 == 0:
+        return t
+    copy = _torch.empty((rows, -(-cols // 8) * 8), dtype=t.dtype, device=t.device)[:, :cols]
+    return copy.copy_(t)
+
+
+_GroupedGemm = None
+
+
+def _load_function():
+    """The autograd function of grouped_gemm (torch is loaded by now)."""
+    global _GroupedGemm
+
+    class GroupedGemm(_torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w, offsets, out_dtype):
+            ctx.save_for_backward(x, w, offsets)
+            return grouped_gemm(x, w, offsets, out_dtype)
+
+        @staticmethod
+        @_torch.autograd.function.once_differentiable
+        def backward(ctx, dy):
+            x, w, offsets = ctx.saved_tensors
+            dy = _bulk_rows(dy.to(x.dtype))
+            dx = dw = None
+            if ctx.needs_input_grad[0]:
+                dx = grouped_gemm_dx(dy, w, offsets, out=_torch.zeros(x.shape, dtype=x.dtype, device=x.device))
+            if ctx.needs_input_grad[1]:
+                dw = grouped_gemm_dw(dy, x, offsets)
+            return dx, dw, None, None
+
+    _GroupedGemm = GroupedGemm
+    return GroupedGemm
 
 
 def grouped_gemm_dx(dy, w, offsets, out_dtype=None, out=None, stream=None):
