@@ -166,9 +166,12 @@ def peaks():
     return {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustained": 1700.0, "source": "fallback"}
 
 
+KERNEL_SOURCES = ("residue_gemm.cu", "ozk_internal.h", "tc_ptx.cuh")  # of the residue GEMM
+
+
 def kernel_source_hash() -> str:
     h = hashlib.sha256()
-    for f in ("residue_gemm.cu", "ozk_internal.h"):
+    for f in KERNEL_SOURCES:
         h.update(open(os.path.join(ROOT, "fp64_gemm_emulation_exponent_gb300", "csrc", f), "rb").read())
     return h.hexdigest()[:16]
 
