@@ -388,9 +388,12 @@ def _empty(shape, dtype, device, stream):
 def _result(out, rows, cols, dtype, device, stream):
     """(tensor, leading dimension, ozk_dtype) of a rows x cols result: out, or a new tensor; dtype None: out's own."""
     if out is None:
+        kind = _DTYPES.get(dtype)
+        if kind is None:
+            _dtype(dtype)  # raises
         if stream is None:
-            return _torch.empty((rows, cols), dtype=dtype, device=device), cols or 1, _DTYPES[dtype]
-        return _empty((rows, cols), dtype, device, stream), cols or 1, _DTYPES[dtype]
+            return _torch.empty((rows, cols), dtype=dtype, device=device), cols or 1, kind
+        return _empty((rows, cols), dtype, device, stream), cols or 1, kind
     if out.shape != (rows, cols):
         raise ValueError(f"out has shape {tuple(out.shape)}, the result ({rows}, {cols})")
     if dtype is not None and out.dtype != dtype:
@@ -726,6 +729,8 @@ def grouped_gemm_dw(dy, x, offsets, out_dtype=None, out=None, stream=None):
     if t != T:
         raise ValueError(f"dy is {tuple(dy.shape)}, x {tuple(x.shape)}")
     if out is None:
+        if out_dtype is not None:
+            _dtype(out_dtype)
         out = _empty((groups, N, K), out_dtype or x.dtype, x.device, stream)
         ld, stride = K or 1, N * (K or 1)
     else:

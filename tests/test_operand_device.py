@@ -194,3 +194,22 @@ def test_host_operands_run_on_the_streams_device(machine):
 def test_status_is_that_of_the_streams_device(machine):
     ozk.ozk_stream_status(FakeStream(3))
     assert machine.calls == [("ozk_stream_status", 3, 0x5003)]
+
+
+RESULTS = {
+    "mx4_dequantize": lambda dtype: ozk.mx4_dequantize(matrix(), dtype),
+    "mx4_gemm": lambda dtype: ozk.mx4_gemm(matrix(), matrix(), out_dtype=dtype),
+    "mx4_grouped_gemm": lambda dtype: ozk.mx4_grouped_gemm(matrix(offsets=offsets()), matrix(groups=2), out_dtype=dtype),
+    "grouped_gemm": lambda dtype: ozk.grouped_gemm(tensor(16, 64), tensor(2, 32, 64), offsets(), out_dtype=dtype),
+    "grouped_gemm_dx": lambda dtype: ozk.grouped_gemm_dx(tensor(16, 32), tensor(2, 32, 64), offsets(), out_dtype=dtype),
+    "grouped_gemm_dw": lambda dtype: ozk.grouped_gemm_dw(tensor(16, 32), tensor(16, 64), offsets(), out_dtype=dtype),
+}
+
+
+@pytest.mark.parametrize("name", RESULTS)
+def test_result_types_that_the_library_lacks(machine, name):
+    """A TypeError that names the type, before anything is allocated or launched."""
+    for dtype in (torch.int32, torch.bool, torch.complex64):
+        with pytest.raises(TypeError, match="ozk_dtype"):
+            RESULTS[name](dtype)
+    assert machine.calls == []
