@@ -30,6 +30,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "lowp.h"
@@ -617,10 +618,13 @@ cudaError_t dispatch(int dtype, int format, int align, F&& f) {
   });
 }
 
+std::atomic<bool> g_with_offsets{false};  // launched yet: without, there is no status to read
+
 }  // namespace
 
 cudaError_t launch_mx4_quantize(const Mx4Matrix& m, const void* x, int64_t ldx, int dtype, float prescale,
                                 int num_sms, cudaStream_t stream) {
+  if (m.offsets != nullptr) g_with_offsets.store(true, std::memory_order_relaxed);
   Mx4Params p = make_params(m, ldx, num_sms);
   p.x = x;
   p.prescale = prescale;
@@ -632,6 +636,7 @@ cudaError_t launch_mx4_quantize(const Mx4Matrix& m, const void* x, int64_t ldx, 
 
 cudaError_t launch_mx4_dequantize(const Mx4Matrix& m, void* out, int64_t ldo, int dtype, int num_sms,
                                   cudaStream_t stream) {
+  if (m.offsets != nullptr) g_with_offsets.store(true, std::memory_order_relaxed);
   Mx4Params p = make_params(m, ldo, num_sms);
   p.out = out;
   return dispatch(dtype, m.format, alignment(out, ldo, dtype), [&](auto t, auto fmt, auto align) {
@@ -640,6 +645,9 @@ cudaError_t launch_mx4_dequantize(const Mx4Matrix& m, void* out, int64_t ldo, in
   });
 }
 
-int take_mx4_status(int* status) { return take_status(status); }
+int take_mx4_status(int* status) {
+  *status = 0;
+  return g_with_offsets.load(std::memory_order_relaxed) ? take_status(status) : OZK_OK;
+}
 
 }  // namespace ozk

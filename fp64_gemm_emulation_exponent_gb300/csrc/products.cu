@@ -42,6 +42,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <map>
@@ -1177,7 +1178,10 @@ cudaError_t choose(const Product& q, int num_sms, cudaStream_t stream) {
 
 }  // namespace
 
+static std::atomic<bool> g_any{false};  // a product was launched: without one there is no status to read
+
 cudaError_t launch_product(const Product& q, int num_sms, cudaStream_t stream) {
+  g_any.store(true, std::memory_order_relaxed);
   switch (q.op) {
     case kForward: return choose<kForward, k16>(q, num_sms, stream);
     case kGradRows: return choose<kGradRows, k16>(q, num_sms, stream);
@@ -1187,7 +1191,10 @@ cudaError_t launch_product(const Product& q, int num_sms, cudaStream_t stream) {
   }
 }
 
-int take_product_status(int* status) { return take_status(status); }
+int take_product_status(int* status) {
+  *status = 0;
+  return g_any.load(std::memory_order_relaxed) ? take_status(status) : OZK_OK;
+}
 
 void withhold_next_product(int pairs, int cta, int kblock, uint32_t timeout_us) {
   g_withhold = {pairs, cta, kblock, timeout_us};

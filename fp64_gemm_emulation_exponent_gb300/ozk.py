@@ -260,7 +260,9 @@ def ozk_dgemm_host_async(M, N, K, A, lda, B, ldb, C, ldc, n_moduli, stream=None)
 def ozk_stream_status(stream=None):
     """Status of the given stream and its device, or of the current ones."""
     torch = _torch or _load_torch()
-    with torch.cuda.device(None if stream is None else stream.device_index):
+    if stream is None or stream.device_index == _current_device():
+        return lib().ozk_stream_status(_stream(stream))
+    with torch.cuda.device(stream.device_index):
         return lib().ozk_stream_status(_stream(stream))
 
 
