@@ -274,13 +274,14 @@ def dgemm(A, B, n_moduli: int = 14, out=None, stream=None, target_bits=None, sca
     """C = A @ B for float64 CUDA tensors through ozk_dgemm (or ozk_dgemm_bits
     when target_bits is given: the moduli count then follows from K; or
     ozk_dgemm_norm with scaling="norm": scales from the rows' 2-norms)."""
-    torch = _torch or _load_torch()
+    if _torch is None:
+        _load_torch()
     M, K = A.shape
     K2, N = B.shape
     if K != K2:
         raise ValueError("inner dimensions differ")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float64, device=A.device)
+        out = _empty((M, N), torch.float64, A.device, stream)
     if scaling == "norm":
         if target_bits is not None:
             raise ValueError("target_bits picks the count of the largest-entry rule")

@@ -52,6 +52,7 @@ class FakeTorch:
 
     def __init__(self):
         self.current = 0
+        self.on, self.allocated_on = None, []
         for name in ("int32", "uint8", "bfloat16", "float16", "float32", "float64"):
             setattr(self, name, getattr(torch, name))
         self._C = self.cuda = self
@@ -74,14 +75,17 @@ class FakeTorch:
 
     @contextlib.contextmanager
     def stream(self, s):
+        before, self.on = self.on, s or self.on
         with self.device(self.current if s is None else s.device_index):
             yield
+        self.on = before
 
     def is_grad_enabled(self):
         return True
 
     def empty(self, *shape, dtype=None, device=None):
         shape = shape[0] if isinstance(shape[0], tuple) else shape
+        self.allocated_on.append(self.on)
         return FakeTensor(shape, dtype, int(str(device)[5:]), storage=1 << 42)
 
 
@@ -213,3 +217,11 @@ def test_result_types_that_the_library_lacks(machine, name):
         with pytest.raises(TypeError, match="ozk_dtype"):
             RESULTS[name](dtype)
     assert machine.calls == []
+
+
+@pytest.mark.parametrize("name", list(LOWP) + ["ozk_dgemm", "ozk_dgemm_norm", "ozk_dgemm_bits"])
+def test_results_are_allocated_on_the_stream_that_writes_them(machine, name):
+    """Memory that another stream's kernels may still be using must not be handed to it."""
+    s = FakeStream(1)
+    {**LOWP, **FP64}[name](1, s)
+    assert machine.fake.allocated_on == [s]
