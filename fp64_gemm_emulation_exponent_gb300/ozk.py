@@ -281,7 +281,7 @@ def dgemm(A, B, n_moduli: int = 14, out=None, stream=None, target_bits=None, sca
     if K != K2:
         raise ValueError("inner dimensions differ")
     if out is None:
-        out = _empty((M, N), torch.float64, A.device, stream)
+        out = _empty((M, N), _torch.float64, A.device, stream)
     if scaling == "norm":
         if target_bits is not None:
             raise ValueError("target_bits picks the count of the largest-entry rule")
