@@ -903,14 +903,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           else stage_block<__nv_bfloat16>(block, quad, lane, lo, hi, p.alpha);
           fence_proxy_async_smem();
           side_sync(side);
-          if (rows >= 32) {  // columns past M the map leaves out
+          // A bulk store leaves out columns past M in whole 16-byte pieces alone: what lies in the piece that M
+          // ends in would be overwritten.
+          const int cols = p.M - m0;
+          if (rows >= 32 && (cols >= kTileRows || cols % 8 == 0)) {
             const int n = OP == kGradWeights ? t.n0 + c : t.row0 + t.n0 + c;
             if (issuer) {
               if (m0 < p.M) tma_store_3d(&tmO, block, m0, n, OP == kGradWeights ? t.e : 0);
               if (m0 + 64 < p.M) tma_store_3d(&tmO, block + kOutHalf, m0 + 64, n, OP == kGradWeights ? t.e : 0);
             }
           } else {
-            store_edge(static_cast<uint16_t*>(p.out) + o - (m - m0), p.ldo, rows, p.M - m0, block, quad, lane);
+            store_edge(static_cast<uint16_t*>(p.out) + o - (m - m0), p.ldo, min(rows, 32), cols, block, quad, lane);
           }
           continue;
         }
