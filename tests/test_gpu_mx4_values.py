@@ -61,3 +61,25 @@ def test_products_of_no_terms_are_zero(alpha, dtype):
     out = torch.full((5, 7), 9.0, device="cuda", dtype=dtype)
     ozk.mx4_grouped_gemm(x, w, alpha=alpha, out=out)
     assert torch.equal(out, torch.zeros_like(out))
+
+
+def test_scales_at_ties_and_their_neighbours():
+    """amax / 6 at and next to every boundary between two E4M3 scales, in fp32: one unit below a tie is below it, although a
+    product with 1/6 would round onto the tie."""
+    ties = (ref.E4M3[:-1] + ref.E4M3[1:]) / 2
+    at = (6 * ties).astype(np.float32)  # exact
+    assert np.array_equal(at.astype(np.float64), 6 * ties)
+    tops = [at]
+    for to in (np.float32(0), np.float32(np.inf)):
+        v = at
+        for _ in range(3):
+            v = np.nextafter(v, to)
+            tops.append(v)
+    x = np.zeros((len(tops) * len(ties), 16), dtype=np.float32)
+    x[:, 3] = np.concatenate(tops)
+    x[:, 7] = -x[:, 3] / 3
+    q = ozk.mx4_quantize(torch.from_numpy(x).cuda(), "nvfp4")
+    code, neg, byte = ref.quantize(x, "nvfp4")
+    assert np.array_equal(ref.stored_scales(q.scales.cpu().numpy(), len(x), 16, "nvfp4", [0, len(x)]), byte)
+    want = ref.values(code, neg, byte, "nvfp4", 16)
+    assert np.array_equal(ozk.mx4_dequantize(q, torch.float64).cpu().numpy(), want)
