@@ -77,8 +77,8 @@ __device__ __forceinline__ int64_t row_of(const Mx4Params& p, int64_t u, int* ch
 // as they came; more in shared memory, cut so that they rise inside [0, rows].
 // A product cuts bad offsets the same way, so codes, scales and products agree
 // on the group of a row.  In lanes they cost no barrier and a row's search no
-// memory: 32 rows in 32 groups 2.6 us with every block checking them first, 2.2
-// so.
+// memory: a row in 8 groups 2.3 us with every block checking them first, 1.8 so;
+// 32 rows in 256 groups 2.7 us with a search in global memory, 2.4 so.
 constexpr int kLaneGroups = 31;
 struct Starts {
   int own;           // start of group `lane`, INT32_MAX past the last end
@@ -86,9 +86,10 @@ struct Starts {
   const int* table;
 };
 
+template <bool RAGGED>
 __device__ __forceinline__ Starts load_starts(const Mx4Params& p, int lane) {
   extern __shared__ int table[];
-  if (p.offsets == nullptr) return {0, false, table};
+  if (!RAGGED) return {0, false, table};
   if (p.groups <= kLaneGroups) return {lane <= p.groups ? p.offsets[lane] : INT32_MAX, true, table};
   bool bad = false;
   for (int i = threadIdx.x; i <= p.groups; i += kThreads) {
@@ -118,20 +119,21 @@ __device__ __forceinline__ void cut_starts(const Mx4Params& p, Starts& s, int la
   if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_status, 2);
   s.own = max(s.own, 0);
 #pragma unroll
-  for (int d = 1; d < 32; d *= 2) s.own = max(s.own, __shfl_up_sync(0xFFFFFFFFu, s.own, d));  // lanes below d: their own
+  for (int d = 1; d < 32; d *= 2) s.own = max(s.own, __shfl_up_sync(0xFFFFFFFFu, s.own, d));  // below d: their own
 }
 
 // Byte offset of the scale word (4 blocks) kg = 0 of `row`, or -1 for a row
 // outside every group (the whole warp, on one row).
+template <bool RAGGED>
 __device__ __forceinline__ int64_t scale_row(const Mx4Params& p, Starts& s, int64_t row64, int lane) {
   const int row = static_cast<int>(row64);  // below 2^30
   int g = 0, o = 0;
-  if (p.offsets != nullptr && p.groups <= kLaneGroups) {
+  if (RAGGED && p.groups <= kLaneGroups) {
     if (s.raw) cut_starts(p, s, lane);
     g = __popc(__ballot_sync(0xFFFFFFFFu, s.own <= row)) - 1;  // a start past the rows is past this one
     if (g < 0 || g >= p.groups) return -1;
     o = __shfl_sync(0xFFFFFFFFu, s.own, g);
-  } else if (p.offsets != nullptr) {
+  } else if (RAGGED) {
     int lo = 0, hi = p.groups;  // the last group that starts at or before the row
     while (lo + 1 < hi) {
       const int mid = (lo + hi) / 2;
@@ -414,14 +416,14 @@ __device__ __forceinline__ void quantize16(const Mx4Params& p, const Raw<T>& r, 
     *reinterpret_cast<uint32_t*>(p.scales + at + static_cast<int64_t>(kg) * 512) = word;
 }
 
-template <typename T, int FMT, int ALIGN>
+template <typename T, int FMT, int ALIGN, bool RAGGED>
 __global__ void __launch_bounds__(kThreads, sizeof(T) > 4 ? 2 : 4) mx4_quantize_kernel(const Mx4Params p) {
   grid_dependency_sync();
   __shared__ alignas(16) uint8_t stages[ALIGN >= 16 ? 16 : kWarps * kWarpElems * sizeof(T)];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint8_t* stage = ALIGN >= 16 ? stages : stages + warp * kWarpElems * sizeof(T);
   const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
-  Starts starts = load_starts(p, lane);
+  Starts starts = load_starts<RAGGED>(p, lane);
   for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < p.units; u += warps) {
     int c;
     const int64_t row = row_of(p, u, &c);
@@ -429,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) > 4 ? 2 : 4) mx4_quantize_
     const int c1 = min(c + p.run, p.chunks);
     Raw<T> r;
     load_raw<T, ALIGN>(src, c * kWarpElems, p.K, lane, stage, r);
-    const int64_t at = scale_row(p, starts, row, lane);
+    const int64_t at = scale_row<RAGGED>(p, starts, row, lane);
     if (at < 0) continue;
 #pragma unroll 2
     for (;;) {  // the next chunk is on its way while this one is quantised
@@ -455,18 +457,23 @@ __device__ __forceinline__ float2 code_pair(uint2 code, int i) {
 // exact in fp32 but for scales from 2^126, where it can pass fp32's range; for
 // FP64, which holds it, such a product is done again in FP64 (for every scale it
 // would take 281 us for 16384 x 8192, 226 so).
-template <typename T, int FMT, int ALIGN>
-__global__ void __launch_bounds__(kThreads, sizeof(T) > 4 ? 3 : 1) mx4_dequantize_kernel(const Mx4Params p) {
+// Blocks of an SM: as many as the registers of a lane's 16 elements leave room for.
+constexpr int dequantize_blocks(int size, int align) {
+  return size > 4 ? 3 : size == 4 ? (align == 16 ? 5 : 4) : align == 32 ? 4 : align == 2 ? 5 : 6;
+}
+
+template <typename T, int FMT, int ALIGN, bool RAGGED>
+__global__ void __launch_bounds__(kThreads, dequantize_blocks(sizeof(T), ALIGN)) mx4_dequantize_kernel(const Mx4Params p) {
   grid_dependency_sync();
   __shared__ alignas(16) uint8_t stages[ALIGN >= 16 ? 16 : kWarps * kWarpElems * sizeof(T)];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   T* stage = reinterpret_cast<T*>(ALIGN >= 16 ? stages : stages + warp * kWarpElems * sizeof(T));
   const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
-  Starts starts = load_starts(p, lane);
+  Starts starts = load_starts<RAGGED>(p, lane);
   for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < p.units; u += warps) {
     int c;
     const int64_t row = row_of(p, u, &c);
-    const int64_t at = scale_row(p, starts, row, lane);
+    const int64_t at = scale_row<RAGGED>(p, starts, row, lane);
     if (at < 0) continue;
     const int c1 = min(c + p.run, p.chunks);
     const uint8_t* codes = p.codes + row * (p.kpad / 2);
@@ -602,16 +609,21 @@ int alignment(const void* x, int64_t ld, int dtype) {
   return a % 32 == 0 ? 32 : a % 16 == 0 ? 16 : a % 4 == 0 ? 4 : 2;
 }
 
-// f(element type, format, alignment) with constants.
+// f(element type, format, alignment, ragged groups) with constants.  A matrix
+// without offsets has kernels without the search for a row's group (1537 x 2090
+// fp16 to MXFP4 3.70 us, 3.82 with it).
 template <typename F>
-cudaError_t dispatch(int dtype, int format, int align, F&& f) {
+cudaError_t dispatch(int dtype, int format, int align, bool ragged, F&& f) {
   return pick_type(dtype, [&](auto t) {
     using T = decltype(t);
+    auto aligned = [&](auto fmt, auto a) {
+      return ragged ? f(t, fmt, a, std::true_type{}) : f(t, fmt, a, std::false_type{});
+    };
     auto with = [&](auto fmt) {
-      if (align == 32) return f(t, fmt, std::integral_constant<int, 32>{});
-      if (align == 16) return f(t, fmt, std::integral_constant<int, 16>{});
-      if (align == 4 || sizeof(T) > 2) return f(t, fmt, std::integral_constant<int, 4>{});
-      return f(t, fmt, std::integral_constant<int, sizeof(T) == 2 ? 2 : 4>{});
+      if (align == 32) return aligned(fmt, std::integral_constant<int, 32>{});
+      if (align == 16) return aligned(fmt, std::integral_constant<int, 16>{});
+      if (align == 4 || sizeof(T) > 2) return aligned(fmt, std::integral_constant<int, 4>{});
+      return aligned(fmt, std::integral_constant<int, sizeof(T) == 2 ? 2 : 4>{});
     };
     return format == OZK_MXFP4 ? with(std::integral_constant<int, OZK_MXFP4>{})
                                : with(std::integral_constant<int, OZK_NVFP4>{});
@@ -628,9 +640,10 @@ cudaError_t launch_mx4_quantize(const Mx4Matrix& m, const void* x, int64_t ldx, 
   Mx4Params p = make_params(m, ldx, num_sms);
   p.x = x;
   p.prescale = prescale;
-  return dispatch(dtype, m.format, alignment(x, ldx, dtype), [&](auto t, auto fmt, auto align) {
-    return launch_dependent(mx4_quantize_kernel<decltype(t), fmt.value, align.value>, dim3(grid_of(p.units, num_sms)),
-                            dim3(kThreads), starts_bytes(m), stream, p);
+  const bool groups = m.offsets != nullptr;
+  return dispatch(dtype, m.format, alignment(x, ldx, dtype), groups, [&](auto t, auto fmt, auto align, auto ragged) {
+    return launch_dependent(mx4_quantize_kernel<decltype(t), fmt.value, align.value, ragged.value>,
+                            dim3(grid_of(p.units, num_sms)), dim3(kThreads), starts_bytes(m), stream, p);
   });
 }
 
@@ -639,9 +652,10 @@ cudaError_t launch_mx4_dequantize(const Mx4Matrix& m, void* out, int64_t ldo, in
   if (m.offsets != nullptr) g_with_offsets.store(true, std::memory_order_relaxed);
   Mx4Params p = make_params(m, ldo, num_sms);
   p.out = out;
-  return dispatch(dtype, m.format, alignment(out, ldo, dtype), [&](auto t, auto fmt, auto align) {
-    return launch_dependent(mx4_dequantize_kernel<decltype(t), fmt.value, align.value>, dim3(grid_of(p.units, num_sms)),
-                            dim3(kThreads), starts_bytes(m), stream, p);
+  const bool groups = m.offsets != nullptr;
+  return dispatch(dtype, m.format, alignment(out, ldo, dtype), groups, [&](auto t, auto fmt, auto align, auto ragged) {
+    return launch_dependent(mx4_dequantize_kernel<decltype(t), fmt.value, align.value, ragged.value>,
+                            dim3(grid_of(p.units, num_sms)), dim3(kThreads), starts_bytes(m), stream, p);
   });
 }
 
