@@ -20,12 +20,13 @@
 //
 // Both ways are bound by HBM and, for 16-bit types, nearly as much by their
 // instructions (about 150 per 512 elements and warp).  Measured on a GB300,
-// 16384 x 8192: bf16 to NVFP4 60.6 us (5.7 TB/s; 51 at the measured 6.68), to
-// MXFP4 57 us, fp32 89 us (6.8 TB/s), back to bf16 58 us (5.9 TB/s); rows that
-// are only 4-byte aligned 81 us.  What counted: a lane's 32 bytes in one access
+// 16384 x 8192: bf16 to NVFP4 58.6 us (5.9 TB/s; 51 at the measured 6.68), to
+// MXFP4 56 us, fp32 88 us (6.9 TB/s), FP64 236 us (4.9 TB/s), back to bf16 59 us (5.9 TB/s), to FP64 225; rows that are only 4-byte
+// aligned 81 us.  What counted: a lane's 32 bytes in one access
 // (two of 16 touch every sector twice; dequantise 74 -> 59 us), the maximum two
 // elements at a time and arithmetic on pairs, quotients without a division
-// (66.5 -> 60.6 us with the loop unrolled).
+// (66.5 -> 60.6 us with the loop unrolled), no search for a row's group where
+// there are no offsets (-> 58.6).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

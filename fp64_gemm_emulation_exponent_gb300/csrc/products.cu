@@ -24,13 +24,13 @@
 //
 // Measured on a GB300 (CUDA events around graph replays; rates against the
 // measured 1852 TFLOP/s bf16 and 6.68 TB/s):
-//   8 groups of 2048 rows, 4096 x 4096, bf16: 290 us forward, 288 us dx, 281 us
-//     dw, 1.90-1.95 PFLOP/s, bound by the MMAs (516 cycles a stage of 512)
-//   8192^3 NVFP4: 150 us, 7.3 PFLOP/s, 0.99 of four times the bf16 rate; a stage
+//   8 groups of 2048 rows, 4096 x 4096, bf16: 288 us forward, 287 us dx, 278 us
+//     dw, 1.91-1.98 PFLOP/s, bound by the MMAs (516 cycles a stage of 512)
+//   8192^3 NVFP4: 150-154 us, 7.2 PFLOP/s, 0.97 of four times the bf16 rate; a stage
 //     of 38 KB an SM takes 525 cycles to arrive, its MMAs 512
-//   8192 rows over 16 groups, 4096 -> 2048, bf16: 96 us, 1.42 PFLOP/s; the
+//   8192 rows over 16 groups, 4096 -> 2048, bf16: 97 us, 1.42 PFLOP/s; the
 //     weights are read for two tiles of rows only, HBM and MMAs about even
-//   1 x 8192 x 4096 NVFP4: 5.4 us, 2.1 of them a launch with nothing to do; one
+//   1 x 8192 x 4096 NVFP4: 5.9 us, 2.1 of them a launch with nothing to do; one
 //     SM takes in 64-74 bytes a cycle, and the 64 tiles are on 64 SMs
 // What did not help: prefetching the next tile's operands into L2 by TMA (10-20%
 // slower: the copies' requests are what is short) or the weights' lines by an
@@ -421,8 +421,8 @@ __device__ __forceinline__ void store_block(T* out, int64_t ldo, int rows, bool 
 // accumulator row, pairs of output rows pack into a register, and stmatrix
 // writes the 8 x 8 pieces transposed.  The four warps that hold the tile's 128
 // output columns of these rows put them together in shared memory (two halves
-// of 64 columns, 128-byte rows, swizzled), and whole blocks leave by TMA
-// stores, full lines that no warp waits for: stored by the warps, in rows of 64
+// of 64 columns, 128-byte rows, swizzled), and whole blocks that end on 16
+// bytes leave by TMA stores, full lines that no warp waits for: stored by the warps, in rows of 64
 // bytes, a block took 535 cycles of its 820 (8192^2 x 1024 NVFP4 37.1 -> 35.3
 // us, 8192^3 151.7 -> 149.7; a token's product 0.1 us slower).
 __device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&v)[16]) {
@@ -452,8 +452,7 @@ __device__ __forceinline__ uint32_t pack16(uint32_t lo, uint32_t hi, float alpha
 }
 // This warp's 32 x 32 values into the block of its four warps (quad: which
 // quarter of the 128 columns).
-constexpr uint32_t kOutHalf = 32 * 128;       // 64 columns of 32 rows
-constexpr uint32_t kOutBlock = 2 * kOutHalf;  // 8 KB
+constexpr uint32_t kOutHalf = 32 * 128;  // 64 columns of 32 rows
 __device__ __forceinline__ uint32_t out_piece(int n, int chunk) {  // 16-byte piece `chunk` (0..15) of row n
   return static_cast<uint32_t>((chunk >> 3) * static_cast<int>(kOutHalf) + n * 128 + (((chunk & 7) ^ (n & 7)) * 16));
 }
@@ -1155,11 +1154,12 @@ cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
 // stage takes about 330 cycles (4-bit 400) to issue however few its rows; with
 // full tiles a pair's takes the 540 (550) of its MMAs and copies, a CTA's the
 // 450 (510) that 32 (36) KB take from L2 with every SM loading.  Over 48
-// sizes of all the operations, up to 8192 rows in 1 to 32 groups, the choice is
-// 0.2% slower than the better of the two, pairs alone 17%, single CTAs alone
-// 3%, and more where it counts: 8192^3 NVFP4 155 and 233 us; 16 groups of ~512 rows, 4096 -> 2048
-// bf16, 96 and 117; but 1000 x 1537 x 2090 MXFP4 11.2 and 7.2, and 32 rows in
-// 32 groups, 4096 -> 2048 NVFP4, 21.7 and 19.6.
+// sizes of all the operations, up to 8192 rows in 1 to 32 groups, the choice
+// takes as long as the better of the two (within 0.2%), pairs alone 15% longer,
+// single CTAs alone 5%, and more where it counts (pairs and single): 8192^3
+// NVFP4 154 and 234 us; 16 groups of 512 rows, 4096 -> 2048 bf16, 92 and 108;
+// but 1000 x 1537 x 2090 MXFP4 to fp32 8.2 and 6.2, and 32 rows in 32 groups,
+// 4096 -> 2048 NVFP4, 30.0 and 28.5.
 template <ProductOp OP, int FMT>
 cudaError_t choose(const Product& q, int num_sms, cudaStream_t stream) {
   const bool mx = OP == kMx4, sum_rows = OP == kGradWeights;
