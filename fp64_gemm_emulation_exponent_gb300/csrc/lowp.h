@@ -57,4 +57,25 @@ cudaError_t launch_product(const Product& q, int num_sms, cudaStream_t stream);
 void withhold_next_product(int pairs, int cta, int kblock, uint32_t timeout_us);  // test hook, see ozk.h
 int take_product_status(int* status);  // the stream is idle; bit 0: a wait ran out, bit 1: bad group offsets
 
+
+// A few 16-bit rows times 4-bit weights (w: groups equal groups of N rows,
+// gated 2 N): y[t, n] = alpha sum_k x[t, k] w[g(t)][n, k], or act of it times
+// that of row N + n.
+struct Gemv {
+  int64_t T, N, K;
+  const int32_t* offsets;  // device, w.groups + 1; null: one group of T rows
+  const void* x;
+  int64_t ldx;
+  int dtype;
+  Mx4Matrix w;
+  float alpha;
+  bool gated;
+  int act;
+  void* y;
+  int64_t ldy;
+  int out_type;
+};
+cudaError_t launch_mx4_gemv(const Gemv& q, int num_sms, cudaStream_t stream);
+int take_gemv_status(int* status);  // the stream is idle; bit 1: bad group offsets
+
 }  // namespace ozk

@@ -77,6 +77,43 @@ int check_weights(const void* w, int64_t N, int64_t K, int64_t ldw, int groups, 
   return OZK_OK;
 }
 
+bool known_activation(int a) { return a >= OZK_SILU && a <= OZK_GELU_TANH; }
+
+// A few 16-bit rows times 4-bit weights, plain or gated.
+int gemv(int64_t T, int64_t N, int64_t K, int groups, const int32_t* offsets, const void* X, int64_t ldx, int dtype,
+         const uint8_t* codes, const uint8_t* scales, int format, float alpha, bool gated, int act, void* Y, int64_t ldy,
+         int out_dtype, cudaStream_t stream) {
+  if (T < 0 || N < 0 || K < 0 || !known_format(format) || groups < 1) return OZK_ERR_INVALID_ARG;
+  if (offsets == nullptr && groups != 1) return OZK_ERR_INVALID_ARG;
+  if (gated && !known_activation(act)) return OZK_ERR_INVALID_ARG;
+  if (dtype != OZK_BF16 && dtype != OZK_F16) return OZK_ERR_UNSUPPORTED;
+  if (out_dtype != OZK_BF16 && out_dtype != OZK_F16 && out_dtype != OZK_F32) return OZK_ERR_UNSUPPORTED;
+  const int64_t per = gated ? 2 : 1;  // rows of w of an output column
+  if (T > kMaxRows || N > kMaxFeatures || K > kMaxFeatures || groups > kMaxGroups || per * N > kMaxRows / groups)
+    return OZK_ERR_UNSUPPORTED;
+  if (T == 0 || N == 0) return OZK_OK;
+  if (!Y || ldy < N || reinterpret_cast<uintptr_t>(Y) % size_of(out_dtype) != 0) return OZK_ERR_INVALID_ARG;
+  const int64_t rows = per * N * groups;
+  if (K > 0) {
+    if (!X || ldx < K || reinterpret_cast<uintptr_t>(X) % 2 != 0) return OZK_ERR_INVALID_ARG;
+    if (!codes || !scales || !aligned16(codes) || !aligned16(scales)) return OZK_ERR_INVALID_ARG;
+    const Span y = span(Y, T, N, ldy, size_of(out_dtype));
+    if (overlap(y, span(X, T, K, ldx, 2)) || overlap(y, span(codes, 1, rows * (ozk_kpad(K) / 2), 0, 1)) ||
+        overlap(y, span(scales, 1, static_cast<int64_t>(ozk_mx4_scale_bytes(rows, K, format, groups)), 0, 1)))
+      return OZK_ERR_INVALID_ARG;
+  }
+  int sms = 0;
+  const int rc = current_device_supported(&sms);
+  if (rc) return rc;
+  const Gemv q = {T, N, K, offsets, X, ldx, dtype, matrix(rows, K, format, nullptr, groups, codes, scales), alpha, gated,
+                  act, Y, ldy, out_dtype};
+  try {  // the launcher's table may allocate; nothing is thrown across the C boundary
+    return launch_mx4_gemv(q, sms, stream) == cudaSuccess ? OZK_OK : OZK_ERR_CUDA;
+  } catch (...) {
+    return OZK_ERR_CUDA;
+  }
+}
+
 }  // namespace
 }  // namespace ozk
 
@@ -174,6 +211,20 @@ int ozk_mx4_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a_codes, const 
                  int out_dtype, ozk_stream_t stream) {
   return ozk_mx4_grouped_gemm(M, N, K, 1, nullptr, a_codes, a_scales, b_codes, b_scales, format, alpha, C, ldc,
                               out_dtype, stream);
+}
+
+int ozk_mx4_gemv(int64_t T, int64_t N, int64_t K, int groups, const int32_t* offsets, const void* X, int64_t ldx,
+                 int dtype, const uint8_t* w_codes, const uint8_t* w_scales, int format, float alpha, void* Y,
+                 int64_t ldy, int out_dtype, ozk_stream_t stream) {
+  return gemv(T, N, K, groups, offsets, X, ldx, dtype, w_codes, w_scales, format, alpha, false, OZK_SILU, Y, ldy,
+              out_dtype, stream);
+}
+
+int ozk_mx4_gated_gemv(int64_t T, int64_t N, int64_t K, int groups, const int32_t* offsets, const void* X, int64_t ldx,
+                       int dtype, const uint8_t* w_codes, const uint8_t* w_scales, int format, float alpha,
+                       int activation, void* Y, int64_t ldy, int out_dtype, ozk_stream_t stream) {
+  return gemv(T, N, K, groups, offsets, X, ldx, dtype, w_codes, w_scales, format, alpha, true, activation, Y, ldy,
+              out_dtype, stream);
 }
 
 int ozk_grouped_gemm(int64_t T, int64_t N, int64_t K, int groups, const int32_t* offsets, const void* X, int64_t ldx,

@@ -29,6 +29,7 @@ OZK_SCALE_NOALLOC_MAX = 262144
 OZK_MAX_GROUPS = 1024
 OZK_BF16, OZK_F16, OZK_F32, OZK_F64 = 0, 1, 2, 3
 OZK_NVFP4, OZK_MXFP4 = 0, 1
+OZK_SILU, OZK_GELU, OZK_GELU_TANH = 0, 1, 2
 
 _i64, _i32, _vp, _sz = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
 _f32 = ctypes.c_float
@@ -74,6 +75,9 @@ SIGNATURES = {
                                    _vp]),
     "ozk_grouped_gemm_dw": (_i32, [_i64, _i64, _i64, _i32, _vp, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _i64, _i32,
                                    _vp]),
+    "ozk_mx4_gemv": (_i32, [_i64, _i64, _i64, _i32, _vp, _vp, _i64, _i32, _vp, _vp, _i32, _f32, _vp, _i64, _i32, _vp]),
+    "ozk_mx4_gated_gemv": (_i32, [_i64, _i64, _i64, _i32, _vp, _vp, _i64, _i32, _vp, _vp, _i32, _f32, _i32, _vp, _i64,
+                                  _i32, _vp]),
     "ozk_withhold_next_product": (_i32, [_i32, _i32, _i32, ctypes.c_uint32]),
     "ozk_event_create": (_i32, [_vp]),
     "ozk_event_destroy": (_i32, [_vp]),
@@ -618,6 +622,64 @@ def mx4_grouped_gemm(x: Mx4, w: Mx4, alpha: float = 1.0, out_dtype=None, out=Non
     if rc:
         raise OzkError("ozk_mx4_grouped_gemm", rc)
     return out
+
+
+_ACTIVATIONS = {"silu": OZK_SILU, "gelu": OZK_GELU, "gelu_tanh": OZK_GELU_TANH}
+
+
+def _activation(name):
+    try:
+        return _ACTIVATIONS[name]
+    except KeyError:
+        raise ValueError(f"unknown activation {name!r} (silu, gelu, gelu_tanh)") from None
+
+
+def _few_rows(name, x, w, offsets, per, act, alpha, out_dtype, out, stream):
+    """mx4_gemv and mx4_gated_gemv: `per` rows of w to an output column, act the arguments of the gated one."""
+    index = _device_index(x)
+    if w._index != index:
+        raise ValueError(f"operands on cuda:{index} and cuda:{w._index}")
+    if w.offsets is not None:
+        raise ValueError("weights in equal groups are expected")
+    if offsets is None:
+        if w.groups != 1:
+            raise ValueError(f"offsets are needed for weights of {w.groups} groups")
+    elif _offsets(offsets, index) != w.groups:
+        raise ValueError(f"offsets of {offsets.shape[0] - 1} groups, weights of {w.groups}")
+    (T, K, ldx), N = _rows(x), w.rows // (w.groups * per)
+    if K != w.K or N * per * w.groups != w.rows:
+        raise ValueError(f"x is {tuple(x.shape)}, the weights {w.rows} x {w.K} in {w.groups} groups")
+    if out_dtype is None and out is None:
+        out_dtype = x.dtype
+    out, ld, kind = _result(out, T, N, out_dtype, x.device, stream)
+    rc = getattr(_lib, name)(T, N, K, w.groups, None if offsets is None else offsets.data_ptr(), x.data_ptr(), ldx,
+                             _dtype(x.dtype), w._codes, w._scales, _FORMATS[w.fmt], alpha, *act, out.data_ptr(), ld, kind,
+                             _stream_at(index, stream))
+    if rc:
+        raise OzkError(name, rc)
+    return out
+
+
+def mx4_gemv(x, w: Mx4, offsets=None, alpha: float = 1.0, out_dtype=None, out=None, stream=None):
+    """alpha * x_t @ w_g(t)^T for a few rows of 16-bit x, not quantised
+    (ozk_mx4_gemv): x [T, K] bf16 or fp16, w a matrix of one group, or from a
+    [groups, N, K] tensor with offsets for the rows of x; [T, N] of out_dtype
+    (default x's).  Rows in no group are not written."""
+    if w._index != _current_device():
+        with _torch.cuda.device(w._index):
+            return mx4_gemv(x, w, offsets, alpha, out_dtype, out, stream)
+    return _few_rows("ozk_mx4_gemv", x, w, offsets, 1, (), alpha, out_dtype, out, stream)
+
+
+def mx4_gated_gemv(x, w: Mx4, offsets=None, activation: str = "silu", alpha: float = 1.0, out_dtype=None, out=None,
+                   stream=None):
+    """act(g) * u for a few rows of 16-bit x (ozk_mx4_gated_gemv): w holds 2 H
+    rows per group, the gate's first, g = alpha * x_t @ w_g(t)[:H]^T and u the
+    same with w_g(t)[H:]; activation "silu", "gelu" or "gelu_tanh"; [T, H]."""
+    if w._index != _current_device():
+        with _torch.cuda.device(w._index):
+            return mx4_gated_gemv(x, w, offsets, activation, alpha, out_dtype, out, stream)
+    return _few_rows("ozk_mx4_gated_gemv", x, w, offsets, 2, (_activation(activation),), alpha, out_dtype, out, stream)
 
 
 def _grouped(first, second, offsets, groups):

@@ -436,6 +436,31 @@ int ozk_mx4_grouped_gemm(int64_t T, int64_t N, int64_t K, int groups, const int3
                          const uint8_t* x_scales, const uint8_t* w_codes, const uint8_t* w_scales, int format,
                          float alpha, void* Y, int64_t ldy, int out_dtype, ozk_stream_t stream);
 
+/* Activations of the gated products: g / (1 + e^-g); g times the normal
+ * distribution function of g; and its approximation g (1 + tanh z) / 2 with
+ * z = sqrt(2 / pi) (g + 0.044715 g^3). */
+typedef enum { OZK_SILU = 0, OZK_GELU = 1, OZK_GELU_TANH = 2 } ozk_activation;
+
+/* Y[t, j] = alpha * sum_k x_tk w_g(t),j,k for a few rows: X is T x K of dtype
+ * OZK_BF16 or OZK_F16, as it is (not quantised), any alignment of its type; w
+ * as in ozk_mx4_grouped_gemm.  offsets as there, or NULL for one group.  Any T
+ * is taken; the weights are read once for every 8 to 32 rows of a group, so
+ * that past some 32 quantised rows and ozk_mx4_grouped_gemm are faster.  Y: T x
+ * N of OZK_BF16, OZK_F16 or OZK_F32, ldy >= N, any alignment of its own type;
+ * it must overlap nothing.  x is used exactly, whatever its range; sums are
+ * formed in fp32 (with MXFP4 scales above 2^100 one may overflow where its
+ * result would not).  K = 0 gives zeros. */
+int ozk_mx4_gemv(int64_t T, int64_t N, int64_t K, int groups, const int32_t* offsets, const void* X, int64_t ldx,
+                 int dtype, const uint8_t* w_codes, const uint8_t* w_scales, int format, float alpha, void* Y,
+                 int64_t ldy, int out_dtype, ozk_stream_t stream);
+
+/* The gated form: w has 2 N rows per group, the gate's first, and
+ * Y[t, j] = act(g) u with g = alpha * sum_k x_tk w_g(t),j,k and u the same with
+ * row N + j; g and u stay in fp32. */
+int ozk_mx4_gated_gemv(int64_t T, int64_t N, int64_t K, int groups, const int32_t* offsets, const void* X, int64_t ldx,
+                       int dtype, const uint8_t* w_codes, const uint8_t* w_scales, int format, float alpha,
+                       int activation, void* Y, int64_t ldy, int out_dtype, ozk_stream_t stream);
+
 /* Y[t, j] = sum_k x_tk w_g(t),j,k for 16-bit operands (dtype OZK_BF16 or
  * OZK_F16): X is T x K, W holds one N x K matrix per group, w_stride elements
  * apart, Y is T x N of dtype or OZK_F32.  X and W are read by bulk tensor
