@@ -17,7 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libozk.so")
 SOURCES = ["ozk_api.cu", "scan_quantize.cu", "residue_gemm.cu", "crt_combine.cu", "crt_fixed.cu",
-           "mx4_quantize.cu", "products.cu", "gemv.cu", "lowp_api.cu"]
+           "mx4_quantize.cu", "products.cu", "gemv.cu", "gated_grad.cu", "lowp_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,158 @@
+// The gradient of a gated product with respect to its two projections:
+//   dpre[t, m] = dh[t, m] s0[t, m],   dpre[t, M + m] = dh[t, m] s1[t, m],
+// s0 = dh/dgate = u act'(g) and s1 = dh/dup = act(g) as the forward product
+// stored them, so no exponential is taken here and the activation is not
+// known.  Each product is rounded once (two 16-bit factors are exact in fp32).
+//
+// Five elements move for one of dh: bound by HBM, 10 T M bytes.  A warp takes a
+// row's run of up to 1024 columns with 16-byte accesses, all three loads of four
+// vectors ahead of the stores.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "lowp.h"
+
+namespace ozk {
+namespace {
+
+__device__ int g_gated_status;  // bit 1: bad group offsets
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kUnroll = 4;
+constexpr int kRun = 32 * 8 * kUnroll;  // columns of a unit
+
+struct GradParams {
+  int64_t lddh, lds, plane, ldo;
+  int T, M, groups, runs;  // runs: units of a row
+  FastDiv div_runs;
+  const int32_t* offsets;
+  const uint16_t *dh, *slopes;
+  uint16_t* out;
+};
+
+// The rows of the groups: they follow one another from the first offset to the
+// largest, cut to [0, T].
+__device__ __forceinline__ int2 rows_of(const GradParams& p) {
+  const int lane = threadIdx.x & 31;
+  int most = 0;
+  bool bad = false;
+  for (int i = lane; i <= p.groups; i += 32) {
+    const int at = p.offsets[i];
+    most = max(most, at);
+    if (blockIdx.x == 0) bad |= at < (i ? p.offsets[i - 1] : 0) || at > p.T;
+  }
+  most = min(static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, most)), p.T);
+  if (blockIdx.x == 0 && __any_sync(0xFFFFFFFFu, bad) && threadIdx.x == 0) atomicOr(&g_gated_status, 2);
+  return {min(max(p.offsets[0], 0), p.T), most};
+}
+
+template <bool BF>
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (BF) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <bool BF>
+__device__ __forceinline__ uint4 mul8(uint4 a, uint4 b) {
+  return make_uint4(mul2<BF>(a.x, b.x), mul2<BF>(a.y, b.y), mul2<BF>(a.z, b.z), mul2<BF>(a.w, b.w));
+}
+__device__ __forceinline__ uint4 load16(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+
+// VEC: rows and halves of dpre that start on 16 bytes; else element by element.
+template <bool BF, bool VEC>
+__global__ void __launch_bounds__(kThreads) gated_grad_kernel(const GradParams p) {
+  grid_dependency_sync();
+  const int lane = threadIdx.x & 31;
+  const int2 span = p.offsets ? rows_of(p) : make_int2(0, p.T);
+  const int64_t units = static_cast<int64_t>(span.y - span.x) * p.runs;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); u < units;
+       u += static_cast<int64_t>(gridDim.x) * kWarps) {
+    int64_t row;
+    if (u < (int64_t{1} << 31)) row = div_fast(static_cast<uint32_t>(u), p.div_runs);
+    else row = u / p.runs;
+    const int c0 = static_cast<int>(u - row * p.runs) * kRun;
+    row += span.x;
+    const uint16_t *dh = p.dh + row * p.lddh, *s0 = p.slopes + row * p.lds, *s1 = s0 + p.plane;
+    uint16_t *o0 = p.out + row * p.ldo, *o1 = o0 + p.M;
+    if (VEC) {
+      uint4 d[kUnroll], a[kUnroll], b[kUnroll];
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i) {
+        const int c = c0 + (i * 32 + lane) * 8;
+        if (c >= p.M) continue;
+        d[i] = load16(dh + c);
+        a[i] = load16(s0 + c);
+        b[i] = load16(s1 + c);
+      }
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i) {
+        const int c = c0 + (i * 32 + lane) * 8;
+        if (c >= p.M) continue;
+        *reinterpret_cast<uint4*>(o0 + c) = mul8<BF>(d[i], a[i]);
+        *reinterpret_cast<uint4*>(o1 + c) = mul8<BF>(d[i], b[i]);
+      }
+    } else {
+      const int end = min(c0 + kRun, p.M);
+      for (int c = c0 + lane; c < end; c += 32) {
+        const uint32_t d = dh[c];
+        o0[c] = static_cast<uint16_t>(mul2<BF>(d, s0[c]));
+        o1[c] = static_cast<uint16_t>(mul2<BF>(d, s1[c]));
+      }
+    }
+  }
+}
+
+std::atomic<bool> g_any{false};
+
+}  // namespace
+
+cudaError_t launch_gated_grad(const GatedGrad& q, int num_sms, cudaStream_t stream) {
+  g_any.store(true, std::memory_order_relaxed);
+  GradParams p = {};
+  p.lddh = q.lddh;
+  p.lds = q.lds;
+  p.plane = q.slope_plane;
+  p.ldo = q.ldo;
+  p.T = static_cast<int>(q.T);
+  p.M = static_cast<int>(q.M);
+  p.groups = q.groups;
+  p.runs = static_cast<int>((q.M + kRun - 1) / kRun);
+  p.div_runs = fast_div(p.runs);
+  p.offsets = q.offsets;
+  p.dh = static_cast<const uint16_t*>(q.dh);
+  p.slopes = static_cast<const uint16_t*>(q.slopes);
+  p.out = static_cast<uint16_t*>(q.out);
+  auto aligned = [](const void* a) { return reinterpret_cast<uintptr_t>(a) % 16 == 0; };
+  const bool vec = aligned(q.dh) && aligned(q.slopes) && aligned(q.out) && q.M % 8 == 0 && (q.T == 1 || q.lddh % 8 == 0) &&
+                   (q.T == 1 || q.lds % 8 == 0) && q.slope_plane % 8 == 0 && (q.T == 1 || q.ldo % 8 == 0);
+  const int64_t units = q.T * p.runs;
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>((units + kWarps - 1) / kWarps, 8 * num_sms)));
+  const bool bf = q.dtype == OZK_BF16;
+  auto kernel = bf ? (vec ? gated_grad_kernel<true, true> : gated_grad_kernel<true, false>)
+                   : (vec ? gated_grad_kernel<false, true> : gated_grad_kernel<false, false>);
+  return launch_dependent(kernel, grid, dim3(kThreads), 0, stream, p);
+}
+
+int take_gated_status(int* status) {
+  *status = 0;
+  if (!g_any.load(std::memory_order_relaxed)) return OZK_OK;
+  int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_gated_status, sizeof(int)) != cudaSuccess) return OZK_ERR_CUDA;
+  if (v) {
+    const int zero = 0;
+    if (cudaMemcpyToSymbol(g_gated_status, &zero, sizeof(int)) != cudaSuccess) return OZK_ERR_CUDA;
+  }
+  *status = v;
+  return OZK_OK;
+}
+
+}  // namespace ozk

@@ -34,8 +34,10 @@ int take_mx4_status(int* status);  // the stream is idle; bit 1: bad group offse
 // The products.  kForward: out[t, m] = sum_k x[t, k] w[e][m, k]; kGradRows:
 // out[t, m] = sum_k dy[t, k] w[e][k, m]; kGradWeights: out[e][n, m] =
 // sum over the rows t of group e of dy[t, n] x[t, m]; kMx4: kForward on 4-bit
-// operands, times alpha.
-enum ProductOp { kForward = 0, kGradRows = 1, kGradWeights = 2, kMx4 = 3 };
+// operands, times alpha; kGated: out[t, m] = act(g) u with g the kForward
+// product with row m of w[e] (2 M rows) and u that with row M + m, and where
+// slopes is given its derivatives by g, u act'(g), and by u, act(g).
+enum ProductOp { kForward = 0, kGradRows = 1, kGradWeights = 2, kMx4 = 3, kGated = 4 };
 struct Product {
   ProductOp op;
   int dtype;                  // of the 16-bit operands
@@ -52,7 +54,24 @@ struct Product {
   int64_t ldo, out_group;
   Mx4Matrix a, b;             // kMx4: rows and weights
   float alpha;
+  int act;                    // kGated
+  void* slopes;               // [2][T][M], rows lds and the two slope_plane elements apart; or null
+  int64_t lds, slope_plane;
 };
+// dpre[t, m] = dh[t, m] slopes[0][t, m], dpre[t, M + m] = dh[t, m] slopes[1][t, m]
+// for the rows of the groups (offsets null: all T rows).
+struct GatedGrad {
+  int64_t T, M;
+  int groups;
+  const int32_t* offsets;
+  int dtype;
+  const void *dh, *slopes;
+  int64_t lddh, lds, slope_plane;
+  void* out;
+  int64_t ldo;
+};
+cudaError_t launch_gated_grad(const GatedGrad& q, int num_sms, cudaStream_t stream);
+int take_gated_status(int* status);  // the stream is idle; bit 1: bad group offsets
 cudaError_t launch_product(const Product& q, int num_sms, cudaStream_t stream);
 void withhold_next_product(int pairs, int cta, int kblock, uint32_t timeout_us);  // test hook, see ozk.h
 int take_product_status(int* status);  // the stream is idle; bit 0: a wait ran out, bit 1: bad group offsets

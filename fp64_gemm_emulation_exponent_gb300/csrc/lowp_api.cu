@@ -43,7 +43,7 @@ Mx4Matrix matrix(int64_t rows, int64_t K, int format, const int32_t* offsets, in
 }
 
 int run(const Product& q, cudaStream_t stream, int sms) {
-  const int64_t tiles_m = (q.M + 127) / 128;
+  const int64_t tiles_m = ((q.op == kGated ? 2 * q.M : q.M) + 127) / 128;
   const int64_t tiles_n = q.op == kGradWeights ? ((q.N + 127) / 128) * q.groups : q.T / 128 + q.groups;
   if (tiles_m > 0 && tiles_n > kMaxTiles / tiles_m) return OZK_ERR_UNSUPPORTED;
   try {  // the launcher's tables may allocate; nothing is thrown across the C boundary
@@ -78,6 +78,12 @@ int check_weights(const void* w, int64_t N, int64_t K, int64_t ldw, int groups, 
 }
 
 bool known_activation(int a) { return a >= OZK_SILU && a <= OZK_GELU_TANH; }
+
+// The two slopes of a gated product: rows of N elements, lds apart, `plane` between the two.
+int check_slopes(const void* s, int64_t T, int64_t N, int64_t lds, int64_t plane) {
+  if (!s || reinterpret_cast<uintptr_t>(s) % 2 != 0 || lds < N || plane < (T - 1) * lds + N) return OZK_ERR_INVALID_ARG;
+  return OZK_OK;
+}
 
 // A few 16-bit rows times 4-bit weights, plain or gated.
 int gemv(int64_t T, int64_t N, int64_t K, int groups, const int32_t* offsets, const void* X, int64_t ldx, int dtype,
@@ -260,6 +266,72 @@ int ozk_grouped_gemm(int64_t T, int64_t N, int64_t K, int groups, const int32_t*
   int sms = 0;
   rc = current_device_supported(&sms);
   return rc ? rc : run(q, stream, sms);
+}
+
+int ozk_grouped_gated_gemm(int64_t T, int64_t N, int64_t K, int groups, const int32_t* offsets, const void* X,
+                           int64_t ldx, const void* W, int64_t ldw, int64_t w_stride, int dtype, int activation,
+                           void* Y, int64_t ldy, void* slopes, int64_t lds, int64_t slope_stride,
+                           ozk_stream_t stream) {
+  int rc = check_grouped(T, N, K, groups, offsets, dtype, dtype);
+  if (rc) return rc;
+  if (!known_activation(activation)) return OZK_ERR_INVALID_ARG;
+  if (2 * N > kMaxFeatures) return OZK_ERR_UNSUPPORTED;
+  if (T == 0 || N == 0) return OZK_OK;
+  if (!Y || ldy < N || reinterpret_cast<uintptr_t>(Y) % 2 != 0) return OZK_ERR_INVALID_ARG;
+  const Span y = span(Y, T, N, ldy, 2), s = span(slopes, T, N, lds, 2, 2, slope_stride);
+  if (slopes) {
+    if ((rc = check_slopes(slopes, T, N, lds, slope_stride))) return rc;
+    if (overlap(y, s)) return OZK_ERR_INVALID_ARG;
+  }
+  if (K > 0) {
+    if ((rc = check_operand(X, K, ldx)) || (rc = check_weights(W, 2 * N, K, ldw, groups, w_stride))) return rc;
+    const Span x = span(X, T, K, ldx, 2), w = span(W, 2 * N, K, ldw, 2, groups, w_stride);
+    if (overlap(y, x) || overlap(y, w) || (slopes && (overlap(s, x) || overlap(s, w)))) return OZK_ERR_INVALID_ARG;
+  }
+  Product q = {};
+  q.op = kGated;
+  q.dtype = dtype;
+  q.out_type = dtype;
+  q.T = T;
+  q.M = N;
+  q.K = K;
+  q.groups = groups;
+  q.offsets = offsets;
+  q.rows = X;
+  q.ld_rows = ldx;
+  q.other = W;
+  q.ld_other = ldw;
+  q.other_group = groups > 1 ? w_stride : 2 * N * ldw;
+  q.out = Y;
+  q.ldo = ldy;
+  q.alpha = 1.0f;
+  q.act = activation;
+  q.slopes = slopes;
+  q.lds = lds;
+  q.slope_plane = slope_stride;
+  int sms = 0;
+  rc = current_device_supported(&sms);
+  return rc ? rc : run(q, stream, sms);
+}
+
+int ozk_gated_grad(int64_t T, int64_t N, int groups, const int32_t* offsets, const void* dH, int64_t lddh,
+                   const void* slopes, int64_t lds, int64_t slope_stride, int dtype, void* dpre, int64_t ldp,
+                   ozk_stream_t stream) {
+  if (T < 0 || N < 0 || groups < 1 || (offsets == nullptr && groups != 1)) return OZK_ERR_INVALID_ARG;
+  if (dtype != OZK_BF16 && dtype != OZK_F16) return OZK_ERR_UNSUPPORTED;
+  if (T > kMaxRows || 2 * N > kMaxFeatures || groups > kMaxGroups) return OZK_ERR_UNSUPPORTED;
+  if (T == 0 || N == 0) return OZK_OK;
+  if (!dH || lddh < N || reinterpret_cast<uintptr_t>(dH) % 2 != 0) return OZK_ERR_INVALID_ARG;
+  if (!dpre || ldp < 2 * N || reinterpret_cast<uintptr_t>(dpre) % 2 != 0) return OZK_ERR_INVALID_ARG;
+  int rc = check_slopes(slopes, T, N, lds, slope_stride);
+  if (rc) return rc;
+  const Span d = span(dpre, T, 2 * N, ldp, 2);
+  if (overlap(d, span(dH, T, N, lddh, 2)) || overlap(d, span(slopes, T, N, lds, 2, 2, slope_stride)))
+    return OZK_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((rc = current_device_supported(&sms))) return rc;
+  const GatedGrad q = {T, N, groups, offsets, dtype, dH, slopes, lddh, lds, slope_stride, dpre, ldp};
+  return launch_gated_grad(q, sms, stream) == cudaSuccess ? OZK_OK : OZK_ERR_CUDA;
 }
 
 int ozk_grouped_gemm_dx(int64_t T, int64_t N, int64_t K, int groups, const int32_t* offsets, const void* dY,

@@ -784,11 +784,12 @@ int ozk_stream_status(ozk_stream_t stream) {
   int status = 0;
   int rc = take_device_status(reinterpret_cast<cudaStream_t>(stream), &status);
   if (rc) return rc;
-  int products = 0, matrices = 0, rows = 0;
-  if ((rc = take_product_status(&products)) || (rc = take_mx4_status(&matrices)) || (rc = take_gemv_status(&rows)))
+  int products = 0, matrices = 0, rows = 0, gated = 0;
+  if ((rc = take_product_status(&products)) || (rc = take_mx4_status(&matrices)) || (rc = take_gemv_status(&rows)) ||
+      (rc = take_gated_status(&gated)))
     return rc;
   if (status || (products & 1)) return OZK_ERR_TIMEOUT;
-  return products || matrices || rows ? OZK_ERR_INVALID_ARG : OZK_OK;
+  return products || matrices || rows || gated ? OZK_ERR_INVALID_ARG : OZK_OK;
 }
 
 int ozk_release_cached(void) {

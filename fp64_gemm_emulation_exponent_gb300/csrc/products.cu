@@ -12,6 +12,10 @@
 //   gradient of x    out[t, m] = sum_k dy[t, k] w[e][k, m]    w M-major
 //   gradient of w    out[e][n, m] = sum_t dy[t, n] x[t, m]    both MN-major,
 //                    the group's rows are the reduction
+//   gated            out[t, m] = act(g) u, g = sum_k x[t, k] w[e][m, k], u the
+//                    same with row M + m: the forward product with rows m and
+//                    M + m of w laid 16 by 16 into a tile, so that a thread of
+//                    the epilogue holds both of an output
 // The MN-major operands are read as they lie (tcgen05's transposed operand
 // form), nothing is transposed in memory.
 //
@@ -48,6 +52,7 @@
 #include <map>
 #include <mutex>
 
+#include "activation.cuh"
 #include "lowp.h"
 #include "tc_ptx.cuh"
 
@@ -75,6 +80,8 @@ struct Config {
   static constexpr bool PAIR = PAIR_;
   static constexpr int BN = BN_;
   static constexpr bool MX = OP == kMx4;
+  static constexpr bool GATED = OP == kGated;
+  static constexpr int COLS = GATED ? kTileRows / 2 : kTileRows;  // output columns of a CTA
   // operands read across K: the weights of the gradient of x, both of the gradient of w
   static constexpr bool A_MN = OP == kGradRows || OP == kGradWeights;
   static constexpr bool B_MN = OP == kGradWeights;
@@ -91,7 +98,7 @@ struct Config {
   static constexpr uint32_t SFA_BYTES = MX ? KG * kScaleTile : 0;
   static constexpr uint32_t SFB_BYTES = MX ? NB * KG * kScaleTile : 0;
   static constexpr uint32_t STAGE = kABytes + B_BYTES + SFA_BYTES + SFB_BYTES;
-  static constexpr int STAGES = MX ? 5 : 6;
+  static constexpr int STAGES = MX || GATED ? 5 : 6;
   // Two accumulators and the scales in 512 TMEM columns: with 256-column
   // accumulators beside scales the two share their last and first columns
   // (48 or 24).  The epilogue takes those first, and the next tile's MMAs
@@ -105,7 +112,8 @@ struct Config {
   // full, empty, tail and peer tail per stage (the tails: gradient of w);
   // accumulator full and empty; drain
   static constexpr int BARS = (OP == kGradWeights ? 4 : 2) * STAGES + 5;
-  static constexpr uint32_t OUT_STAGE = 8192;  // of each side of the epilogue: 32 rows of 128 16-bit columns
+  // of each side of the epilogue: 32 rows of 128 16-bit columns; gated, of 64 and as many of both slopes
+  static constexpr uint32_t OUT_STAGE = GATED ? 12288 : 8192;
   static constexpr uint32_t CTRL = 384;  // barriers, TMEM address, abort flag; from 256 on the loaders' last issues
   static constexpr uint32_t FIXED = 1024 + STAGES * STAGE + 2 * OUT_STAGE + CTRL;
   static_assert(8 * BARS + 8 <= 256 && 256 + 2 * 8 * STAGES <= CTRL, "control words");
@@ -124,6 +132,10 @@ struct ProductParams {
   int64_t ldo, out_group;
   float alpha;
   bool vec;        // 16-byte stores: a 16-bit output whose rows are 16-byte aligned
+  void* slopes;    // gated: the result's two slopes, [2][T][M], or null
+  int64_t lds, slope_plane;
+  bool vec_slopes;
+  int act;
   uint64_t timeout_ns;  // limit of a pipeline wait: what a whole tile's stages may take, and 2 s
   int withhold_kb, withhold_cta;  // the stage that test runs withhold (of that CTA's first tile), or -1
   uint32_t idesc;  // types, majorness, M; N is filled in per tile
@@ -177,6 +189,22 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                                 uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
       : "memory");
 }
 
@@ -369,7 +397,7 @@ __device__ __forceinline__ Tile tile_at(const ProductParams& p, const Group* g, 
     n = div_fast(r, p.div_tail);
     m += r - n * (static_cast<unsigned>(p.tiles_m) % kSuper);
   }
-  t.m0 = static_cast<int>(m) * (kTileRows * C::CTAS);
+  t.m0 = static_cast<int>(m) * (C::COLS * C::CTAS);
   const int step = tile_rows<C, OP>(static_cast<int>(total_n));
   t.n0 = static_cast<int>(n) * step;
   t.n = min(step, static_cast<int>(total_n) - t.n0);
@@ -489,6 +517,76 @@ __device__ __forceinline__ void store_edge(uint16_t* out, int64_t ldo, int rows,
                  : "memory");
     uint16_t* dst = out + n * ldo + 8 * chunk;
     if (8 * chunk + 8 <= cols) {
+      *reinterpret_cast<uint4*>(dst) = w;
+    } else {
+      const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (8 * chunk + j < cols) dst[j] = static_cast<uint16_t>(e[j / 2] >> (16 * (j & 1)));
+    }
+  }
+}
+
+// ---- gated products ----
+// TMEM lanes 32 q .. + 15 are rows 16 q .. of the gate, the 16 lanes after them
+// the same rows of the other projection: read in the 16 x 256-bit form, a
+// thread has g and u of an output at the same place of two registers.  The
+// activation and the product are taken on the fp32 sums; what leaves is
+// rounded once.  Up to three blocks of 32 rows by 64 columns (the result, its
+// slopes by u and by g) go through shared memory as above.
+constexpr uint32_t kGatedBlock = 32 * 128;
+template <typename T>
+__device__ __forceinline__ void stage_gated(uint32_t block, int quad, int lane, const uint32_t (&v)[16]) {
+  const int piece = lane >> 3;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const uint32_t addr = block + out_piece(8 * (2 * q + (piece >> 1)) + (lane & 7), 2 * quad + (piece & 1));
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                 "r"(pack16<T>(v[8 * q], v[8 * q + 1], 1.0f)), "r"(pack16<T>(v[8 * q + 2], v[8 * q + 3], 1.0f)),
+                 "r"(pack16<T>(v[8 * q + 4], v[8 * q + 5], 1.0f)), "r"(pack16<T>(v[8 * q + 6], v[8 * q + 7], 1.0f))
+                 : "memory");
+  }
+}
+// act(g) u over g, and where asked for the slopes u act'(g) and act(g).
+template <int ACT>
+__device__ __forceinline__ void gate(uint32_t (&g)[16], uint32_t (&u)[16], bool slopes, uint32_t (&da)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float x = __uint_as_float(g[i]), y = __uint_as_float(u[i]);
+    const float p = act_p(x, ACT), a = x * p;
+    if (slopes) da[i] = __float_as_uint(y * act_slope(x, p, ACT));
+    g[i] = __float_as_uint(a * y);
+    u[i] = __float_as_uint(a);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void stage_gate(uint32_t block, int quad, int lane, uint32_t (&g)[16], uint32_t (&u)[16], bool slopes,
+                                           int act) {
+  uint32_t da[16] = {};
+  if (act == OZK_SILU) gate<OZK_SILU>(g, u, slopes, da);
+  else if (act == OZK_GELU) gate<OZK_GELU>(g, u, slopes, da);
+  else gate<OZK_GELU_TANH>(g, u, slopes, da);
+  stage_gated<T>(block, quad, lane, g);
+  if (slopes) {
+    stage_gated<T>(block + kGatedBlock, quad, lane, da);
+    stage_gated<T>(block + 2 * kGatedBlock, quad, lane, u);
+  }
+}
+// `rows` rows and `cols` columns of such a block by ordinary stores: this warp's 8 rows.
+__device__ __forceinline__ void store_gated(uint16_t* out, int64_t ldo, int rows, int cols, uint32_t block, int quad, int lane,
+                                            bool vec) {
+  const int chunk = lane & 7;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int n = 8 * quad + 4 * i + (lane >> 3);
+    if (n >= rows || 8 * chunk >= cols) continue;
+    uint4 w;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                 : "r"(block + out_piece(n, chunk))
+                 : "memory");
+    uint16_t* dst = out + n * ldo + 8 * chunk;
+    if (vec && 8 * chunk + 8 <= cols) {
       *reinterpret_cast<uint4*>(dst) = w;
     } else {
       const uint32_t e[4] = {w.x, w.y, w.z, w.w};
@@ -654,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true, waited = p.offsets != nullptr;
     for (int wave = 0, u; ok && (u = walk.at(wave)) >= 0; ++wave) {
       const Tile t = tile_at<C, OP>(p, g, u, e);
-      const int m0 = t.m0 + static_cast<int>(rank) * kTileRows;
+      const int m0 = t.m0 + static_cast<int>(rank) * C::COLS;
       const int n0 = t.n0 + static_cast<int>(rank) * t.half;
       const int boxes = (t.half + C::BOX - 1) / C::BOX;
       const uint32_t bytes = kABytes + static_cast<uint32_t>(boxes) * C::BOX_BYTES + C::SFA_BYTES + C::SFB_BYTES;
@@ -690,6 +788,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t a = sA + stage * kABytes, b = sB + stage * C::B_BYTES;
           const int k0 = kb * C::BLOCK_K;
           if constexpr (OP == kForward) load3(a, &tmW, k0, m0, t.e);
+          if constexpr (OP == kGated) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {  // 16 rows of each projection
+              if (PAIR) tma_load_4d_pair(a + j * (kABytes / 4), &tmW, k0, m0 + 16 * j, 0, t.e, bar);
+              else tma_load_4d(a + j * (kABytes / 4), &tmW, k0, m0 + 16 * j, 0, t.e, bar);
+            }
+          }
           if constexpr (OP == kMx4) load3(a, &tmW, k0 / 2, m0, t.e);
           if constexpr (OP == kGradRows) {
             load3(a, &tmW, m0, k0, t.e);
@@ -880,6 +985,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c = 64 * (C::SHARED && ab == 0 ? (i + kBlocks - 1) % kBlocks : i) + 32 * side;
         const int rows = t.n - c;
         const int64_t o = at + c * p.ldo;
+        if constexpr (OP == kGated) {
+          uint32_t lo[16], hi[16];
+          if (rows > 0) {
+            if (has) {
+              tmem_ld_rows(taddr + static_cast<uint32_t>(c), lo);
+              tmem_ld_rows(taddr + static_cast<uint32_t>(c) + (16u << 16), hi);
+              tmem_wait_rows(lo, hi);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) lo[j] = hi[j] = 0u;
+            }
+          }
+          if (held && i == kBlocks - 1) release();
+          if (rows <= 0) continue;
+          const int m0 = t.m0 + static_cast<int>(rank) * C::COLS, cols = p.M - m0, n = t.row0 + t.n0 + c;
+          const bool issuer = quad == 0 && elect_one(), slopes = p.slopes != nullptr;
+          if (issuer) bulk_wait_read();  // the block's last stores have read it
+          side_sync(side);
+          if (p.out_type == OZK_F16) stage_gate<__half>(block, quad, lane, lo, hi, slopes, p.act);
+          else stage_gate<__nv_bfloat16>(block, quad, lane, lo, hi, slopes, p.act);
+          fence_proxy_async_smem();
+          side_sync(side);
+          const bool whole = rows >= 32 && (cols >= C::COLS || (cols > 0 && cols % 8 == 0));  // see below
+          if (whole && p.vec) {
+            if (issuer) tma_store_3d(&tmO, block, m0, n, 0);
+          } else if (cols > 0) {
+            store_gated(static_cast<uint16_t*>(p.out) + static_cast<int64_t>(n) * p.ldo + m0, p.ldo, min(rows, 32), cols, block,
+                        quad, lane, p.vec);
+          }
+          if (slopes) {
+            if (whole && p.vec_slopes) {
+              if (issuer) {
+                tma_store_3d(&tmSW, block + kGatedBlock, m0, n, 0);
+                tma_store_3d(&tmSW, block + 2 * kGatedBlock, m0, n, 1);
+              }
+            } else if (cols > 0) {
+              uint16_t* s = static_cast<uint16_t*>(p.slopes) + static_cast<int64_t>(n) * p.lds + m0;
+              store_gated(s, p.lds, min(rows, 32), cols, block + kGatedBlock, quad, lane, p.vec_slopes);
+              store_gated(s + p.slope_plane, p.lds, min(rows, 32), cols, block + 2 * kGatedBlock, quad, lane, p.vec_slopes);
+            }
+          }
+          continue;
+        }
         if (p.vec) {
           uint32_t lo[16], hi[16];
           if (rows > 0) {
@@ -938,7 +1086,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // the stores in flight finish before the CTA's shared memory goes
-    if (p.vec && quad == 0) {
+    if ((p.vec || p.vec_slopes) && quad == 0) {
       if (elect_one()) bulk_wait_all();
       __syncwarp();
     }
@@ -972,9 +1120,9 @@ bool make_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* 
               const int64_t* strides, const uint32_t* box, bool swizzle) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
-  cuuint64_t d[3], s[2];
-  cuuint32_t b[3];
-  const cuuint32_t step[3] = {1, 1, 1};
+  cuuint64_t d[4], s[3];
+  cuuint32_t b[4];
+  const cuuint32_t step[4] = {1, 1, 1, 1};
   for (int i = 0; i < rank; ++i) {
     d[i] = static_cast<cuuint64_t>(std::max<int64_t>(dims[i], 1));
     b[i] = box[i];
@@ -1044,6 +1192,13 @@ cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
   p.alpha = q.K ? q.alpha : 1.0f;  // a sum of no terms is zero, whatever alpha
   p.vec = q.out_type != OZK_F32 && reinterpret_cast<uintptr_t>(q.out) % 16 == 0 && q.ldo % 8 == 0 &&
           (OP != kGradWeights || q.groups == 1 || q.out_group % 8 == 0);
+  if (C::GATED) {
+    p.act = q.act;
+    p.slopes = q.slopes;
+    p.lds = q.lds;
+    p.slope_plane = q.slope_plane;
+    p.vec_slopes = q.slopes && reinterpret_cast<uintptr_t>(q.slopes) % 16 == 0 && q.lds % 8 == 0 && q.slope_plane % 8 == 0;
+  }
   const int64_t terms = OP == kGradWeights ? q.T : q.K;
   p.timeout_ns = kTimeoutNs + kStageNs * static_cast<uint64_t>(terms / C::BLOCK_K);
   p.withhold_kb = -1;
@@ -1053,7 +1208,7 @@ cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
     p.withhold_cta = g_withhold.cta;
     g_withhold.timeout_us = 0;
   }
-  p.tiles_m = static_cast<int>((q.M + (kTileRows * C::CTAS) - 1) / (kTileRows * C::CTAS));
+  p.tiles_m = static_cast<int>((q.M + (C::COLS * C::CTAS) - 1) / (C::COLS * C::CTAS));
   p.tiles_n = static_cast<int>((q.N + C::BN - 1) / C::BN);
   p.div_tail = fast_div(p.tiles_m % kSuper);
   // D fp32; types; MN-major operands; M of the MMA
@@ -1081,6 +1236,11 @@ cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
       const int64_t dims[2] = {q.M, q.T}, strides[1] = {2 * q.ld_other};
       const uint32_t box[2] = {64, 64};
       ok = make_map(&tmW, type, 2, q.other, dims, strides, box, true);
+    } else if (C::GATED) {
+      const int64_t dims[4] = {q.K, q.M, 2, q.groups};
+      const int64_t strides[3] = {2 * q.ld_other, 2 * q.ld_other * q.M, 2 * q.other_group};
+      const uint32_t box[4] = {64, 16, 2, 1};
+      ok = make_map(&tmW, type, 4, q.other, dims, strides, box, true);
     } else {
       const int64_t dims[3] = {OP == kForward ? q.K : q.M, OP == kForward ? q.M : q.K, q.groups};
       const int64_t strides[2] = {2 * q.ld_other, 2 * q.other_group};
@@ -1112,6 +1272,13 @@ cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
     const uint32_t box[3] = {64, 32, 1};
     if (!make_map(&tmO, q.out_type == OZK_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q.out,
                   dims, strides, box, true))
+      return cudaErrorInvalidValue;
+  }
+  if (p.vec_slopes) {
+    const int64_t dims[3] = {q.M, q.T, 2}, strides[2] = {2 * q.lds, 2 * q.slope_plane};
+    const uint32_t box[3] = {64, 32, 1};
+    if (!make_map(&tmSW, q.out_type == OZK_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                  q.slopes, dims, strides, box, true))
       return cudaErrorInvalidValue;
   }
   auto kernel = product_kernel<OP, FMT, BN, PAIR>;
@@ -1167,9 +1334,10 @@ cudaError_t choose(const Product& q, int num_sms, cudaStream_t stream) {
   const double groups = sum_rows ? q.groups : std::min(static_cast<double>(q.groups), t);
   const double rows = std::max(sum_rows ? static_cast<double>(q.N) : t / groups, 1.0);
   const double stages = std::ceil((sum_rows ? t / groups : static_cast<double>(q.K)) / (mx ? 256 : 64));
+  const double m = static_cast<double>(q.M) * (OP == kGated ? 2 : 1);  // columns of the M side
   auto cost = [&](int bn, int cols, int slots, double per_row, double fixed, double launch) {
     const double per_group = std::ceil(rows / bn);
-    const double waves = std::ceil(groups * per_group * std::ceil(static_cast<double>(q.M) / cols) / slots);
+    const double waves = std::ceil(groups * per_group * std::ceil(m / cols) / slots);
     return waves * (stages * std::max(mx ? 400.0 : 330.0, per_row * rows / per_group) + fixed) + launch;
   };
   const double pair = cost(256, 256, num_sms / 2, mx ? 2.15 : 2.1, 3000, 2000);
@@ -1189,6 +1357,7 @@ cudaError_t launch_product(const Product& q, int num_sms, cudaStream_t stream) {
     case kForward: return choose<kForward, k16>(q, num_sms, stream);
     case kGradRows: return choose<kGradRows, k16>(q, num_sms, stream);
     case kGradWeights: return choose<kGradWeights, k16>(q, num_sms, stream);
+    case kGated: return choose<kGated, k16>(q, num_sms, stream);
     default:
       return q.a.format == OZK_MXFP4 ? choose<kMx4, kMx>(q, num_sms, stream) : choose<kMx4, kNv>(q, num_sms, stream);
   }

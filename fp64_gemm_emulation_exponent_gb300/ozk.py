@@ -78,6 +78,9 @@ SIGNATURES = {
     "ozk_mx4_gemv": (_i32, [_i64, _i64, _i64, _i32, _vp, _vp, _i64, _i32, _vp, _vp, _i32, _f32, _vp, _i64, _i32, _vp]),
     "ozk_mx4_gated_gemv": (_i32, [_i64, _i64, _i64, _i32, _vp, _vp, _i64, _i32, _vp, _vp, _i32, _f32, _i32, _vp, _i64,
                                   _i32, _vp]),
+    "ozk_grouped_gated_gemm": (_i32, [_i64, _i64, _i64, _i32, _vp, _vp, _i64, _vp, _i64, _i64, _i32, _i32, _vp, _i64, _vp,
+                                      _i64, _i64, _vp]),
+    "ozk_gated_grad": (_i32, [_i64, _i64, _i32, _vp, _vp, _i64, _vp, _i64, _i64, _i32, _vp, _i64, _vp]),
     "ozk_withhold_next_product": (_i32, [_i32, _i32, _i32, ctypes.c_uint32]),
     "ozk_event_create": (_i32, [_vp]),
     "ozk_event_destroy": (_i32, [_vp]),
@@ -809,6 +812,110 @@ def grouped_gemm_dw(dy, x, offsets, out_dtype=None, out=None, stream=None):
                                   out.data_ptr(), ld, stride, _dtype(out.dtype), _stream_at(index, stream))
     if rc:
         raise OzkError("ozk_grouped_gemm_dw", rc)
+    return out
+
+
+_GatedGemm = None
+
+
+def _load_gated():
+    """The autograd function of grouped_gated_gemm (torch is loaded by now)."""
+    global _GatedGemm
+
+    class GatedGemm(_torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w, offsets, activation):
+            T, H = x.shape[0], w.shape[1] // 2
+            slopes = _torch.empty((2, T, -(-H // 8) * 8), dtype=x.dtype, device=x.device)[:, :, :H]
+            ctx.save_for_backward(x, w, offsets, slopes)
+            return grouped_gated_gemm(x, w, offsets, activation, slopes=slopes)
+
+        @staticmethod
+        @_torch.autograd.function.once_differentiable
+        def backward(ctx, dh):
+            x, w, offsets, slopes = ctx.saved_tensors
+            (T, H), dx, dw = dh.shape, None, None
+            # rows that bulk copies can read
+            room = _torch.empty((T, -(-2 * H // 8) * 8), dtype=x.dtype, device=x.device)
+            dpre = gated_grad(dh, slopes, offsets, out=room[:, : 2 * H])
+            if ctx.needs_input_grad[0]:
+                dx = grouped_gemm_dx(dpre, w, offsets, out=_torch.zeros(x.shape, dtype=x.dtype, device=x.device))
+            if ctx.needs_input_grad[1]:
+                dw = grouped_gemm_dw(dpre, x, offsets)
+            return dx, dw, None, None
+
+    _GatedGemm = GatedGemm
+    return GatedGemm
+
+
+def grouped_gated_gemm(x, w, offsets, activation: str = "silu", out=None, slopes=None, stream=None):
+    """h[t] = act(x[t] @ w[g(t)][:H]^T) * (x[t] @ w[g(t)][H:]^T)
+    (ozk_grouped_gated_gemm): x [T, K], w [groups, 2 H, K] of one 16-bit type,
+    the gate's rows first; activation "silu", "gelu" or "gelu_tanh"; [T, H] of
+    their type.  Rows in no group are not written.  slopes, a [2, T, H] tensor,
+    takes dh/dgate and dh/dup, which gated_grad turns a gradient of h with.
+
+    Autograd records it where x or w asks for a gradient (gated_grad, then
+    grouped_gemm_dx and grouped_gemm_dw where asked for; zeros for rows in no
+    group), once: there is no second derivative.  With out or slopes given no
+    graph is recorded."""
+    groups, N, K, ldw, stride = _groups(w)
+    _, kind, index = _grouped(x, w, offsets, groups)
+    act = _activation(activation)
+    if index != _current_device():
+        with _torch.cuda.device(index):
+            return grouped_gated_gemm(x, w, offsets, activation, out, slopes, stream)
+    if out is None and slopes is None and (x.requires_grad or w.requires_grad) and _torch.is_grad_enabled():
+        with _torch.cuda.stream(stream):
+            return (_GatedGemm or _load_gated()).apply(x, w, offsets, activation)
+    T, k, ldx = _rows(x)
+    if k != K or N % 2:
+        raise ValueError(f"x is {tuple(x.shape)}, the weights {tuple(w.shape)}")
+    out, ld, _ = _result(out, T, N // 2, x.dtype, x.device, stream)
+    at, lds, plane = (None, 0, 0) if slopes is None else _slopes(slopes, T, N // 2, x.dtype, index)
+    rc = _lib.ozk_grouped_gated_gemm(T, N // 2, K, groups, offsets.data_ptr(), x.data_ptr(), ldx, w.data_ptr(), ldw,
+                                     stride, kind, act, out.data_ptr(), ld, at, lds, plane, _stream_at(index, stream))
+    if rc:
+        raise OzkError("ozk_grouped_gated_gemm", rc)
+    return out
+
+
+def _slopes(slopes, T, H, dtype, index):
+    """(address, leading dimension, stride between the two) of a gated product's slopes."""
+    if slopes.shape != (2, T, H):
+        raise ValueError(f"slopes have shape {tuple(slopes.shape)}, (2, {T}, {H}) is expected")
+    if slopes.dtype != dtype:
+        raise TypeError(f"slopes are {slopes.dtype}, the operands {dtype}")
+    _same_device(index, slopes)
+    return (slopes.data_ptr(), *_groups(slopes)[3:])
+
+
+def gated_grad(dh, slopes, offsets=None, out=None, stream=None):
+    """The gradient with respect to a gated product's two projections
+    (ozk_gated_grad): dh [T, H] times each of slopes [2, T, H], side by side,
+    [T, 2 H] of the slopes' type (dh of another type is rounded to it).  With it
+    as dy, grouped_gemm_dx and grouped_gemm_dw give the gradients of x and w.
+    With offsets, rows in no group are not written."""
+    if _torch is None:
+        _load_torch()
+    index = _device_index(slopes)
+    _same_device(index, dh)
+    if index != _current_device():
+        with _torch.cuda.device(index):
+            return gated_grad(dh, slopes, offsets, out, stream)
+    groups = 1 if offsets is None else _offsets(offsets, index)
+    if len(dh.shape) != 2:
+        raise ValueError("expected a 2-D gradient")
+    T, H = dh.shape
+    at, lds, plane = _slopes(slopes, T, H, slopes.dtype, index)
+    if dh.dtype != slopes.dtype or dh.stride(1) != 1 and H > 1 or dh.stride(0) < H and T > 1:
+        with _torch.cuda.stream(stream):  # converted where the call runs; an expanded gradient is laid out
+            dh = dh.to(slopes.dtype).contiguous()
+    out, ld, kind = _result(out, T, 2 * H, slopes.dtype, slopes.device, stream)
+    rc = _lib.ozk_gated_grad(T, H, groups, None if offsets is None else offsets.data_ptr(), dh.data_ptr(), _rows(dh)[2],
+                             at, lds, plane, kind, out.data_ptr(), ld, _stream_at(index, stream))
+    if rc:
+        raise OzkError("ozk_gated_grad", rc)
     return out
 
 

@@ -482,6 +482,29 @@ int ozk_grouped_gemm_dw(int64_t T, int64_t N, int64_t K, int groups, const int32
                         int64_t lddy, const void* X, int64_t ldx, int dtype, void* dW, int64_t lddw, int64_t dw_stride,
                         int out_dtype, ozk_stream_t stream);
 
+/* The gated product of a feed-forward block: W holds 2 N rows per group, the
+ * gate's first, and Y[t, j] = act(g) u with g = sum_k x_tk w_g(t),j,k and u the
+ * same with row N + j; g, u and the activation stay in fp32, Y (T x N, of
+ * dtype) is rounded once.  slopes, where not NULL, takes what the gradients
+ * need, both rounded to dtype: row t of the first matrix (rows lds elements
+ * apart) is dY/dg = u act'(g), that of the second, slope_stride elements after
+ * it, dY/du = act(g).  Operand requirements and groups as above, 2 N <= 2^22;
+ * Y and slopes need the alignment of their type only. */
+int ozk_grouped_gated_gemm(int64_t T, int64_t N, int64_t K, int groups, const int32_t* offsets, const void* X,
+                           int64_t ldx, const void* W, int64_t ldw, int64_t w_stride, int dtype, int activation,
+                           void* Y, int64_t ldy, void* slopes, int64_t lds, int64_t slope_stride,
+                           ozk_stream_t stream);
+
+/* The gradient with respect to the two projections, from that of Y and the
+ * slopes: dpre (T x 2 N) has dpre[t, j] = dh_tj dY/dg and dpre[t, N + j] =
+ * dh_tj dY/du, each rounded once to dtype.  With it as dY, ozk_grouped_gemm_dx
+ * and ozk_grouped_gemm_dw (of 2 N rows of w) give the gradients of x and w.
+ * offsets as above, or NULL for all rows; rows in no group are not written.
+ * Any alignment of the type. */
+int ozk_gated_grad(int64_t T, int64_t N, int groups, const int32_t* offsets, const void* dH, int64_t lddh,
+                   const void* slopes, int64_t lds, int64_t slope_stride, int dtype, void* dpre, int64_t ldp,
+                   ozk_stream_t stream);
+
 /* ------------------------------------------------------------------ */
 /* Test hooks of the failure path.                                     */
 /* ------------------------------------------------------------------ */
@@ -506,7 +529,7 @@ int ozk_residue_gemm_withheld(int64_t M, int64_t N, int64_t K, const uint16_t* a
                               int withhold_kb, uint32_t timeout_us, ozk_stream_t stream);
 
 /* The next product (ozk_mx4_gemm, ozk_mx4_grouped_gemm, ozk_grouped_gemm and
- * its gradients) that this host thread launches runs on CTA pairs (pairs 1) or
+ * its gradients, ozk_grouped_gated_gemm) that this host thread launches runs on CTA pairs (pairs 1) or
  * single CTAs (0), with every pipeline wait limited to timeout_us microseconds
  * (up to 10^6; 0 takes the request back) and the copies of k-block `kblock`
  * (64 terms, 256 for 4-bit operands) of the first tile of CTA `cta` (0; on
