@@ -17,17 +17,18 @@
 //     the 4 bytes that ldmatrix hands it out of 16 (32 weights), as terms 2 q,
 //     2 q + 1, 2 q + 8, 2 q + 9 of two steps, and the rows of x are read in
 //     the same order.
-// Rows of bf16 x do not fit fp16 as they are.  A panel (some columns of a
-// row) is scaled by a power of two that brings its largest element to
-// [2^15, 2^16): exact for every element down to 2^-32 of the largest.  Where a
-// panel holds smaller ones, they take part in a further run over the weights,
-// scaled by 2^33 more, and so on (at most 8 runs); activations all but never
-// have them.
+// bf16 rows do not fit fp16 as they are.  A warp scales each row by a power of
+// two that brings the largest element of the first chunk it takes to [2^9,
+// 2^10): exact as fp16 for every element from 2^-26 to 2^6 of that one.  Every
+// chunk is checked for it; where one does not fit, the sums are put away and
+// the scale starts again from that chunk, and elements that are too small even
+// so take part in further passes over the chunk, 27 binades at a time.
 //
 // A block owns 16 R output rows of w (gated: 8 R of each projection) and all
 // of K; its warps take the chunks of 128 columns in turn, each through a ring
-// of its own in shared memory filled by asynchronous copies, and the warps'
-// sums are added at the end in a fixed order.
+// of its own in shared memory (codes, scales and x) filled by asynchronous
+// copies, no barrier between them, and the warps' sums are added at the end in
+// a fixed order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -44,25 +45,32 @@ namespace {
 
 __device__ int g_gemv_status;  // bit 1: bad group offsets
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kChunk = 128;              // columns of a chunk: 64 bytes of codes a row
-constexpr int kRange = 33;               // binades of a panel's elements that one run takes
-constexpr int kMxShift = 22;             // MXFP4 sums are formed 2^-22 smaller: s 2^-22 stays below overflow
+constexpr int kTop = 9;         // exponent that the largest element of a row is scaled to
+constexpr int kHead = 6;        // binades above it that fp16 has room for
+constexpr int kBelow = 26;      // binades below it that stay exact: down to 2^-17, 7 bits above fp16's last
 
-template <int FMT, int R, int NT>
+// W: warps. NT: tiles of 8 rows of x; 0: up to four rows, which the lanes convert together.
+template <int FMT, int R, int NT, int W>
 struct Shape {
   static constexpr bool NV = FMT == OZK_NVFP4;
-  static constexpr int WORDS = NV ? 2 : 1;                       // scale words of a row and chunk
-  static constexpr int CODES = R * 1024;                         // bytes of a chunk
-  static constexpr int STAGE = CODES + R * 16 * WORDS * 4;
-  static constexpr int DEPTH = R == 4 ? 3 : 4;
-  static constexpr int TOKENS = 8 * NT;
-  static constexpr int PANEL = 4096 / NT;                        // columns of x that are staged at a time
-  static constexpr int PITCH = PANEL * 2 + 64;                   // most bytes of a staged row: see pitch
-  static constexpr int RING = kWarps * DEPTH * STAGE;
-  static_assert(kWarps * R * NT * 4 * 32 * 4 <= RING, "the warps' sums take the ring's place");
-  static_assert(PANEL % (kChunk * kWarps) == 0, "every warp has as many chunks of a panel");
+  static constexpr bool FEW = NT == 0;
+  static constexpr int TILES = FEW ? 1 : NT;
+  static constexpr int TOKENS = FEW ? 4 : 8 * NT;
+  static constexpr int ROWS = FEW ? 4 : NT;       // rows of x that a lane keeps a scale for
+  static constexpr int CHUNK = FEW ? 256 : 128;   // columns of a chunk
+  static constexpr int ROW = CHUNK / 2;           // bytes of codes of a row
+  static constexpr int PIECES = ROW / 16;
+  static constexpr int WORDS = CHUNK / (NV ? 64 : 128);  // scale words of a row
+  static constexpr int CODES = R * 16 * ROW;
+  static constexpr int SCALES = (R * 16 * WORDS * 4 + 255) / 256 * 256;  // rows of x start on 256 bytes
+  static constexpr int XROW = CHUNK * 2;          // bytes of a row of x
+  static constexpr int DEPTH = FEW ? (R == 1 ? 3 : 2) : R == 4 || NT == 4 ? 2 : 4;
+  static constexpr int SUMS = R * TILES * 512;    // bytes of a warp's sums
+  static_assert(!FEW || W * DEPTH * (CODES + SCALES) % 512 == 0, "rows of x start on 512 bytes");
+  static constexpr int stage(int tokens) { return CODES + SCALES + (FEW ? 0 : tokens * XROW); }
+  static constexpr int bytes(int tokens) {
+    return W * (DEPTH * stage(tokens) + SUMS + (FEW ? tokens * XROW : 0));
+  }
 };
 
 struct GemvParams {
@@ -80,17 +88,17 @@ struct GemvParams {
   float alpha;
   int act;                 // gated only
   bool vec;                // rows of x start on 16 bytes
-  int pitch;               // bytes of a staged row of x: 64 more than a multiple of 128, so that rows alternate in banks
+  int tokens;              // rows of x that a stage has room for
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
-// 16 or 4 bytes to shared memory, zeros where !valid.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+// 16 and 4 bytes to shared memory.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -125,24 +133,22 @@ __device__ __forceinline__ void decode8(uint32_t w, uint32_t (&h)[4]) {
       : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
       : "r"(w));
 }
+// Both halves of a times the low or the high half of b.
+template <bool HIGH>
 __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+  const __half2 s = *reinterpret_cast<__half2*>(&b), v = __hmul2(*reinterpret_cast<__half2*>(&a), HIGH ? __high2half2(s) : __low2half2(s));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Two E4M3 bytes as an fp16 pair; two E8M0 bytes as a bf16 pair (2^-127 is one of its subnormals, 255 is NaN).
+__device__ __forceinline__ uint32_t e4m3_half2(uint32_t two) {
   uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
   return r;
 }
-// Byte `sel` of a word of E4M3 scales as an fp16 pair.
-__device__ __forceinline__ uint32_t scale_half2(uint32_t word, uint32_t sel) {
-  const uint32_t both = __byte_perm(word, 0, sel * 0x11u);
+__device__ __forceinline__ uint32_t e8m0_bf162(uint32_t two) {
   uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(both)));
+  asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
   return r;
-}
-// 2^(b - 127 - kMxShift) of byte `i` of a word of E8M0 scales; 255 is NaN.
-__device__ __forceinline__ float scale_mx(uint32_t word, int i) {
-  const uint32_t b = (word >> (8 * i)) & 0xFFu;
-  // in two exact steps: 2^(b - 127) is subnormal for b = 0, and small ones stay exact down to 2^-149
-  const float s = __uint_as_float(b == 255u ? 0x7FC00000u : b == 0u ? 0x00400000u : b << 23);
-  return s * (1.0f / (1 << kMxShift));
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -197,7 +203,7 @@ __device__ __forceinline__ Found find_group(const GemvParams& p, int rank) {
   return f;
 }
 
-// Elements [k, k + 8) of a row of x as stored, zeros from K on.
+// Elements [k, k + 8) of a row of x as stored, zeros from K on, at any alignment.
 __device__ __forceinline__ uint4 load8(const uint16_t* row, int k, int K, bool vec) {
   if (vec && k + 8 <= K) {
     uint4 v;
@@ -218,17 +224,79 @@ __device__ __forceinline__ float scaled(float v, int e) {
   const int half = e / 2;
   return v * pow2f(half) * pow2f(e - half);
 }
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+// ---- bf16 pairs as fp16 pairs
+// Largest and smallest magnitudes of some elements, in both halves: m + 0x7FFF
+// a half makes zeros 0x7FFF and others 0x8000 + (m - 1), so that the unsigned
+// maximum and the signed minimum leave zeros out.
+struct Range {
+  uint32_t hi = 0x7FFF7FFFu, lo = 0x7FFF7FFFu;
+  __device__ __forceinline__ void add(uint32_t a, uint32_t b) {
+    a = (a & 0x7FFF7FFFu) + 0x7FFF7FFFu;
+    b = (b & 0x7FFF7FFFu) + 0x7FFF7FFFu;
+    hi = __vimax3_u16x2(hi, a, b);
+    lo = __vimin3_s16x2(lo, a, b);
+  }
+  __device__ __forceinline__ void add(const uint4& v) {
+    add(v.x, v.y);
+    add(v.z, v.w);
+  }
+  // Over all lanes of the warp.
+  __device__ __forceinline__ void warp_wide() {
+    hi = __reduce_max_sync(0xFFFFFFFFu, max(hi & 0xFFFFu, hi >> 16)) * 0x10001u;
+    const int least = __reduce_min_sync(0xFFFFFFFFu, min(static_cast<int>(static_cast<int16_t>(lo & 0xFFFFu)), static_cast<int>(lo) >> 16));
+    lo = (static_cast<uint32_t>(least) & 0xFFFFu) * 0x10001u;
+  }
+  // Whether all but zeros have exponents from E - kBelow to E + kHead.
+  __device__ __forceinline__ bool within(int E) const {
+    const uint32_t most = static_cast<uint32_t>(min((E + kHead + 1) << 7, 0x8000)) + 0x7FFEu;
+    const int least = E - kBelow <= 1 ? -0x8000 : ((E - kBelow) << 7) - 0x8001;
+    return max(hi & 0xFFFFu, hi >> 16) <= most &&
+           min(static_cast<int16_t>(lo & 0xFFFFu), static_cast<int16_t>(lo >> 16)) >= least;
+  }
+  // Biased exponents of the largest and the smallest but zero (0 as 1); without any element: none.
+  __device__ __forceinline__ bool any() const { return (hi & 0x80008000u) != 0u; }
+  __device__ __forceinline__ int top() const {
+    const uint32_t m = max(hi & 0xFFFFu, hi >> 16);
+    return max(static_cast<int>((m - 0x7FFFu) >> 7), 1);
+  }
+  __device__ __forceinline__ int bottom() const {
+    const int a = static_cast<int16_t>(lo & 0xFFFFu), b = static_cast<int16_t>(lo >> 16);
+    return max((min(a, b) + 0x8001) >> 7, 1);
+  }
+};
+__device__ __forceinline__ uint32_t to_half2(uint32_t pair, uint32_t factor) {
+  uint32_t v, r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(pair), "r"(factor));
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__uint_as_float(v & 0xFFFF0000u)), "f"(__uint_as_float(v << 16)));
   return r;
 }
+// The scale 2^shift(E) for a largest exponent E, as a bf16 pair.
+__device__ __forceinline__ int shift_of(int E) { return min(kTop + 127 - E, 127); }
+__device__ __forceinline__ uint32_t factor_of(int E) { return static_cast<uint32_t>((shift_of(E) + 127) << 7) * 0x10001u; }
+// Those of a pair with exponents from E down to E - kBelow, zeros for the others.
+__device__ __forceinline__ uint32_t only(uint32_t pair, int E) {
+  const uint32_t top = E < 1 ? 0u : static_cast<uint32_t>(E + 1) << 7;
+  const uint32_t bottom = E - kBelow <= 1 ? 0u : static_cast<uint32_t>(E - kBelow) << 7;
+  const uint32_t l = pair & 0x7FFFu, h = pair >> 16 & 0x7FFFu;
+  if (l < bottom || l >= top) pair &= 0xFFFF0000u;
+  if (h < bottom || h >= top) pair &= 0x0000FFFFu;
+  return pair;
+}
+__device__ __forceinline__ uint4 only(uint4 v, int E) {
+  return make_uint4(only(v.x, E), only(v.y, E), only(v.z, E), only(v.w, E));
+}
+__device__ __forceinline__ uint4 to_half2(uint4 v, uint32_t factor) {
+  return make_uint4(to_half2(v.x, factor), to_half2(v.y, factor), to_half2(v.z, factor), to_half2(v.w, factor));
+}
 
-template <int FMT, int R, int NT, bool GATED, bool BF>
-__global__ void __launch_bounds__(kThreads) gemv_kernel(const GemvParams p) {
-  using S = Shape<FMT, R, NT>;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint32_t s_max[S::TOKENS], s_min[S::TOKENS];
+// Blocks of an SM that registers are kept for.
+constexpr int blocks_of(int R, int NT, int W) { return (NT == 0 ? R == 1 ? 24 : 16 : R * NT > 4 ? 8 : 16) / W; }
+
+template <int FMT, int R, int NT, int W, bool GATED, bool BF>
+__global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const GemvParams p) {
+  using S = Shape<FMT, R, NT, W>;
+  constexpr int TILES = S::TILES;
+  extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_dependency_sync();
 
@@ -242,267 +310,340 @@ __global__ void __launch_bounds__(kThreads) gemv_kernel(const GemvParams p) {
     if (rows == 0) return;
   }
 
-  // This block's rows of w: row r of tile i, rows past the last one doubled.
-  constexpr int kOut = GATED ? 8 : 16;  // output columns of a tile
-  const int n0 = blockIdx.x * (kOut * R);
-  auto w_row = [&](int i, int r) {
-    const int n = min(n0 + kOut * i + (GATED ? r & 7 : r), p.N - 1);
-    return GATED && r >= 8 ? p.N + n : n;
-  };
+  // This block's output columns: tile i has kOut of them, 32 from the next
+  // tile's, so that the scale words of all tiles lie side by side.
+  constexpr int kOut = GATED ? 8 : 16, kSub = 32 / kOut;
+  const int n0 = static_cast<int>(blockIdx.x) / kSub * (32 * R) + static_cast<int>(blockIdx.x) % kSub * kOut;
+  if (n0 >= p.N) return;
   const int64_t group_row = static_cast<int64_t>(e) * p.w_rows;
   const uint8_t* codes = p.codes + group_row * (p.kpad / 2);
   const uint8_t* scales = p.scales + (group_row / 128 + e) * p.words * 512;
 
-  const uint32_t ring = smem_addr(smem) + static_cast<uint32_t>(warp * S::DEPTH * S::STAGE);
-  const uint32_t xs = smem_addr(smem) + S::RING;
-  const int chunks = (p.kpad + kChunk - 1) / kChunk;
-
-  // The rows that this lane copies: 4 lanes a row of 64 bytes, 8 rows at a time.
-  const uint8_t* src[2 * R];
-  uint32_t dst[2 * R];
-#pragma unroll
-  for (int j = 0; j < 2 * R; ++j) {
-    const int r = (j & 1) * 8 + (lane >> 2), piece = lane & 3;
-    src[j] = codes + static_cast<int64_t>(w_row(j >> 1, r)) * (p.kpad / 2) + piece * 16;
-    dst[j] = static_cast<uint32_t>((j >> 1) * 1024 + r * 64 + ((piece ^ (r >> 1 & 3)) * 16));
-  }
-  constexpr int kScaleCopies = (R * 16 * S::WORDS + 31) / 32;
-  const uint8_t* ssrc[kScaleCopies];
-#pragma unroll
-  for (int j = 0; j < kScaleCopies; ++j) {  // word (lane + 32 j) of a chunk: [word][tile][row]
-    const int i = lane + 32 * j, word = i / (16 * R), tile = i / 16 % R, row = w_row(tile, i % 16);
-    ssrc[j] = scales + (static_cast<int64_t>(row / 128) * p.words + word) * 512 + row % 32 * 16 + row / 32 % 4 * 4;
-  }
-  auto fetch = [&](int chunk, int slot) {
-    const uint32_t at = ring + static_cast<uint32_t>(slot * S::STAGE);
-    const bool in = chunk * kChunk + (lane & 3) * 32 < p.kpad;
-    const int64_t off = in ? static_cast<int64_t>(chunk) * (kChunk / 2) : 0;
-#pragma unroll
-    for (int j = 0; j < 2 * R; ++j) copy16(at + dst[j], in ? src[j] + off : codes, in);
-#pragma unroll
-    for (int j = 0; j < kScaleCopies; ++j) {
-      const int i = lane + 32 * j, word = i / (16 * R);
-      const bool sin = chunk * S::WORDS + word < p.words;
-      if (i < R * 16 * S::WORDS)
-        copy4(at + S::CODES + i * 4, sin ? ssrc[j] + static_cast<int64_t>(chunk) * S::WORDS * 512 : scales, sin);
-    }
+  // A warp's ring: stages of codes, scale words and (not FEW) p.tokens rows of
+  // x.  Then the warps' sums, and where FEW those rows as fp16.  16-byte
+  // pieces are swapped within a row so that the rows that are read together lie
+  // in different banks.
+  const uint32_t stage = static_cast<uint32_t>(S::stage(p.tokens));
+  const uint32_t ring = smem_addr(smem) + static_cast<uint32_t>(warp * S::DEPTH) * stage;
+  float* sums = reinterpret_cast<float*>(smem + W * S::DEPTH * stage);
+  const uint32_t x16 = smem_addr(sums) + W * S::SUMS + static_cast<uint32_t>(warp * p.tokens * S::XROW);
+  const int chunks = (p.kpad + S::CHUNK - 1) / S::CHUNK;
+  auto code_piece = [](int r, int piece) {
+    return static_cast<uint32_t>(r * S::ROW + ((piece ^ (S::FEW ? r & 7 : r >> 1 & 3)) * 16));
   };
+  auto x_piece = [](int t, int piece) { return static_cast<uint32_t>(t * S::XROW + ((piece ^ (t & 1) * 4) * 16)); };
+
+  // What this lane copies of a chunk: piece `lane % PIECES` of every
+  // 32 / PIECES-th of the tiles' rows, and scale words.  Rows past the last one
+  // are left out: what lies in their place reaches only sums that are not
+  // written.
+  constexpr int kCopies = R * 16 * S::PIECES / 32, kStep = 32 / S::PIECES;
+  auto w_row = [&](int r) {  // of row r of the tiles
+    const int n = n0 + r / 16 * 32 + (GATED ? r & 7 : r & 15);
+    return GATED && (r & 8) ? p.N + n : n;
+  };
+  auto in_range = [&](int r) { return n0 + r / 16 * 32 + (GATED ? r & 7 : r & 15) < p.N; };
+  const int r0 = lane / S::PIECES;
+  const int64_t pitch = p.kpad / 2;
+  const uint8_t* src = codes + (n0 + r0) * pitch + lane % S::PIECES * 16;  // of rows r0 + kStep j: see from()
+  const bool all_rows = n0 + 32 * (R - 1) + kOut <= p.N;
+  const uint32_t dst = code_piece(r0, lane % S::PIECES);
+  constexpr int kScaleCopies = (R * 16 * S::WORDS + 31) / 32;
+  int64_t ssrc[kScaleCopies];  // offsets of the words (lane + 32 j) of a chunk: [row][word]
+#pragma unroll
+  for (int j = 0; j < kScaleCopies; ++j) {
+    const int i = lane + 32 * j, row = w_row(i / S::WORDS);
+    ssrc[j] = (static_cast<int64_t>(row / 128) * p.words + i % S::WORDS) * 512 + row % 32 * 16 + row / 32 % 4 * 4;
+  }
 
   for (int t0 = 0; t0 < rows; t0 += S::TOKENS) {
     const int tokens = min(S::TOKENS, rows - t0);
     const uint16_t* x = p.x + (static_cast<int64_t>(row0) + t0) * p.ldx;
-    float tot[R][NT][4];
+    auto fetch = [&](int chunk, int slot) {
+      const uint32_t at = ring + static_cast<uint32_t>(slot) * stage;
+      const uint8_t* from = src + static_cast<int64_t>(chunk) * S::ROW;
+      const uint8_t* sfrom = scales + static_cast<int64_t>(chunk) * S::WORDS * 512;
+      auto code = [&](int j) {
+        // rows 8 apart (where FEW, 4: pieces differ by one bit) have their pieces in the same places
+        const uint32_t to = S::FEW && (j & 1) ? dst ^ 64u : dst;
+        constexpr int kPer = 16 / kStep;  // copies of a tile
+        const int64_t row = j / kPer * 32 + (GATED ? j % (kPer / 2) * kStep + (j % kPer >= kPer / 2 ? p.N : 0) : j % kPer * kStep);
+        copy16(at + to + j * kStep * S::ROW, from + row * pitch);
+      };
+      const bool last = (chunk + 1) * S::CHUNK > p.kpad;
+      if (all_rows && !last) {
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+        for (int j = 0; j < kCopies; ++j) code(j);
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+        for (int j = 0; j < kScaleCopies; ++j)
+          if (R * 16 * S::WORDS % 32 == 0 || j + 1 < kScaleCopies || lane + 32 * j < R * 16 * S::WORDS)
+            copy4(at + S::CODES + (lane + 32 * j) * 4, sfrom + ssrc[j]);
+      } else {  // the rows, columns and words that are there
+        const bool in = chunk * S::CHUNK + lane % S::PIECES * 32 < p.kpad;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tot[i][n][c] = 0.0f;
-
-    bool more = false;  // elements are left for a further run
-    int run = 0;
-    do {
-      more = false;
-      int next = warp;  // chunk that is fetched next
+        for (int j = 0; j < kCopies; ++j)
+          if (in && in_range(r0 + kStep * j)) code(j);
 #pragma unroll
-      for (int s = 0; s < S::DEPTH - 1; ++s) {
-        if (next < chunks) fetch(next, s);
-        copy_commit();
-        next += kWarps;
+        for (int j = 0; j < kScaleCopies; ++j) {
+          const int i = lane + 32 * j;
+          if (i < R * 16 * S::WORDS && in_range(i / S::WORDS) && chunk * S::WORDS + i % S::WORDS < p.words)
+            copy4(at + S::CODES + i * 4, sfrom + ssrc[j]);
+        }
       }
-      int slot = 0;
-      int chunk = warp;
-      for (int k0 = 0; k0 < p.kpad; k0 += S::PANEL) {
-        // ---- the panel of x, as fp16
-        __syncthreads();  // the last panel (or the sums before) is done with
-        const int vectors = min(S::PANEL, (p.kpad - k0 + kChunk - 1) / kChunk * kChunk) / 8;
-        if (BF && tid < S::TOKENS) {
-          s_max[tid] = 0u;
-          s_min[tid] = 0xFFFFu;
-        }
-        if (BF) __syncthreads();
-        for (int t = 0; t < tokens; ++t) {
-          uint32_t hi = 0u, lo = 0xFFFFFFFFu;
-          for (int v = tid; v < vectors; v += kThreads) {
-            const uint4 w = load8(x + t * p.ldx, k0 + 8 * v, p.K, p.vec);
-            sts128(xs + static_cast<uint32_t>(t * p.pitch + 16 * v), w);
-            if (BF) {
-              const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+      if (!S::FEW) {
+        const int k = chunk * S::CHUNK + (lane & 15) * 8;
+        const uint32_t to = at + S::CODES + S::SCALES + x_piece(lane >> 4, lane & 15);
+        const uint16_t* row = x + (lane >> 4) * p.ldx + k;
+        if (p.vec && (chunk + 1) * S::CHUNK <= p.K) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t m = a[i] & 0x7FFF7FFFu;
-                hi = __vmaxu2(hi, m);
-                lo = __vminu2(lo, (m + 0x7FFF7FFFu) ^ 0x80008000u);  // m - 1, zeros last
-              }
-            }
-          }
-          if (BF) {
-            hi = __reduce_max_sync(0xFFFFFFFFu, max(hi & 0xFFFFu, hi >> 16));
-            lo = __reduce_min_sync(0xFFFFFFFFu, min(lo & 0xFFFFu, lo >> 16));
-            if (lane == 0) {
-              atomicMax(&s_max[t], hi);
-              atomicMin(&s_min[t], lo);
-            }
-          }
-        }
-        __syncthreads();
-        if (BF) {
-          for (int t = 0; t < tokens; ++t) {
-            // exponent of the largest element; this run takes those from `top` down to `bottom` (bit patterns)
-            const int E = max(static_cast<int>(s_max[t] >> 7), 1) - kRange * run;
-            const uint32_t top = E < 1 ? 0u : static_cast<uint32_t>(E + 1) << 7;  // below 1: all of them are through
-            const uint32_t bottom = E - (kRange - 1) <= 1 ? 0u : static_cast<uint32_t>(E - (kRange - 1)) << 7;
-            const uint32_t least = s_min[t] + 1u;  // the smallest but zero; 0x10000: none
-            const bool all = run == 0 && least >= bottom;
-            if (least < bottom) more = true;
-            const int shift = 142 - max(E, 1);
-            const float f1 = pow2f(shift / 2), f2 = pow2f(shift - shift / 2);
-            for (int v = tid; v < vectors; v += kThreads) {
-              const uint32_t at = xs + static_cast<uint32_t>(t * p.pitch + 16 * v);
-              const uint4 w = lds128(at);
-              uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t u = a[i] << 16, h = a[i] & 0xFFFF0000u;
-                if (!all) {
-                  const uint32_t ml = a[i] & 0x7FFFu, mh = a[i] >> 16 & 0x7FFFu;
-                  if (ml < bottom || ml >= top) u = 0u;
-                  if (mh < bottom || mh >= top) h = 0u;
-                }
-                a[i] = pack_half2(__uint_as_float(u) * f1 * f2, __uint_as_float(h) * f1 * f2);
-              }
-              sts128(at, make_uint4(a[0], a[1], a[2], a[3]));
-            }
-          }
-          __syncthreads();
-        }
-
-        // ---- this warp's chunks of the panel
-        float acc[R][NT][4];
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) acc[i][n][c] = 0.0f;
+          for (int i = 0; i < S::TOKENS / 2; ++i)
+            if (2 * i + (lane >> 4) < tokens) copy16(to + i * 2 * S::XROW, row + i * 2 * p.ldx);
+        } else {
 #pragma unroll 1
-        for (; chunk < chunks && chunk * kChunk < k0 + S::PANEL; chunk += kWarps) {
-          copy_wait<S::DEPTH - 2>();
-          __syncwarp();
-          // the slot that was used before this one is free
-          if (next < chunks) fetch(next, slot == 0 ? S::DEPTH - 1 : slot - 1);
-          copy_commit();
-          next += kWarps;
-          const uint32_t at = ring + static_cast<uint32_t>(slot * S::STAGE);
-          const uint32_t xat = xs + static_cast<uint32_t>((lane >> 2) * p.pitch + (chunk * kChunk - k0) * 2 + (lane & 3) * 16);
-          uint32_t sc[R][2][S::WORDS];
+          for (int i = 0; 2 * i + (lane >> 4) < tokens; ++i) sts128(to + i * 2 * S::XROW, load8(row + i * 2 * p.ldx - k, k, p.K, false));
+        }
+      }
+    };
+    // FEW: this lane's eight elements of every row of a chunk.
+    uint4 xr[4];
+    auto fetch_x = [&](int chunk) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        if (t < tokens) xr[t] = load8(x + t * p.ldx, chunk * S::CHUNK + lane * 8, p.K, p.vec);
+    };
+
+    float acc[R][TILES][4];
+    auto clear = [&]() {
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int n = 0; n < TILES; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[i][n][c] = 0.0f;
+    };
+    clear();
+    // The largest exponent that a row's scale is made for: FEW, of row t; else of this lane's row (lane / 4) of tile n.
+    int E[S::ROWS];
+    uint32_t factor[S::ROWS];  // 2^shift(E)
+#pragma unroll
+    for (int n = 0; n < S::ROWS; ++n) E[n] = 0, factor[n] = 0u;
+    bool kept = false;  // sums of an earlier scale have been put away
+    float* mine = sums + warp * (S::SUMS / 4) + lane;
+    // Puts the sums away without their scale (2^shift(E - down)); rows 2 q, 2 q + 1 of a tile are this lane's columns.
+    auto put_away = [&](int down) {
+#pragma unroll
+      for (int n = 0; n < TILES; ++n) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          int back = 0;
+          if (BF && S::FEW) back = -shift_of((lane & 1 ? E[2 + c] : E[c]) - down);  // rows past the fourth are nobody's
+          if (BF && !S::FEW) back = __shfl_sync(0xFFFFFFFFu, -shift_of(E[n] - down), (2 * (lane & 3) + c) * 4);
 #pragma unroll
           for (int i = 0; i < R; ++i)
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
+            for (int h = 0; h < 4; h += 2) {
+              float* at = mine + ((i * TILES + n) * 4 + c + h) * 32;
+              const float v = BF ? scaled(acc[i][n][c + h], back) : acc[i][n][c + h];
+              *at = kept ? *at + v : v;
+            }
+        }
+      }
+      kept = true;
+    };
+
+    int next = warp;  // chunk that is fetched next
 #pragma unroll
-              for (int w = 0; w < S::WORDS; ++w)
-                sc[i][half][w] = lds32(at + S::CODES + static_cast<uint32_t>((w * R + i) * 16 + half * 8 + (lane >> 2)) * 4);
+    for (int s = 0; s < S::DEPTH - 1; ++s) {
+      if (next < chunks) fetch(next, s);
+      copy_commit();
+      next += W;
+    }
+    if (S::FEW && warp < chunks) fetch_x(warp);
+    int slot = 0;
+#pragma unroll 1
+    for (int chunk = warp; chunk < chunks; chunk += W) {
+      __syncwarp();  // the slot that was used before this one is free
+      if (next < chunks) fetch(next, slot == 0 ? S::DEPTH - 1 : slot - 1);
+      copy_commit();
+      copy_wait<S::DEPTH - 1>();
+      __syncwarp();
+      next += W;
+      const uint32_t at = ring + static_cast<uint32_t>(slot) * stage;
+      const uint32_t xat = S::FEW ? x16 : at + S::CODES + S::SCALES;
+
+      // One pass over the chunk's weights; part: only elements of x with exponents from E - down to kBelow below it.
+      // Lanes of rows that are not there read the last one; their sums are nobody's.
+      auto pass = [&](bool part, int down) {
+        const uint32_t wat = at + code_piece(lane & 15, lane >> 4);
+        const uint32_t sat = at + S::CODES + static_cast<uint32_t>((lane >> 2) * S::WORDS * 4);
+        uint32_t xrow[TILES];
 #pragma unroll
-          for (int s = 0; s < 4; s += 2) {
-            uint4 xb[2][NT];
+        for (int n = 0; n < TILES; ++n) xrow[n] = xat + x_piece(min(8 * n + (lane >> 2), tokens - 1), lane & 3);
+        const int pairs = min(S::CHUNK, p.kpad - chunk * S::CHUNK) / 64;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+        for (int s = 0; s < S::CHUNK / 64; ++s) {  // 64 columns: two segments of 32
+          if (s >= pairs) break;
+          uint4 xb[2][TILES];
 #pragma unroll
-              for (int n = 0; n < NT; ++n)
-                xb[j][n] = 8 * n + (lane >> 2) < tokens ? lds128(xat + static_cast<uint32_t>(8 * n * p.pitch + (s + j) * 64))
-                                                        : make_uint4(0u, 0u, 0u, 0u);
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-              const int r = (lane & 7) + (lane & 8);
-              uint32_t w[4];
-              ldmatrix4(at + static_cast<uint32_t>(i * 1024 + r * 64 + (((s + (lane >> 4)) ^ (r >> 1 & 3)) * 16)), w);
+            for (int n = 0; n < TILES; ++n) {
+              uint4 v = lds128(xrow[n] ^ static_cast<uint32_t>((2 * s + j) * 64));
+              if (BF && !S::FEW) {
+                uint32_t f = factor[n];
+                if (part) {
+                  asm volatile("");  // a branch: the masks are not worth a test in every pass
+                  v = only(v, E[n] - down);
+                  f = factor_of(E[n] - down);
+                }
+                v = to_half2(v, f);
+              }
+              xb[j][n] = v;
+            }
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                uint32_t lo[4], hi[4];
-                decode8(w[2 * j], lo);
-                decode8(w[2 * j + 1], hi);
-                if (S::NV) {
-                  const uint32_t sel = 2u * ((s + j) & 1) + ((lane >> 1) & 1u);
-                  const uint32_t sl = scale_half2(sc[i][0][(s + j) >> 1 & (S::WORDS - 1)], sel);
-                  const uint32_t sh = scale_half2(sc[i][1][(s + j) >> 1 & (S::WORDS - 1)], sel);
+          for (int i = 0; i < R; ++i) {
+            uint32_t w[4];
+            ldmatrix4((wat ^ static_cast<uint32_t>(s * 32)) + i * 16 * S::ROW, w);
+            const uint32_t word = sat + static_cast<uint32_t>(i * 16 * S::WORDS + (S::NV ? s : s >> 1)) * 4;
+            uint32_t sl = lds32(word), sh = lds32(word + 8 * S::WORDS * 4);
+            if (S::NV) {  // of a word's four blocks of 16 the lane's own: one in each segment
+              const uint32_t pick = lane & 2 ? 0x31u : 0x20u;
+              sl = e4m3_half2(__byte_perm(sl, 0, pick));
+              sh = e4m3_half2(__byte_perm(sh, 0, pick));
+            } else {
+              sl = e8m0_bf162(s & 1 ? sl >> 16 : sl);
+              sh = e8m0_bf162(s & 1 ? sh >> 16 : sh);
+            }
 #pragma unroll
-                  for (int c = 0; c < 4; ++c) {
-                    lo[c] = mul_half2(lo[c], sl);
-                    hi[c] = mul_half2(hi[c], sh);
-                  }
+            for (int j = 0; j < 2; ++j) {
+              uint32_t lo[4], hi[4];
+              decode8(w[2 * j], lo);
+              decode8(w[2 * j + 1], hi);
+              if (S::NV) {
 #pragma unroll
-                  for (int n = 0; n < NT; ++n) {
-                    mma16816(acc[i][n], lo[0], hi[0], lo[1], hi[1], xb[j][n].x, xb[j][n].y);
-                    mma16816(acc[i][n], lo[2], hi[2], lo[3], hi[3], xb[j][n].z, xb[j][n].w);
-                  }
-                } else {
-                  const float sl = scale_mx(sc[i][0][0], s + j), sh = scale_mx(sc[i][1][0], s + j);
+                for (int c = 0; c < 4; ++c) {
+                  lo[c] = j ? mul_half2<true>(lo[c], sl) : mul_half2<false>(lo[c], sl);
+                  hi[c] = j ? mul_half2<true>(hi[c], sh) : mul_half2<false>(hi[c], sh);
+                }
 #pragma unroll
-                  for (int n = 0; n < NT; ++n) {
-                    float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    mma16816(c, lo[0], hi[0], lo[1], hi[1], xb[j][n].x, xb[j][n].y);
-                    mma16816(c, lo[2], hi[2], lo[3], hi[3], xb[j][n].z, xb[j][n].w);
-                    acc[i][n][0] = fmaf(c[0], sl, acc[i][n][0]);
-                    acc[i][n][1] = fmaf(c[1], sl, acc[i][n][1]);
-                    acc[i][n][2] = fmaf(c[2], sh, acc[i][n][2]);
-                    acc[i][n][3] = fmaf(c[3], sh, acc[i][n][3]);
-                  }
+                for (int n = 0; n < TILES; ++n) {
+                  mma16816(acc[i][n], lo[0], hi[0], lo[1], hi[1], xb[j][n].x, xb[j][n].y);
+                  mma16816(acc[i][n], lo[2], hi[2], lo[3], hi[3], xb[j][n].z, xb[j][n].w);
+                }
+              } else {
+                const float fl = __uint_as_float(j ? sl & 0xFFFF0000u : sl << 16);
+                const float fh = __uint_as_float(j ? sh & 0xFFFF0000u : sh << 16);
+#pragma unroll
+                for (int n = 0; n < TILES; ++n) {
+                  float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                  mma16816(c, lo[0], hi[0], lo[1], hi[1], xb[j][n].x, xb[j][n].y);
+                  mma16816(c, lo[2], hi[2], lo[3], hi[3], xb[j][n].z, xb[j][n].w);
+                  acc[i][n][0] = fmaf(c[0], fl, acc[i][n][0]);
+                  acc[i][n][1] = fmaf(c[1], fl, acc[i][n][1]);
+                  acc[i][n][2] = fmaf(c[2], fh, acc[i][n][2]);
+                  acc[i][n][3] = fmaf(c[3], fh, acc[i][n][3]);
                 }
               }
             }
           }
-          slot = slot + 1 == S::DEPTH ? 0 : slot + 1;
         }
-        // ---- into the sums, without the panel's scale
+      };
+      // FEW: this chunk's rows, converted, to shared memory.
+      auto stage_x = [&](bool part, int down) {
+        __syncwarp();
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int t = 8 * n + 2 * (lane & 3) + c;
-            int back = S::NV ? 0 : kMxShift;
-            if (BF && t < tokens) back += max(max(static_cast<int>(s_max[t] >> 7), 1) - kRange * run, 1) - 142;
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-              tot[i][n][c] += scaled(acc[i][n][c], back);
-              tot[i][n][c + 2] += scaled(acc[i][n][c + 2], back);
-            }
-          }
-      }
-      copy_wait<0>();
-      ++run;
-    } while (BF && __syncthreads_or(more));
+        for (int t = 0; t < 4; ++t) {
+          if (t >= tokens) break;
+          if (!BF) sts128(x16 + x_piece(t, lane), xr[t]);
+          else if (!part) sts128(x16 + x_piece(t, lane), to_half2(xr[t], factor[t]));
+          else sts128(x16 + x_piece(t, lane), to_half2(only(xr[t], E[t] - down), factor_of(E[t] - down)));
+        }
+        __syncwarp();
+      };
 
-    // ---- the warps' sums, in order; all copies are in, and no warp reads the ring any more
-    __syncthreads();
-    float* part = reinterpret_cast<float*>(smem);
+      // ---- do this chunk's rows fit their scales?
+      bool part = false;               // some do not, whatever the scale
+      int low[S::ROWS];                // a row's smallest exponent
+      if (BF) {
+        Range range[S::ROWS];
+        bool fits = true;
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+        for (int n = 0; n < S::ROWS; ++n) {
+          if (S::FEW) {
+            if (n >= tokens) break;
+            range[n].add(xr[n]);
+          } else {
+            const uint32_t row = xat + x_piece(min(8 * n + (lane >> 2), tokens - 1), lane & 3);
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+            for (int s = 0; s < S::CHUNK / 32; ++s) range[n].add(lds128(row ^ static_cast<uint32_t>(s * 64)));
+          }
+          fits = fits && E[n] > 0 && range[n].within(E[n]);
+        }
+        if (!__all_sync(0xFFFFFFFFu, fits)) {
+          if (chunk != warp) {
+            put_away(0);
+            clear();
+          }
+          bool small = false;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) part[((warp * R + i) * NT + n) * 128 + c * 32 + lane] = tot[i][n][c];
+          for (int n = 0; n < S::ROWS; ++n) {
+            if (S::FEW) {
+              if (n < tokens) range[n].warp_wide();
+            } else {
+#pragma unroll
+              for (int d = 1; d < 4; d *= 2) {
+                range[n].hi = __vmaxu2(range[n].hi, __shfl_xor_sync(0xFFFFFFFFu, range[n].hi, d));
+                range[n].lo = __vmins2(range[n].lo, __shfl_xor_sync(0xFFFFFFFFu, range[n].lo, d));
+              }
+            }
+            E[n] = range[n].any() ? range[n].top() : 1;
+            low[n] = range[n].any() ? range[n].bottom() : 256;
+            factor[n] = factor_of(E[n]);
+            small = small || low[n] < E[n] - kBelow;
+          }
+          part = __any_sync(0xFFFFFFFFu, small);
+        }
+      }
+      for (int down = 0;; down += kBelow + 1) {
+        if (S::FEW) stage_x(part, down);
+        pass(part, down);
+        if (!BF || !part) break;
+        put_away(down);
+        clear();
+        bool left = false;
+#pragma unroll
+        for (int n = 0; n < S::ROWS; ++n) left = left || low[n] < E[n] - down - kBelow;
+        if (!__any_sync(0xFFFFFFFFu, left)) break;
+      }
+      if (S::FEW && chunk + W < chunks) fetch_x(chunk + W);
+      slot = slot + 1 == S::DEPTH ? 0 : slot + 1;
+    }
+    put_away(0);
+    copy_wait<0>();
+
+    // ---- the warps' sums, in order
     __syncthreads();
     auto sum = [&](int i, int n, int c, int l) {
       float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) v += part[((w * R + i) * NT + n) * 128 + c * 32 + l];
+      for (int w = 0; w < W; ++w) v += sums[w * (S::SUMS / 4) + ((i * TILES + n) * 4 + c) * 32 + l];
       return v;
     };
-    for (int o = tid; o < R * NT * (GATED ? 64 : 128); o += kThreads) {
+    constexpr int kRows = S::FEW ? 4 : 8;  // rows of x of a tile that can be there
+    for (int o = tid; o < R * TILES * kRows * kOut; o += 32 * W) {
       // a value of lane l = 4 row + token / 2: c = token % 2, + 2 for the second eight rows of the tile
-      const int col = o % kOut, t = o / kOut % 8, n = o / kOut / 8 % NT, i = o / kOut / 8 / NT;
+      const int col = o % kOut, t = o / kOut % kRows, n = o / (kOut * kRows) % TILES, i = o / (kOut * kRows * TILES);
       const int l = (col & 7) * 4 + (t >> 1), c = t & 1;
-      const int token = 8 * n + t, out = n0 + kOut * i + col;
+      const int token = 8 * n + t, out = n0 + 32 * i + col;
       if (token >= tokens || out >= p.N) continue;
       float v = p.alpha * sum(i, n, GATED ? c : c + 2 * (col >> 3), l);
       if (GATED) v = act_value(v, p.act) * (p.alpha * sum(i, n, c + 2, l));
-      const int64_t at = (static_cast<int64_t>(row0) + t0 + token) * p.ldy + out;
-      if (p.out_type == OZK_F32) static_cast<float*>(p.y)[at] = v;
-      else if (p.out_type == OZK_F16) static_cast<__half*>(p.y)[at] = __float2half_rn(v);
-      else static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(v);
+      const int64_t to = (static_cast<int64_t>(row0) + t0 + token) * p.ldy + out;
+      if (p.out_type == OZK_F32) static_cast<float*>(p.y)[to] = v;
+      else if (p.out_type == OZK_F16) static_cast<__half*>(p.y)[to] = __float2half_rn(v);
+      else static_cast<__nv_bfloat16*>(p.y)[to] = __float2bfloat16_rn(v);
     }
-    __syncthreads();  // the ring is filled again
+    if (t0 + S::TOKENS < rows) __syncthreads();  // the sums' places are used again
   }
 }
 
@@ -520,19 +661,17 @@ cudaError_t allow_smem(const void* kernel, int bytes) {
   return it->second;
 }
 
-template <int FMT, int R, int NT, bool GATED, bool BF>
+template <int FMT, int R, int NT, int W, bool GATED, bool BF>
 cudaError_t launch(GemvParams p, cudaStream_t stream) {
-  using S = Shape<FMT, R, NT>;
-  auto kernel = gemv_kernel<FMT, R, NT, GATED, BF>;
-  constexpr int kMost = S::RING + S::TOKENS * S::PITCH;
-  static_assert(kMost + 8 * S::TOKENS <= 232448, "shared memory");
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), kMost);
+  using S = Shape<FMT, R, NT, W>;
+  auto kernel = gemv_kernel<FMT, R, NT, W, GATED, BF>;
+  static_assert(S::bytes(S::TOKENS) <= 232448, "shared memory");
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), S::bytes(S::TOKENS));
   if (e != cudaSuccess) return e;
-  const int per = (GATED ? 8 : 16) * R;
-  const dim3 grid((p.N + per - 1) / per, p.offsets ? std::min(p.groups, p.T) : 1);
-  p.pitch = std::min(S::PANEL, (p.kpad + kChunk - 1) / kChunk * kChunk) * 2 + 64;
-  const size_t smem = S::RING + static_cast<size_t>(std::min(p.T, S::TOKENS)) * p.pitch;
-  return launch_dependent(kernel, grid, dim3(kThreads), smem, stream, p);
+  const int sub = GATED ? 4 : 2;  // blocks that share 32 R columns
+  const dim3 grid((p.N + 32 * R - 1) / (32 * R) * sub, p.offsets ? std::min(p.groups, p.T) : 1);
+  p.tokens = std::min(p.T, S::TOKENS);
+  return launch_dependent(kernel, grid, dim3(32 * W), S::bytes(p.tokens), stream, p);
 }
 
 template <int FMT, bool GATED, bool BF>
@@ -540,13 +679,18 @@ cudaError_t choose(const GemvParams& p, int num_sms, cudaStream_t stream) {
   const int active = p.offsets ? std::min(p.groups, p.T) : 1;
   const int rows = (p.T + active - 1) / active;  // of a group, as their mean: the offsets are on the device
   const int64_t tiles = static_cast<int64_t>((p.N + (GATED ? 7 : 15)) / (GATED ? 8 : 16)) * active;
-  if (rows <= 8) {
-    if (tiles >= 16 * num_sms) return launch<FMT, 4, 1, GATED, BF>(p, stream);
-    if (tiles >= 4 * num_sms) return launch<FMT, 2, 1, GATED, BF>(p, stream);
-    return launch<FMT, 1, 1, GATED, BF>(p, stream);
+  if (rows <= 4) {
+    if (tiles >= 8 * num_sms) return launch<FMT, 2, 0, 4, GATED, BF>(p, stream);
+    if (tiles >= 3 * num_sms) return launch<FMT, 2, 0, 8, GATED, BF>(p, stream);
+    return launch<FMT, 1, 0, 8, GATED, BF>(p, stream);
   }
-  if (rows <= 16) return tiles >= 3 * num_sms ? launch<FMT, 4, 2, GATED, BF>(p, stream) : launch<FMT, 1, 2, GATED, BF>(p, stream);
-  return tiles >= 2 * num_sms ? launch<FMT, 2, 4, GATED, BF>(p, stream) : launch<FMT, 1, 4, GATED, BF>(p, stream);
+  if (rows <= 8) {
+    if (tiles >= 4 * num_sms) return launch<FMT, 2, 1, 8, GATED, BF>(p, stream);
+    return launch<FMT, 1, 1, 8, GATED, BF>(p, stream);
+  }
+  if (rows <= 16)
+    return tiles >= 3 * num_sms ? launch<FMT, 4, 2, 8, GATED, BF>(p, stream) : launch<FMT, 1, 2, 8, GATED, BF>(p, stream);
+  return tiles >= 2 * num_sms ? launch<FMT, 2, 4, 8, GATED, BF>(p, stream) : launch<FMT, 1, 4, 8, GATED, BF>(p, stream);
 }
 
 std::atomic<bool> g_any{false};

@@ -448,7 +448,7 @@ typedef enum { OZK_SILU = 0, OZK_GELU = 1, OZK_GELU_TANH = 2 } ozk_activation;
  * that past some 32 quantised rows and ozk_mx4_grouped_gemm are faster.  Y: T x
  * N of OZK_BF16, OZK_F16 or OZK_F32, ldy >= N, any alignment of its own type;
  * it must overlap nothing.  x is used exactly, whatever its range; sums are
- * formed in fp32 (with MXFP4 scales above 2^100 one may overflow where its
+ * formed in fp32 (with MXFP4 scales above 2^96 one may overflow where its
  * result would not).  K = 0 gives zeros. */
 int ozk_mx4_gemv(int64_t T, int64_t N, int64_t K, int groups, const int32_t* offsets, const void* X, int64_t ldx,
                  int dtype, const uint8_t* w_codes, const uint8_t* w_scales, int format, float alpha, void* Y,
