@@ -6,7 +6,8 @@
 //
 // Five elements move for one of dh: bound by HBM, 10 T M bytes.  A warp takes a
 // row's run of up to 1024 columns with 16-byte accesses, all three loads of four
-// vectors ahead of the stores.
+// vectors ahead of the stores.  Where the gradient of x follows, the kernel also
+// clears its rows in no group, which the product leaves as they are.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -32,6 +33,9 @@ struct GradParams {
   const int32_t* offsets;
   const uint16_t *dh, *slopes;
   uint16_t* out;
+  uint16_t* clear;   // T x K, or null: rows in no group are set to zero
+  int64_t ldc;
+  int K;
 };
 
 // The rows of the groups: they follow one another from the first offset to the
@@ -65,6 +69,16 @@ __device__ __forceinline__ uint4 load16(const uint16_t* p) {
   uint4 v;
   asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
   return v;
+}
+
+// Zeros into row `row` of what is to be cleared: the whole warp.
+__device__ __forceinline__ void clear_row(const GradParams& p, int64_t row, int lane) {
+  uint16_t* to = p.clear + row * p.ldc;
+  const int head = min(p.K, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(to) & 15)) / 2 % 8));
+  for (int c = lane; c < head; c += 32) to[c] = 0;
+  const int vectors = (p.K - head) / 8;
+  for (int v = lane; v < vectors; v += 32) *reinterpret_cast<uint4*>(to + head + 8 * v) = make_uint4(0u, 0u, 0u, 0u);
+  for (int c = head + 8 * vectors + lane; c < p.K; c += 32) to[c] = 0;
 }
 
 // VEC: rows and halves of dpre that start on 16 bytes; else element by element.
@@ -109,6 +123,10 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const GradParams p
       }
     }
   }
+  if (p.clear == nullptr) return;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); r < span.x + (p.T - span.y); r += step)
+    clear_row(p, r < span.x ? r : r - span.x + span.y, lane);
 }
 
 std::atomic<bool> g_any{false};
@@ -131,6 +149,9 @@ cudaError_t launch_gated_grad(const GatedGrad& q, int num_sms, cudaStream_t stre
   p.dh = static_cast<const uint16_t*>(q.dh);
   p.slopes = static_cast<const uint16_t*>(q.slopes);
   p.out = static_cast<uint16_t*>(q.out);
+  p.clear = static_cast<uint16_t*>(q.clear);
+  p.ldc = q.ldc;
+  p.K = static_cast<int>(q.K);
   auto aligned = [](const void* a) { return reinterpret_cast<uintptr_t>(a) % 16 == 0; };
   const bool vec = aligned(q.dh) && aligned(q.slopes) && aligned(q.out) && q.M % 8 == 0 && (q.T == 1 || q.lddh % 8 == 0) &&
                    (q.T == 1 || q.lds % 8 == 0) && q.slope_plane % 8 == 0 && (q.T == 1 || q.ldo % 8 == 0);

@@ -69,6 +69,8 @@ struct GatedGrad {
   int64_t lddh, lds, slope_plane;
   void* out;
   int64_t ldo;
+  void* clear;  // T x K, rows ldc apart: zeros for rows in no group; or null
+  int64_t K, ldc;
 };
 cudaError_t launch_gated_grad(const GatedGrad& q, int num_sms, cudaStream_t stream);
 int take_gated_status(int* status);  // the stream is idle; bit 1: bad group offsets

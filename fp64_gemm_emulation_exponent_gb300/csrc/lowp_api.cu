@@ -330,8 +330,44 @@ int ozk_gated_grad(int64_t T, int64_t N, int groups, const int32_t* offsets, con
     return OZK_ERR_INVALID_ARG;
   int sms = 0;
   if ((rc = current_device_supported(&sms))) return rc;
-  const GatedGrad q = {T, N, groups, offsets, dtype, dH, slopes, lddh, lds, slope_stride, dpre, ldp};
+  const GatedGrad q = {T, N, groups, offsets, dtype, dH, slopes, lddh, lds, slope_stride, dpre, ldp, nullptr, 0, 0};
   return launch_gated_grad(q, sms, stream) == cudaSuccess ? OZK_OK : OZK_ERR_CUDA;
+}
+
+int ozk_grouped_gated_gemm_grad(int64_t T, int64_t N, int64_t K, int groups, const int32_t* offsets, const void* dH,
+                                int64_t lddh, const void* slopes, int64_t lds, int64_t slope_stride, const void* X,
+                                int64_t ldx, const void* W, int64_t ldw, int64_t w_stride, int dtype, void* dpre,
+                                int64_t ldp, void* dX, int64_t lddx, void* dW, int64_t lddw, int64_t dw_stride,
+                                ozk_stream_t stream) {
+  int rc = check_grouped(T, N, K, groups, offsets, dtype, dtype);
+  if (rc) return rc;
+  if (2 * N > kMaxFeatures) return OZK_ERR_UNSUPPORTED;
+  if (T > 0 && N > 0) {
+    if (!dH || lddh < N || reinterpret_cast<uintptr_t>(dH) % 2 != 0) return OZK_ERR_INVALID_ARG;
+    if ((rc = check_slopes(slopes, T, N, lds, slope_stride)) || (rc = check_operand(dpre, 2 * N, ldp))) return rc;
+    const Span d = span(dpre, T, 2 * N, ldp, 2), h = span(dH, T, N, lddh, 2), s = span(slopes, T, N, lds, 2, 2, slope_stride);
+    if (overlap(d, h) || overlap(d, s) || overlap(d, span(X, T, K, ldx, 2)) ||
+        overlap(d, span(W, 2 * N, K, ldw, 2, groups, w_stride)))
+      return OZK_ERR_INVALID_ARG;
+    if (dX && K > 0) {
+      const Span x = span(dX, T, K, lddx, 2);
+      if (overlap(x, h) || overlap(x, s)) return OZK_ERR_INVALID_ARG;  // cleared while they are read
+      if ((rc = check_weights(W, 2 * N, K, ldw, groups, w_stride))) return rc;
+    }
+    if (dW && K > 0 && (rc = check_operand(X, K, ldx))) return rc;
+  }
+  if (dX && T > 0 && K > 0 && (lddx < K || reinterpret_cast<uintptr_t>(dX) % 2 != 0)) return OZK_ERR_INVALID_ARG;
+  if (dW && N > 0 && K > 0 && (lddw < K || (groups > 1 && dw_stride < (2 * N - 1) * lddw + K))) return OZK_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((rc = current_device_supported(&sms))) return rc;
+  if (T > 0 && (N > 0 || (dX && K > 0))) {
+    const GatedGrad q = {T, N, groups, offsets, dtype, dH, slopes, lddh, lds, slope_stride, dpre, ldp, K > 0 ? dX : nullptr, K, lddx};
+    if (launch_gated_grad(q, sms, stream) != cudaSuccess) return OZK_ERR_CUDA;
+  }
+  if (dX && (rc = ozk_grouped_gemm_dx(T, 2 * N, K, groups, offsets, dpre, ldp, W, ldw, w_stride, dtype, dX, lddx, dtype, stream)))
+    return rc;
+  return dW ? ozk_grouped_gemm_dw(T, 2 * N, K, groups, offsets, dpre, ldp, X, ldx, dtype, dW, lddw, dw_stride, dtype, stream)
+            : OZK_OK;
 }
 
 int ozk_grouped_gemm_dx(int64_t T, int64_t N, int64_t K, int groups, const int32_t* offsets, const void* dY,

@@ -80,6 +80,8 @@ SIGNATURES = {
                                   _i32, _vp]),
     "ozk_grouped_gated_gemm": (_i32, [_i64, _i64, _i64, _i32, _vp, _vp, _i64, _vp, _i64, _i64, _i32, _i32, _vp, _i64, _vp,
                                       _i64, _i64, _vp]),
+    "ozk_grouped_gated_gemm_grad": (_i32, [_i64, _i64, _i64, _i32, _vp, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64,
+                                           _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp]),
     "ozk_gated_grad": (_i32, [_i64, _i64, _i32, _vp, _vp, _i64, _vp, _i64, _i64, _i32, _vp, _i64, _vp]),
     "ozk_withhold_next_product": (_i32, [_i32, _i32, _i32, ctypes.c_uint32]),
     "ozk_event_create": (_i32, [_vp]),
@@ -826,7 +828,9 @@ def _load_gated():
         @staticmethod
         def forward(ctx, x, w, offsets, activation):
             T, H = x.shape[0], w.shape[1] // 2
-            slopes = _torch.empty((2, T, -(-H // 8) * 8), dtype=x.dtype, device=x.device)[:, :, :H]
+            slopes = _torch.empty((2, T, -(-H // 8) * 8), dtype=x.dtype, device=x.device)
+            if H % 8:
+                slopes = slopes[:, :, :H]
             ctx.save_for_backward(x, w, offsets, slopes)
             return grouped_gated_gemm(x, w, offsets, activation, slopes=slopes)
 
@@ -834,14 +838,7 @@ def _load_gated():
         @_torch.autograd.function.once_differentiable
         def backward(ctx, dh):
             x, w, offsets, slopes = ctx.saved_tensors
-            (T, H), dx, dw = dh.shape, None, None
-            # rows that bulk copies can read
-            room = _torch.empty((T, -(-2 * H // 8) * 8), dtype=x.dtype, device=x.device)
-            dpre = gated_grad(dh, slopes, offsets, out=room[:, : 2 * H])
-            if ctx.needs_input_grad[0]:
-                dx = grouped_gemm_dx(dpre, w, offsets, out=_torch.zeros(x.shape, dtype=x.dtype, device=x.device))
-            if ctx.needs_input_grad[1]:
-                dw = grouped_gemm_dw(dpre, x, offsets)
+            dx, dw = grouped_gated_gemm_grad(dh, x, w, offsets, slopes, *ctx.needs_input_grad[:2])
             return dx, dw, None, None
 
     _GatedGemm = GatedGemm
@@ -855,10 +852,9 @@ def grouped_gated_gemm(x, w, offsets, activation: str = "silu", out=None, slopes
     their type.  Rows in no group are not written.  slopes, a [2, T, H] tensor,
     takes dh/dgate and dh/dup, which gated_grad turns a gradient of h with.
 
-    Autograd records it where x or w asks for a gradient (gated_grad, then
-    grouped_gemm_dx and grouped_gemm_dw where asked for; zeros for rows in no
-    group), once: there is no second derivative.  With out or slopes given no
-    graph is recorded."""
+    Autograd records it where x or w asks for a gradient
+    (grouped_gated_gemm_grad), once: there is no second derivative.  With out or
+    slopes given no graph is recorded."""
     groups, N, K, ldw, stride = _groups(w)
     _, kind, index = _grouped(x, w, offsets, groups)
     act = _activation(activation)
@@ -890,6 +886,15 @@ def _slopes(slopes, T, H, dtype, index):
     return (slopes.data_ptr(), *_groups(slopes)[3:])
 
 
+def _plain_rows(t, dtype):
+    """(t, leading dimension), t rounded to dtype and laid out in rows where it is not (an expanded gradient)."""
+    (rows, cols), (sr, sc) = t.shape, t.stride()
+    if t.dtype != dtype or sc != 1 and cols > 1 or sr < cols and rows > 1:
+        t = t.to(dtype).contiguous()
+        return t, cols or 1
+    return t, sr if rows > 1 else _one_row(cols)
+
+
 def gated_grad(dh, slopes, offsets=None, out=None, stream=None):
     """The gradient with respect to a gated product's two projections
     (ozk_gated_grad): dh [T, H] times each of slopes [2, T, H], side by side,
@@ -908,15 +913,47 @@ def gated_grad(dh, slopes, offsets=None, out=None, stream=None):
         raise ValueError("expected a 2-D gradient")
     T, H = dh.shape
     at, lds, plane = _slopes(slopes, T, H, slopes.dtype, index)
-    if dh.dtype != slopes.dtype or dh.stride(1) != 1 and H > 1 or dh.stride(0) < H and T > 1:
-        with _torch.cuda.stream(stream):  # converted where the call runs; an expanded gradient is laid out
-            dh = dh.to(slopes.dtype).contiguous()
     out, ld, kind = _result(out, T, 2 * H, slopes.dtype, slopes.device, stream)
-    rc = _lib.ozk_gated_grad(T, H, groups, None if offsets is None else offsets.data_ptr(), dh.data_ptr(), _rows(dh)[2],
-                             at, lds, plane, kind, out.data_ptr(), ld, _stream_at(index, stream))
+    with _torch.cuda.stream(stream):
+        dh, lddh = _plain_rows(dh, slopes.dtype)
+        rc = _lib.ozk_gated_grad(T, H, groups, None if offsets is None else offsets.data_ptr(), dh.data_ptr(), lddh, at, lds,
+                                 plane, kind, out.data_ptr(), ld, _stream_at(index, stream))
     if rc:
         raise OzkError("ozk_gated_grad", rc)
     return out
+
+
+def grouped_gated_gemm_grad(dh, x, w, offsets, slopes, need_dx: bool = True, need_dw: bool = True, stream=None):
+    """(dx, dw) of grouped_gated_gemm from the gradient of its result and the
+    slopes that it kept (ozk_grouped_gated_gemm_grad), both of x's type (dh of
+    another type is rounded to it); None for one that is not asked for.  dx is
+    zero in rows of no group, dw [groups, 2 H, K] for groups without rows."""
+    groups, N, K, ldw, stride = _groups(w)
+    _, kind, index = _grouped(x, w, offsets, groups)
+    if index != _current_device():
+        with _torch.cuda.device(index):
+            return grouped_gated_gemm_grad(dh, x, w, offsets, slopes, need_dx, need_dw, stream)
+    T, k, ldx = _rows(x)
+    if k != K or N % 2:
+        raise ValueError(f"x is {tuple(x.shape)}, the weights {tuple(w.shape)}")
+    if dh.shape != (T, N // 2):
+        raise ValueError(f"the gradient has shape {tuple(dh.shape)}, the result ({T}, {N // 2})")
+    _same_device(index, dh)
+    at, lds, plane = _slopes(slopes, T, N // 2, x.dtype, index)
+    torch, kw = _torch, {"dtype": x.dtype, "device": x.device}
+    with torch.cuda.stream(stream):
+        dh, lddh = _plain_rows(dh, x.dtype)
+        ldp = -(-N // 8) * 8  # rows that bulk copies can read
+        dpre = torch.empty((T, ldp), **kw)
+        dx = torch.empty((T, K), **kw) if need_dx else None
+        dw = torch.empty((groups, N, K), **kw) if need_dw else None
+        rc = _lib.ozk_grouped_gated_gemm_grad(
+            T, N // 2, K, groups, offsets.data_ptr(), dh.data_ptr(), lddh, at, lds, plane, x.data_ptr(), ldx, w.data_ptr(),
+            ldw, stride, kind, dpre.data_ptr(), ldp, dx.data_ptr() if need_dx else None, K or 1,
+            dw.data_ptr() if need_dw else None, K or 1, N * (K or 1), _stream_at(index, stream))
+    if rc:
+        raise OzkError("ozk_grouped_gated_gemm_grad", rc)
+    return dx, dw
 
 
 # ---------------------------------------------------------------- events

@@ -257,3 +257,28 @@ def test_refusals():
         ozk.gated_grad(torch.empty(16, 32, dtype=x.dtype), slopes)
     with pytest.raises(ozk.OzkError):
         ozk.gated_grad(slopes[0], slopes, out=torch.empty(0, dtype=x.dtype, device="cuda").set_(slopes.untyped_storage(), 0, (16, 64)))
+
+
+@pytest.mark.parametrize("H,K", [(61, 72), (64, 40)])
+def test_backward_pass_in_one_call(H, K):
+    """It is gated_grad and both products, with zeros where a row has no group and a group no rows; what is not asked
+    for is not computed."""
+    x, w, offsets, starts = setup([9, 0, 40], H, K, torch.bfloat16, before=3, after=6)
+    T = x.shape[0]
+    slopes = normal(2, T, H, seed=4, dtype=x.dtype)
+    dh = normal(T, H, seed=3, dtype=torch.float32)
+    torch.full((1 << 18,), float("nan"), device="cuda", dtype=torch.bfloat16)  # what unwritten memory would hold
+    room = torch.zeros(T, -(-2 * H // 8) * 8, dtype=x.dtype, device="cuda")
+    dpre = ozk.gated_grad(dh, slopes, offsets, out=room[:, : 2 * H])
+    want_x = ozk.grouped_gemm_dx(dpre, w, offsets, out=torch.zeros(T, K, dtype=x.dtype, device="cuda"))
+    want_w = ozk.grouped_gemm_dw(dpre, x, offsets)
+    dx, dw = ozk.grouped_gated_gemm_grad(dh, x, w, offsets, slopes)
+    assert torch.equal(dx, want_x) and torch.equal(dw, want_w) and not dw[1].any()
+    assert ozk.grouped_gated_gemm_grad(dh, x, w, offsets, slopes, need_dw=False)[1] is None
+    dx, dw = ozk.grouped_gated_gemm_grad(dh, x, w, offsets, slopes, need_dx=False)
+    assert dx is None and torch.equal(dw, want_w)
+    with pytest.raises(ValueError):
+        ozk.grouped_gated_gemm_grad(dh[:, :H - 1], x, w, offsets, slopes)
+    with pytest.raises(ValueError):
+        ozk.grouped_gated_gemm_grad(dh, x, w, offsets, slopes[:, :, : H - 1])
+    assert ozk.ozk_stream_status() == 0
