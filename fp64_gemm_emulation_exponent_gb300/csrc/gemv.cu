@@ -62,15 +62,16 @@ struct Shape {
   static constexpr int PIECES = ROW / 16;
   static constexpr int WORDS = CHUNK / (NV ? 64 : 128);  // scale words of a row
   static constexpr int CODES = R * 16 * ROW;
-  static constexpr int SCALES = (R * 16 * WORDS * 4 + 255) / 256 * 256;  // rows of x start on 256 bytes
+  static constexpr int SCALES = (R * 16 * WORDS * 4 + 255) / 256 * 256;
   static constexpr int XROW = CHUNK * 2;          // bytes of a row of x
-  static constexpr int DEPTH = FEW ? (R == 1 ? 3 : 2) : R == 4 || NT == 4 ? 2 : 4;
-  static constexpr int SUMS = R * TILES * 512;    // bytes of a warp's sums
-  static_assert(!FEW || W * DEPTH * (CODES + SCALES) % 512 == 0, "rows of x start on 512 bytes");
-  static constexpr int stage(int tokens) { return CODES + SCALES + (FEW ? 0 : tokens * XROW); }
-  static constexpr int bytes(int tokens) {
-    return W * (DEPTH * stage(tokens) + SUMS + (FEW ? tokens * XROW : 0));
-  }
+  static constexpr int DEPTH = FEW && R == 1 ? 3 : 2;
+  static constexpr int STAGE = CODES + SCALES;
+  static constexpr int SUMS = R * TILES * 512;    // bytes of a warp's sums, at its end in the ring's place
+  // A warp's part of shared memory: its ring, and the rows of x of one chunk.
+  static constexpr int RING = (DEPTH * STAGE + 511) / 512 * 512;
+  static constexpr int part(int tokens) { return RING + tokens * XROW; }
+  static constexpr int bytes(int tokens) { return W * part(tokens); }
+  static_assert(SUMS <= RING, "the sums take the ring's place");
 };
 
 struct GemvParams {
@@ -204,12 +205,13 @@ __device__ __forceinline__ Found find_group(const GemvParams& p, int rank) {
 }
 
 // Elements [k, k + 8) of a row of x as stored, zeros from K on, at any alignment.
+__device__ __forceinline__ uint4 load16(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint4 load8(const uint16_t* row, int k, int K, bool vec) {
-  if (vec && k + 8 <= K) {
-    uint4 v;
-    asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(row + k) : "memory");
-    return v;
-  }
+  if (vec && k + 8 <= K) return load16(row + k);
   uint32_t e[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) e[i] = k + i < K ? row[k + i] : 0u;
@@ -290,7 +292,7 @@ __device__ __forceinline__ uint4 to_half2(uint4 v, uint32_t factor) {
 }
 
 // Blocks of an SM that registers are kept for.
-constexpr int blocks_of(int R, int NT, int W) { return (NT == 0 ? R == 1 ? 24 : 16 : R * NT > 4 ? 8 : 16) / W; }
+constexpr int blocks_of(int R, int NT, int W) { return (NT == 0 && R == 1 ? 24 : 16) / W; }
 
 template <int FMT, int R, int NT, int W, bool GATED, bool BF>
 __global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const GemvParams p) {
@@ -319,14 +321,12 @@ __global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const
   const uint8_t* codes = p.codes + group_row * (p.kpad / 2);
   const uint8_t* scales = p.scales + (group_row / 128 + e) * p.words * 512;
 
-  // A warp's ring: stages of codes, scale words and (not FEW) p.tokens rows of
-  // x.  Then the warps' sums, and where FEW those rows as fp16.  16-byte
-  // pieces are swapped within a row so that the rows that are read together lie
-  // in different banks.
-  const uint32_t stage = static_cast<uint32_t>(S::stage(p.tokens));
-  const uint32_t ring = smem_addr(smem) + static_cast<uint32_t>(warp * S::DEPTH) * stage;
-  float* sums = reinterpret_cast<float*>(smem + W * S::DEPTH * stage);
-  const uint32_t x16 = smem_addr(sums) + W * S::SUMS + static_cast<uint32_t>(warp * p.tokens * S::XROW);
+  // A warp's ring of codes and scale words, and one chunk's rows of x (FEW: as
+  // fp16; else as they came).  16-byte pieces are swapped within a row so that
+  // the rows that are read together lie in different banks.
+  const uint32_t part_bytes = static_cast<uint32_t>(S::part(p.tokens));
+  const uint32_t ring = smem_addr(smem) + static_cast<uint32_t>(warp) * part_bytes;
+  const uint32_t xat = ring + S::RING;
   const int chunks = (p.kpad + S::CHUNK - 1) / S::CHUNK;
   auto code_piece = [](int r, int piece) {
     return static_cast<uint32_t>(r * S::ROW + ((piece ^ (S::FEW ? r & 7 : r >> 1 & 3)) * 16));
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const
     const int tokens = min(S::TOKENS, rows - t0);
     const uint16_t* x = p.x + (static_cast<int64_t>(row0) + t0) * p.ldx;
     auto fetch = [&](int chunk, int slot) {
-      const uint32_t at = ring + static_cast<uint32_t>(slot) * stage;
+      const uint32_t at = ring + static_cast<uint32_t>(slot * S::STAGE);
       const uint8_t* from = src + static_cast<int64_t>(chunk) * S::ROW;
       const uint8_t* sfrom = scales + static_cast<int64_t>(chunk) * S::WORDS * 512;
       auto code = [&](int j) {
@@ -390,28 +390,34 @@ __global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const
             copy4(at + S::CODES + i * 4, sfrom + ssrc[j]);
         }
       }
-      if (!S::FEW) {
-        const int k = chunk * S::CHUNK + (lane & 15) * 8;
-        const uint32_t to = at + S::CODES + S::SCALES + x_piece(lane >> 4, lane & 15);
-        const uint16_t* row = x + (lane >> 4) * p.ldx + k;
-        if (p.vec && (chunk + 1) * S::CHUNK <= p.K) {
-#pragma unroll
-          for (int i = 0; i < S::TOKENS / 2; ++i)
-            if (2 * i + (lane >> 4) < tokens) copy16(to + i * 2 * S::XROW, row + i * 2 * p.ldx);
-        } else {
-#pragma unroll 1
-          for (int i = 0; 2 * i + (lane >> 4) < tokens; ++i) sts128(to + i * 2 * S::XROW, load8(row + i * 2 * p.ldx - k, k, p.K, false));
-        }
-      }
     };
-    // FEW: this lane's eight elements of every row of a chunk.
+    // The chunk's rows of x: to shared memory, or FEW this lane's eight elements of every row.
     uint4 xr[4];
     auto fetch_x = [&](int chunk) {
+      const bool whole = p.vec && (chunk + 1) * S::CHUNK <= p.K;
+      if (S::FEW) {
+        const int k = chunk * S::CHUNK + lane * 8;
+        const uint16_t* row = x + k;
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-        if (t < tokens) xr[t] = load8(x + t * p.ldx, chunk * S::CHUNK + lane * 8, p.K, p.vec);
+        for (int t = 0; t < 4; ++t) {
+          if (t >= tokens) break;
+          xr[t] = whole ? load16(row) : load8(row - k, k, p.K, p.vec);
+          row += p.ldx;
+        }
+        return;
+      }
+      const int k = chunk * S::CHUNK + (lane & 15) * 8;
+      const uint32_t to = xat + x_piece(lane >> 4, lane & 15);
+      const uint16_t* row = x + (lane >> 4) * p.ldx + k;
+      if (whole) {
+#pragma unroll
+        for (int i = 0; i < S::TOKENS / 2; ++i)
+          if (2 * i + (lane >> 4) < tokens) copy16(to + i * 2 * S::XROW, row + i * 2 * p.ldx);
+      } else {
+#pragma unroll 1
+        for (int i = 0; 2 * i + (lane >> 4) < tokens; ++i) sts128(to + i * 2 * S::XROW, load8(row + i * 2 * p.ldx - k, k, p.K, p.vec));
+      }
     };
-
     float acc[R][TILES][4];
     auto clear = [&]() {
 #pragma unroll
@@ -428,9 +434,11 @@ __global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const
 #pragma unroll
     for (int n = 0; n < S::ROWS; ++n) E[n] = 0, factor[n] = 0u;
     bool kept = false;  // sums of an earlier scale have been put away
-    float* mine = sums + warp * (S::SUMS / 4) + lane;
-    // Puts the sums away without their scale (2^shift(E - down)); rows 2 q, 2 q + 1 of a tile are this lane's columns.
-    auto put_away = [&](int down) {
+    volatile float away[R * TILES * 4];  // in local memory: hardly ever used
+    // Puts the sums away without their scale (2^shift(E - down)), at last into the ring's place; rows 2 q, 2 q + 1 of a
+    // tile are this lane's columns.
+    float* mine = reinterpret_cast<float*>(smem + static_cast<size_t>(warp) * part_bytes) + lane;
+    auto put_away = [&](int down, bool last) {
 #pragma unroll
       for (int n = 0; n < TILES; ++n) {
 #pragma unroll
@@ -442,9 +450,11 @@ __global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const
           for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int h = 0; h < 4; h += 2) {
-              float* at = mine + ((i * TILES + n) * 4 + c + h) * 32;
-              const float v = BF ? scaled(acc[i][n][c + h], back) : acc[i][n][c + h];
-              *at = kept ? *at + v : v;
+              const int at = (i * TILES + n) * 4 + c + h;
+              float v = BF ? scaled(acc[i][n][c + h], back) : acc[i][n][c + h];
+              if (kept) v += away[at];
+              if (last) mine[at * 32] = v;
+              else away[at] = v;
             }
         }
       }
@@ -458,18 +468,18 @@ __global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const
       copy_commit();
       next += W;
     }
-    if (S::FEW && warp < chunks) fetch_x(warp);
+    if (warp < chunks) fetch_x(warp);
+    if (!S::FEW) copy_commit();
     int slot = 0;
 #pragma unroll 1
     for (int chunk = warp; chunk < chunks; chunk += W) {
       __syncwarp();  // the slot that was used before this one is free
       if (next < chunks) fetch(next, slot == 0 ? S::DEPTH - 1 : slot - 1);
       copy_commit();
-      copy_wait<S::DEPTH - 1>();
+      copy_wait<S::DEPTH - 1>();  // all but the latest are in, x among them
       __syncwarp();
       next += W;
-      const uint32_t at = ring + static_cast<uint32_t>(slot) * stage;
-      const uint32_t xat = S::FEW ? x16 : at + S::CODES + S::SCALES;
+      const uint32_t at = ring + static_cast<uint32_t>(slot * S::STAGE);
 
       // One pass over the chunk's weights; part: only elements of x with exponents from E - down to kBelow below it.
       // Lanes of rows that are not there read the last one; their sums are nobody's.
@@ -554,9 +564,9 @@ __global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           if (t >= tokens) break;
-          if (!BF) sts128(x16 + x_piece(t, lane), xr[t]);
-          else if (!part) sts128(x16 + x_piece(t, lane), to_half2(xr[t], factor[t]));
-          else sts128(x16 + x_piece(t, lane), to_half2(only(xr[t], E[t] - down), factor_of(E[t] - down)));
+          if (!BF) sts128(xat + x_piece(t, lane), xr[t]);
+          else if (!part) sts128(xat + x_piece(t, lane), to_half2(xr[t], factor[t]));
+          else sts128(xat + x_piece(t, lane), to_half2(only(xr[t], E[t] - down), factor_of(E[t] - down)));
         }
         __syncwarp();
       };
@@ -581,7 +591,7 @@ __global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const
         }
         if (!__all_sync(0xFFFFFFFFu, fits)) {
           if (chunk != warp) {
-            put_away(0);
+            put_away(0, false);
             clear();
           }
           bool small = false;
@@ -608,25 +618,29 @@ __global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const
         if (S::FEW) stage_x(part, down);
         pass(part, down);
         if (!BF || !part) break;
-        put_away(down);
+        put_away(down, false);
         clear();
         bool left = false;
 #pragma unroll
         for (int n = 0; n < S::ROWS; ++n) left = left || low[n] < E[n] - down - kBelow;
         if (!__any_sync(0xFFFFFFFFu, left)) break;
       }
-      if (S::FEW && chunk + W < chunks) fetch_x(chunk + W);
+      if (!S::FEW) __syncwarp();
+      if (chunk + W < chunks) fetch_x(chunk + W);
+      if (!S::FEW) copy_commit();
       slot = slot + 1 == S::DEPTH ? 0 : slot + 1;
     }
-    put_away(0);
     copy_wait<0>();
+    __syncwarp();
+    put_away(0, true);
 
     // ---- the warps' sums, in order
     __syncthreads();
     auto sum = [&](int i, int n, int c, int l) {
       float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < W; ++w) v += sums[w * (S::SUMS / 4) + ((i * TILES + n) * 4 + c) * 32 + l];
+      for (int w = 0; w < W; ++w)
+        v += reinterpret_cast<const float*>(smem + static_cast<size_t>(w) * part_bytes)[((i * TILES + n) * 4 + c) * 32 + l];
       return v;
     };
     constexpr int kRows = S::FEW ? 4 : 8;  // rows of x of a tile that can be there
@@ -643,7 +657,7 @@ __global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const
       else if (p.out_type == OZK_F16) static_cast<__half*>(p.y)[to] = __float2half_rn(v);
       else static_cast<__nv_bfloat16*>(p.y)[to] = __float2bfloat16_rn(v);
     }
-    if (t0 + S::TOKENS < rows) __syncthreads();  // the sums' places are used again
+    if (t0 + S::TOKENS < rows) __syncthreads();  // the rings are filled again
   }
 }
 
@@ -689,8 +703,8 @@ cudaError_t choose(const GemvParams& p, int num_sms, cudaStream_t stream) {
     return launch<FMT, 1, 1, 8, GATED, BF>(p, stream);
   }
   if (rows <= 16)
-    return tiles >= 3 * num_sms ? launch<FMT, 4, 2, 8, GATED, BF>(p, stream) : launch<FMT, 1, 2, 8, GATED, BF>(p, stream);
-  return tiles >= 2 * num_sms ? launch<FMT, 2, 4, 8, GATED, BF>(p, stream) : launch<FMT, 1, 4, 8, GATED, BF>(p, stream);
+    return tiles >= 3 * num_sms ? launch<FMT, 4, 2, 16, GATED, BF>(p, stream) : launch<FMT, 1, 2, 8, GATED, BF>(p, stream);
+  return tiles >= 2 * num_sms ? launch<FMT, 2, 4, 16, GATED, BF>(p, stream) : launch<FMT, 1, 4, 8, GATED, BF>(p, stream);
 }
 
 std::atomic<bool> g_any{false};

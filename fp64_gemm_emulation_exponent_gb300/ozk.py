@@ -826,13 +826,14 @@ def _load_gated():
 
     class GatedGemm(_torch.autograd.Function):
         @staticmethod
-        def forward(ctx, x, w, offsets, activation):
-            T, H = x.shape[0], w.shape[1] // 2
-            slopes = _torch.empty((2, T, -(-H // 8) * 8), dtype=x.dtype, device=x.device)
-            if H % 8:
-                slopes = slopes[:, :, :H]
-            ctx.save_for_backward(x, w, offsets, slopes)
-            return grouped_gated_gemm(x, w, offsets, activation, slopes=slopes)
+        def forward(ctx, x, w, offsets, args):
+            T, H = args[:2]
+            room = -(-H // 8) * 8
+            slopes = _torch.empty((2, T, room), dtype=x.dtype, device=x.device)
+            h = _torch.empty((T, H), dtype=x.dtype, device=x.device)
+            _gated(args, h.data_ptr(), H or 1, slopes.data_ptr(), room, T * room)
+            ctx.save_for_backward(x, w, offsets, slopes if room == H else slopes[:, :, :H])
+            return h
 
         @staticmethod
         @_torch.autograd.function.once_differentiable
@@ -861,19 +862,27 @@ def grouped_gated_gemm(x, w, offsets, activation: str = "silu", out=None, slopes
     if index != _current_device():
         with _torch.cuda.device(index):
             return grouped_gated_gemm(x, w, offsets, activation, out, slopes, stream)
-    if out is None and slopes is None and (x.requires_grad or w.requires_grad) and _torch.is_grad_enabled():
-        with _torch.cuda.stream(stream):
-            return (_GatedGemm or _load_gated()).apply(x, w, offsets, activation)
     T, k, ldx = _rows(x)
     if k != K or N % 2:
         raise ValueError(f"x is {tuple(x.shape)}, the weights {tuple(w.shape)}")
+    args = (T, N // 2, K, groups, offsets.data_ptr(), x.data_ptr(), ldx, w.data_ptr(), ldw, stride, kind, act,
+            _stream_at(index, stream))
+    if out is None and slopes is None and (x.requires_grad or w.requires_grad) and _torch.is_grad_enabled():
+        function = _GatedGemm or _load_gated()
+        if stream is None:
+            return function.apply(x, w, offsets, args)
+        with _torch.cuda.stream(stream):
+            return function.apply(x, w, offsets, args)
     out, ld, _ = _result(out, T, N // 2, x.dtype, x.device, stream)
     at, lds, plane = (None, 0, 0) if slopes is None else _slopes(slopes, T, N // 2, x.dtype, index)
-    rc = _lib.ozk_grouped_gated_gemm(T, N // 2, K, groups, offsets.data_ptr(), x.data_ptr(), ldx, w.data_ptr(), ldw,
-                                     stride, kind, act, out.data_ptr(), ld, at, lds, plane, _stream_at(index, stream))
+    _gated(args, out.data_ptr(), ld, at, lds, plane)
+    return out
+
+
+def _gated(args, out, ld, slopes, lds, plane):
+    rc = _lib.ozk_grouped_gated_gemm(*args[:-1], out, ld, slopes, lds, plane, args[-1])
     if rc:
         raise OzkError("ozk_grouped_gated_gemm", rc)
-    return out
 
 
 def _slopes(slopes, T, H, dtype, index):
@@ -913,11 +922,13 @@ def gated_grad(dh, slopes, offsets=None, out=None, stream=None):
         raise ValueError("expected a 2-D gradient")
     T, H = dh.shape
     at, lds, plane = _slopes(slopes, T, H, slopes.dtype, index)
-    out, ld, kind = _result(out, T, 2 * H, slopes.dtype, slopes.device, stream)
-    with _torch.cuda.stream(stream):
-        dh, lddh = _plain_rows(dh, slopes.dtype)
-        rc = _lib.ozk_gated_grad(T, H, groups, None if offsets is None else offsets.data_ptr(), dh.data_ptr(), lddh, at, lds,
-                                 plane, kind, out.data_ptr(), ld, _stream_at(index, stream))
+    if stream is not None:  # what is allocated belongs to the stream that writes it
+        with _torch.cuda.stream(stream):
+            return gated_grad(dh, slopes, offsets, out)
+    out, ld, kind = _result(out, T, 2 * H, slopes.dtype, slopes.device, None)
+    dh, lddh = _plain_rows(dh, slopes.dtype)
+    rc = _lib.ozk_gated_grad(T, H, groups, None if offsets is None else offsets.data_ptr(), dh.data_ptr(), lddh, at, lds, plane,
+                             kind, out.data_ptr(), ld, _current_stream(index))
     if rc:
         raise OzkError("ozk_gated_grad", rc)
     return out
@@ -940,17 +951,19 @@ def grouped_gated_gemm_grad(dh, x, w, offsets, slopes, need_dx: bool = True, nee
         raise ValueError(f"the gradient has shape {tuple(dh.shape)}, the result ({T}, {N // 2})")
     _same_device(index, dh)
     at, lds, plane = _slopes(slopes, T, N // 2, x.dtype, index)
-    torch, kw = _torch, {"dtype": x.dtype, "device": x.device}
-    with torch.cuda.stream(stream):
-        dh, lddh = _plain_rows(dh, x.dtype)
-        ldp = -(-N // 8) * 8  # rows that bulk copies can read
-        dpre = torch.empty((T, ldp), **kw)
-        dx = torch.empty((T, K), **kw) if need_dx else None
-        dw = torch.empty((groups, N, K), **kw) if need_dw else None
-        rc = _lib.ozk_grouped_gated_gemm_grad(
-            T, N // 2, K, groups, offsets.data_ptr(), dh.data_ptr(), lddh, at, lds, plane, x.data_ptr(), ldx, w.data_ptr(),
-            ldw, stride, kind, dpre.data_ptr(), ldp, dx.data_ptr() if need_dx else None, K or 1,
-            dw.data_ptr() if need_dw else None, K or 1, N * (K or 1), _stream_at(index, stream))
+    if stream is not None:  # what is allocated belongs to the stream that writes it
+        with _torch.cuda.stream(stream):
+            return grouped_gated_gemm_grad(dh, x, w, offsets, slopes, need_dx, need_dw)
+    empty, dtype, device = _torch.empty, x.dtype, x.device
+    dh, lddh = _plain_rows(dh, dtype)
+    ldp = -(-N // 8) * 8  # rows that bulk copies can read
+    dpre = empty((T, ldp), dtype=dtype, device=device)
+    dx = empty((T, K), dtype=dtype, device=device) if need_dx else None
+    dw = empty((groups, N, K), dtype=dtype, device=device) if need_dw else None
+    rc = _lib.ozk_grouped_gated_gemm_grad(
+        T, N // 2, K, groups, offsets.data_ptr(), dh.data_ptr(), lddh, at, lds, plane, x.data_ptr(), ldx, w.data_ptr(), ldw,
+        stride, kind, dpre.data_ptr(), ldp, dx.data_ptr() if need_dx else None, K or 1, dw.data_ptr() if need_dw else None,
+        K or 1, N * (K or 1), _current_stream(index))
     if rc:
         raise OzkError("ozk_grouped_gated_gemm_grad", rc)
     return dx, dw
