@@ -49,14 +49,14 @@ constexpr int kTop = 9;         // exponent that the largest element of a row is
 constexpr int kHead = 6;        // binades above it that fp16 has room for
 constexpr int kBelow = 26;      // binades below it that stay exact: down to 2^-17, 7 bits above fp16's last
 
-// W: warps. NT: tiles of 8 rows of x; 0: up to four rows, which the lanes convert together.
+// W: warps. NT: tiles of 8 rows of x; 0: one or two rows, which the lanes convert together.
 template <int FMT, int R, int NT, int W>
 struct Shape {
   static constexpr bool NV = FMT == OZK_NVFP4;
   static constexpr bool FEW = NT == 0;
   static constexpr int TILES = FEW ? 1 : NT;
-  static constexpr int TOKENS = FEW ? 4 : 8 * NT;
-  static constexpr int ROWS = FEW ? 4 : NT;       // rows of x that a lane keeps a scale for
+  static constexpr int TOKENS = FEW ? 2 : 8 * NT;
+  static constexpr int ROWS = FEW ? 2 : NT;       // rows of x that a lane keeps a scale for
   static constexpr int CHUNK = FEW ? 256 : 128;   // columns of a chunk
   static constexpr int ROW = CHUNK / 2;           // bytes of codes of a row
   static constexpr int PIECES = ROW / 16;
@@ -67,9 +67,12 @@ struct Shape {
   static constexpr int DEPTH = FEW && R == 1 ? 3 : 2;
   static constexpr int STAGE = CODES + SCALES;
   static constexpr int SUMS = R * TILES * 512;    // bytes of a warp's sums, at its end in the ring's place
-  // A warp's part of shared memory: its ring, and the rows of x of one chunk.
+  // Chunks of x that a warp has room for: with two, the next one's rows come while one is multiplied.
+  static constexpr int XCHUNKS = NT == 1 ? 2 : 1;
+  // A warp's part of shared memory: its ring, and rows of x.
   static constexpr int RING = (DEPTH * STAGE + 511) / 512 * 512;
-  static constexpr int part(int tokens) { return RING + tokens * XROW; }
+  static constexpr int part(int tokens) { return RING + XCHUNKS * tokens * XROW; }
+  static_assert(XCHUNKS == 1 || DEPTH == 2, "codes and x take turns alike");
   static constexpr int bytes(int tokens) { return W * part(tokens); }
   static_assert(SUMS <= RING, "the sums take the ring's place");
 };
@@ -89,17 +92,17 @@ struct GemvParams {
   float alpha;
   int act;                 // gated only
   bool vec;                // rows of x start on 16 bytes
+  bool side;               // the scale words of a block's tiles lie side by side
   int tokens;              // rows of x that a stage has room for
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
-// 16 and 4 bytes to shared memory.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+// 4, 8 or 16 bytes to shared memory.
+template <int BYTES>
+__device__ __forceinline__ void copy(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -117,10 +120,16 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&v)[N]) {
+  if constexpr (N == 1) {
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[0]) : "r"(addr) : "memory");
+  } else if constexpr (N == 2) {
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(addr) : "memory");
+  } else {
+    static_assert(N == 4, "one, two or four words");
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
+  }
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -248,12 +257,14 @@ struct Range {
     const int least = __reduce_min_sync(0xFFFFFFFFu, min(static_cast<int>(static_cast<int16_t>(lo & 0xFFFFu)), static_cast<int>(lo) >> 16));
     lo = (static_cast<uint32_t>(least) & 0xFFFFu) * 0x10001u;
   }
-  // Whether all but zeros have exponents from E - kBelow to E + kHead.
-  __device__ __forceinline__ bool within(int E) const {
+  // What hi and lo are when all but zeros have exponents from E - kBelow to E + kHead.
+  static __device__ __forceinline__ Range within(int E) {
     const uint32_t most = static_cast<uint32_t>(min((E + kHead + 1) << 7, 0x8000)) + 0x7FFEu;
     const int least = E - kBelow <= 1 ? -0x8000 : ((E - kBelow) << 7) - 0x8001;
-    return max(hi & 0xFFFFu, hi >> 16) <= most &&
-           min(static_cast<int16_t>(lo & 0xFFFFu), static_cast<int16_t>(lo >> 16)) >= least;
+    return {most * 0x10001u, (static_cast<uint32_t>(least) & 0xFFFFu) * 0x10001u};
+  }
+  __device__ __forceinline__ bool inside(const Range& r) const {
+    return __vmaxu2(hi, r.hi) == r.hi && __vmins2(lo, r.lo) == r.lo;
   }
   // Biased exponents of the largest and the smallest but zero (0 as 1); without any element: none.
   __device__ __forceinline__ bool any() const { return (hi & 0x80008000u) != 0u; }
@@ -291,6 +302,132 @@ __device__ __forceinline__ uint4 to_half2(uint4 v, uint32_t factor) {
   return make_uint4(to_half2(v.x, factor), to_half2(v.y, factor), to_half2(v.z, factor), to_half2(v.w, factor));
 }
 
+// Where 16-byte pieces lie: of a row of codes of a tile, and of a row of x.
+template <typename S>
+__device__ __forceinline__ uint32_t code_piece(int r, int piece) {
+  return static_cast<uint32_t>(r * S::ROW + ((piece ^ (S::FEW ? r & 7 : r >> 1 & 3)) * 16));
+}
+template <typename S>
+__device__ __forceinline__ uint32_t x_piece(int t, int piece) {
+  return static_cast<uint32_t>(t * S::XROW + ((piece ^ (t & 1) * 4) * 16));
+}
+
+// acc += the products of a chunk's weights (stage at `at`) with its rows of x
+// (at `xat`; convert makes fp16 of eight elements of this lane's row of tile
+// n).  Lanes of rows that are not there read the last one; their sums are
+// nobody's.
+template <typename S, int R, typename F>
+__device__ __forceinline__ void multiply(uint32_t at, uint32_t xat, int tokens, int pairs, float (&acc)[R][S::TILES][4], F convert) {
+  constexpr int TILES = S::TILES;
+  const int lane = threadIdx.x & 31;
+  const uint32_t wat = at + code_piece<S>(lane & 15, lane >> 4);
+  const uint32_t sat = at + S::CODES + static_cast<uint32_t>((lane >> 2) * (4 * R));
+  uint32_t xrow[TILES];
+#pragma unroll
+  for (int n = 0; n < TILES; ++n) xrow[n] = xat + x_piece<S>(min(8 * n + (lane >> 2), tokens - 1), lane & 3);
+#pragma unroll
+  for (int s = 0; s < S::CHUNK / 64; ++s) {  // 64 columns: two segments of 32
+    if (s >= pairs) break;                   // the last chunk
+    uint4 xb[2][TILES];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int n = 0; n < TILES; ++n) xb[j][n] = convert(lds128(xrow[n] ^ static_cast<uint32_t>((2 * s + j) * 64)), n);
+    uint32_t scl[R], sch[R];  // of rows lane / 4 and lane / 4 + 8 of the tiles
+    lds_words(sat + (S::NV ? s : s >> 1) * (64 * R), scl);
+    lds_words(sat + (S::NV ? s : s >> 1) * (64 * R) + 32 * R, sch);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      uint32_t w[4];
+      ldmatrix4((wat ^ static_cast<uint32_t>(s * 32)) + i * 16 * S::ROW, w);
+      uint32_t sl = scl[i], sh = sch[i];
+      if (S::NV) {  // of a word's four blocks of 16 the lane's own: one in each segment
+        const uint32_t pick = lane & 2 ? 0x31u : 0x20u;
+        sl = e4m3_half2(__byte_perm(sl, 0, pick));
+        sh = e4m3_half2(__byte_perm(sh, 0, pick));
+      } else {
+        sl = e8m0_bf162(s & 1 ? sl >> 16 : sl);
+        sh = e8m0_bf162(s & 1 ? sh >> 16 : sh);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t lo[4], hi[4];
+        decode8(w[2 * j], lo);
+        decode8(w[2 * j + 1], hi);
+        if (S::NV) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            lo[c] = j ? mul_half2<true>(lo[c], sl) : mul_half2<false>(lo[c], sl);
+            hi[c] = j ? mul_half2<true>(hi[c], sh) : mul_half2<false>(hi[c], sh);
+          }
+#pragma unroll
+          for (int n = 0; n < TILES; ++n) {
+            mma16816(acc[i][n], lo[0], hi[0], lo[1], hi[1], xb[j][n].x, xb[j][n].y);
+            mma16816(acc[i][n], lo[2], hi[2], lo[3], hi[3], xb[j][n].z, xb[j][n].w);
+          }
+        } else {
+          const float fl = __uint_as_float(j ? sl & 0xFFFF0000u : sl << 16);
+          const float fh = __uint_as_float(j ? sh & 0xFFFF0000u : sh << 16);
+#pragma unroll
+          for (int n = 0; n < TILES; ++n) {
+            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            mma16816(c, lo[0], hi[0], lo[1], hi[1], xb[j][n].x, xb[j][n].y);
+            mma16816(c, lo[2], hi[2], lo[3], hi[3], xb[j][n].z, xb[j][n].w);
+            acc[i][n][0] = fmaf(c[0], fl, acc[i][n][0]);
+            acc[i][n][1] = fmaf(c[1], fl, acc[i][n][1]);
+            acc[i][n][2] = fmaf(c[2], fh, acc[i][n][2]);
+            acc[i][n][3] = fmaf(c[3], fh, acc[i][n][3]);
+          }
+        }
+      }
+    }
+  }
+}
+
+// Calls f(i, n, c, 2^back) for every sum of this lane (tile i, rows of x 8 n + 2 (lane % 4) + c % 2), where E is the
+// exponent that the scale of this lane's row (lane / 4) of tile n was made for.
+template <int R, int TILES, typename F>
+__device__ __forceinline__ void unscaled(const int (&E)[TILES], F f) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = 0; n < TILES; ++n)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int back = __shfl_sync(0xFFFFFFFFu, -shift_of(E[n]), (2 * (lane & 3) + c) * 4);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        f(i, n, c, back);
+        f(i, n, c + 2, back);
+      }
+    }
+}
+
+// A chunk whose rows of x (as they came, at `xat`) hold elements too small for
+// their largest one's scale: one run over its weights for every kBelow + 1
+// binades, added to `away`.  E and low: exponents of the largest and the
+// smallest element of this lane's row of every tile.  Out of line: hardly ever
+// called, and the loop that calls it keeps its registers.
+template <typename S, int R>
+__device__ __noinline__ void multiply_wide(uint32_t at, uint32_t xat, int tokens, int pairs, const int (&E)[S::TILES],
+                                           const int (&low)[S::TILES], float* away) {
+  constexpr int TILES = S::TILES;
+  int top[TILES];
+#pragma unroll
+  for (int n = 0; n < TILES; ++n) top[n] = E[n];
+  for (;;) {
+    float acc[R][TILES][4] = {};
+    multiply<S, R>(at, xat, tokens, pairs, acc, [&](uint4 v, int n) { return to_half2(only(v, top[n]), factor_of(top[n])); });
+    unscaled<R>(top, [&](int i, int n, int c, int back) { away[(i * TILES + n) * 4 + c] += scaled(acc[i][n][c], back); });
+    bool left = false;
+#pragma unroll
+    for (int n = 0; n < TILES; ++n) {
+      left = left || low[n] < top[n] - kBelow;
+      top[n] -= kBelow + 1;
+    }
+    if (!__any_sync(0xFFFFFFFFu, left)) return;
+  }
+}
+
 // Blocks of an SM that registers are kept for.
 constexpr int blocks_of(int R, int NT, int W) { return (NT == 0 && R == 1 ? 24 : 16) / W; }
 
@@ -321,18 +458,13 @@ __global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const
   const uint8_t* codes = p.codes + group_row * (p.kpad / 2);
   const uint8_t* scales = p.scales + (group_row / 128 + e) * p.words * 512;
 
-  // A warp's ring of codes and scale words, and one chunk's rows of x (FEW: as
-  // fp16; else as they came).  16-byte pieces are swapped within a row so that
+  // A warp's ring of codes and scale words, and one or two chunks' rows of x (FEW:
+  // as fp16; else as they came).  16-byte pieces are swapped within a row so that
   // the rows that are read together lie in different banks.
   const uint32_t part_bytes = static_cast<uint32_t>(S::part(p.tokens));
   const uint32_t ring = smem_addr(smem) + static_cast<uint32_t>(warp) * part_bytes;
-  const uint32_t xat = ring + S::RING;
+  const uint32_t xat0 = ring + S::RING;
   const int chunks = (p.kpad + S::CHUNK - 1) / S::CHUNK;
-  auto code_piece = [](int r, int piece) {
-    return static_cast<uint32_t>(r * S::ROW + ((piece ^ (S::FEW ? r & 7 : r >> 1 & 3)) * 16));
-  };
-  auto x_piece = [](int t, int piece) { return static_cast<uint32_t>(t * S::XROW + ((piece ^ (t & 1) * 4) * 16)); };
-
   // What this lane copies of a chunk: piece `lane % PIECES` of every
   // 32 / PIECES-th of the tiles' rows, and scale words.  Rows past the last one
   // are left out: what lies in their place reaches only sums that are not
@@ -344,17 +476,17 @@ __global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const
   };
   auto in_range = [&](int r) { return n0 + r / 16 * 32 + (GATED ? r & 7 : r & 15) < p.N; };
   const int r0 = lane / S::PIECES;
-  const int64_t pitch = p.kpad / 2;
-  const uint8_t* src = codes + (n0 + r0) * pitch + lane % S::PIECES * 16;  // of rows r0 + kStep j: see from()
+  const uint32_t pitch = static_cast<uint32_t>(p.kpad / 2);
+  const uint8_t* src = codes + static_cast<int64_t>(n0 + r0) * pitch + lane % S::PIECES * 16;
+  const int64_t up = GATED ? static_cast<int64_t>(p.N) * pitch : 0;  // from a row to that of the other projection
   const bool all_rows = n0 + 32 * (R - 1) + kOut <= p.N;
-  const uint32_t dst = code_piece(r0, lane % S::PIECES);
-  constexpr int kScaleCopies = (R * 16 * S::WORDS + 31) / 32;
-  int64_t ssrc[kScaleCopies];  // offsets of the words (lane + 32 j) of a chunk: [row][word]
+  const uint32_t dst = code_piece<S>(r0, lane % S::PIECES);
+  // Scale words (lane + 32 j) of a chunk, each of all tiles: [word][row of a tile][tile]
+  constexpr int kScaleCopies = (16 * S::WORDS + 31) / 32;
+  auto scale_at = [&](int row) { return static_cast<int64_t>(row / 128) * p.words * 512 + row % 32 * 16 + row / 32 % 4 * 4; };
+  const uint8_t* ssrc[kScaleCopies];
 #pragma unroll
-  for (int j = 0; j < kScaleCopies; ++j) {
-    const int i = lane + 32 * j, row = w_row(i / S::WORDS);
-    ssrc[j] = (static_cast<int64_t>(row / 128) * p.words + i % S::WORDS) * 512 + row % 32 * 16 + row / 32 % 4 * 4;
-  }
+  for (int j = 0; j < kScaleCopies; ++j) ssrc[j] = scales + scale_at(w_row(lane & 15)) + (lane / 16 + 2 * j) * 512;
 
   for (int t0 = 0; t0 < rows; t0 += S::TOKENS) {
     const int tokens = min(S::TOKENS, rows - t0);
@@ -362,44 +494,50 @@ __global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const
     auto fetch = [&](int chunk, int slot) {
       const uint32_t at = ring + static_cast<uint32_t>(slot * S::STAGE);
       const uint8_t* from = src + static_cast<int64_t>(chunk) * S::ROW;
-      const uint8_t* sfrom = scales + static_cast<int64_t>(chunk) * S::WORDS * 512;
+      const int64_t sfrom = static_cast<int64_t>(chunk) * (S::WORDS * 512);
       auto code = [&](int j) {
         // rows 8 apart (where FEW, 4: pieces differ by one bit) have their pieces in the same places
         const uint32_t to = S::FEW && (j & 1) ? dst ^ 64u : dst;
         constexpr int kPer = 16 / kStep;  // copies of a tile
-        const int64_t row = j / kPer * 32 + (GATED ? j % (kPer / 2) * kStep + (j % kPer >= kPer / 2 ? p.N : 0) : j % kPer * kStep);
-        copy16(at + to + j * kStep * S::ROW, from + row * pitch);
+        const uint32_t row = j / kPer * 32 + (GATED ? j % (kPer / 2) : j % kPer) * kStep;
+        copy<16>(at + to + j * kStep * S::ROW, (GATED && j % kPer >= kPer / 2 ? from + up : from) + static_cast<uint64_t>(row) * pitch);
       };
-      const bool last = (chunk + 1) * S::CHUNK > p.kpad;
-      if (all_rows && !last) {
+      auto scale = [&](int j) {
+        const uint32_t to = at + S::CODES + (lane + 32 * j) * (4 * R);
+        if (p.side) {
+          copy<4 * R>(to, ssrc[j] + sfrom);
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < R; ++i)
+            if (in_range(16 * i + (lane & 15)))
+              copy<4>(to + 4 * i, scales + scale_at(w_row(16 * i + (lane & 15))) + (lane / 16 + 2 * j) * 512 + sfrom);
+        }
+      };
+      if (all_rows && (chunk + 1) * S::CHUNK <= p.kpad) {
 #pragma unroll
         for (int j = 0; j < kCopies; ++j) code(j);
 #pragma unroll
         for (int j = 0; j < kScaleCopies; ++j)
-          if (R * 16 * S::WORDS % 32 == 0 || j + 1 < kScaleCopies || lane + 32 * j < R * 16 * S::WORDS)
-            copy4(at + S::CODES + (lane + 32 * j) * 4, sfrom + ssrc[j]);
+          if (S::WORDS > 1 || lane < 16) scale(j);
       } else {  // the rows, columns and words that are there
         const bool in = chunk * S::CHUNK + lane % S::PIECES * 32 < p.kpad;
 #pragma unroll
         for (int j = 0; j < kCopies; ++j)
           if (in && in_range(r0 + kStep * j)) code(j);
 #pragma unroll
-        for (int j = 0; j < kScaleCopies; ++j) {
-          const int i = lane + 32 * j;
-          if (i < R * 16 * S::WORDS && in_range(i / S::WORDS) && chunk * S::WORDS + i % S::WORDS < p.words)
-            copy4(at + S::CODES + i * 4, sfrom + ssrc[j]);
-        }
+        for (int j = 0; j < kScaleCopies; ++j)
+          if ((S::WORDS > 1 || lane < 16) && in_range(lane & 15) && chunk * S::WORDS + lane / 16 + 2 * j < p.words) scale(j);
       }
     };
     // The chunk's rows of x: to shared memory, or FEW this lane's eight elements of every row.
-    uint4 xr[4];
-    auto fetch_x = [&](int chunk) {
+    uint4 xr[2];
+    auto fetch_x = [&](int chunk, int slot) {
       const bool whole = p.vec && (chunk + 1) * S::CHUNK <= p.K;
       if (S::FEW) {
         const int k = chunk * S::CHUNK + lane * 8;
         const uint16_t* row = x + k;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
+        for (int t = 0; t < 2; ++t) {
           if (t >= tokens) break;
           xr[t] = whole ? load16(row) : load8(row - k, k, p.K, p.vec);
           row += p.ldx;
@@ -407,12 +545,12 @@ __global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const
         return;
       }
       const int k = chunk * S::CHUNK + (lane & 15) * 8;
-      const uint32_t to = xat + x_piece(lane >> 4, lane & 15);
+      const uint32_t to = xat0 + static_cast<uint32_t>(slot * p.tokens * S::XROW) + x_piece<S>(lane >> 4, lane & 15);
       const uint16_t* row = x + (lane >> 4) * p.ldx + k;
       if (whole) {
 #pragma unroll
         for (int i = 0; i < S::TOKENS / 2; ++i)
-          if (2 * i + (lane >> 4) < tokens) copy16(to + i * 2 * S::XROW, row + i * 2 * p.ldx);
+          if (2 * i + (lane >> 4) < tokens) copy<16>(to + i * 2 * S::XROW, row + i * 2 * p.ldx);
       } else {
 #pragma unroll 1
         for (int i = 0; 2 * i + (lane >> 4) < tokens; ++i) sts128(to + i * 2 * S::XROW, load8(row + i * 2 * p.ldx - k, k, p.K, p.vec));
@@ -428,148 +566,55 @@ __global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const
           for (int c = 0; c < 4; ++c) acc[i][n][c] = 0.0f;
     };
     clear();
-    // The largest exponent that a row's scale is made for: FEW, of row t; else of this lane's row (lane / 4) of tile n.
+    // The largest exponent that a row's scale is made for, the scale 2^shift(E), and what fits it: FEW, of row t; else of
+    // this lane's row (lane / 4) of tile n.
     int E[S::ROWS];
-    uint32_t factor[S::ROWS];  // 2^shift(E)
+    uint32_t factor[S::ROWS];
+    Range limit[S::ROWS];
 #pragma unroll
-    for (int n = 0; n < S::ROWS; ++n) E[n] = 0, factor[n] = 0u;
-    bool kept = false;  // sums of an earlier scale have been put away
-    volatile float away[R * TILES * 4];  // in local memory: hardly ever used
-    // Puts the sums away without their scale (2^shift(E - down)), at last into the ring's place; rows 2 q, 2 q + 1 of a
-    // tile are this lane's columns.
-    float* mine = reinterpret_cast<float*>(smem + static_cast<size_t>(warp) * part_bytes) + lane;
-    auto put_away = [&](int down, bool last) {
+    for (int n = 0; n < S::ROWS; ++n) E[n] = 0, factor[n] = 0u, limit[n] = {0u, 0u};  // nothing fits
+    auto row_values = [&](const int (&of)[S::ROWS], int (&own)[TILES]) {  // those of this lane's rows
 #pragma unroll
-      for (int n = 0; n < TILES; ++n) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          int back = 0;
-          if (BF && S::FEW) back = -shift_of((lane & 1 ? E[2 + c] : E[c]) - down);  // rows past the fourth are nobody's
-          if (BF && !S::FEW) back = __shfl_sync(0xFFFFFFFFu, -shift_of(E[n] - down), (2 * (lane & 3) + c) * 4);
-#pragma unroll
-          for (int i = 0; i < R; ++i)
-#pragma unroll
-            for (int h = 0; h < 4; h += 2) {
-              const int at = (i * TILES + n) * 4 + c + h;
-              float v = BF ? scaled(acc[i][n][c + h], back) : acc[i][n][c + h];
-              if (kept) v += away[at];
-              if (last) mine[at * 32] = v;
-              else away[at] = v;
-            }
-        }
-      }
-      kept = true;
+      for (int n = 0; n < TILES; ++n) own[n] = S::FEW ? of[(lane >> 2) ? S::ROWS - 1 : 0] : of[n];
+    };
+    bool kept = false;          // sums of an earlier scale have been put away
+    float away[R * TILES * 4];  // in local memory: hardly ever used
+    // The sums without their scale to `to`, with what was put away.
+    auto put = [&](auto&& to) {
+      int own[TILES];
+      row_values(E, own);
+      unscaled<R>(own, [&](int i, int n, int c, int back) {
+        const int at = (i * TILES + n) * 4 + c;
+        const float v = BF ? scaled(acc[i][n][c], back) : acc[i][n][c];
+        to(at, kept ? v + away[at] : v);
+      });
     };
 
     int next = warp;  // chunk that is fetched next
 #pragma unroll
     for (int s = 0; s < S::DEPTH - 1; ++s) {
       if (next < chunks) fetch(next, s);
+      if (S::XCHUNKS == 2 && next < chunks) fetch_x(next, s);
       copy_commit();
       next += W;
     }
-    if (warp < chunks) fetch_x(warp);
-    if (!S::FEW) copy_commit();
+    if (S::XCHUNKS == 1 && warp < chunks) fetch_x(warp, 0);
+    if (S::XCHUNKS == 1 && !S::FEW) copy_commit();
     int slot = 0;
 #pragma unroll 1
     for (int chunk = warp; chunk < chunks; chunk += W) {
       __syncwarp();  // the slot that was used before this one is free
-      if (next < chunks) fetch(next, slot == 0 ? S::DEPTH - 1 : slot - 1);
+      const int spare = slot == 0 ? S::DEPTH - 1 : slot - 1;
+      if (next < chunks) {
+        fetch(next, spare);
+        if (S::XCHUNKS == 2) fetch_x(next, spare);
+      }
       copy_commit();
       copy_wait<S::DEPTH - 1>();  // all but the latest are in, x among them
       __syncwarp();
       next += W;
+      const uint32_t xat = xat0 + (S::XCHUNKS == 2 ? static_cast<uint32_t>(slot * p.tokens * S::XROW) : 0u);
       const uint32_t at = ring + static_cast<uint32_t>(slot * S::STAGE);
-
-      // One pass over the chunk's weights; part: only elements of x with exponents from E - down to kBelow below it.
-      // Lanes of rows that are not there read the last one; their sums are nobody's.
-      auto pass = [&](bool part, int down) {
-        const uint32_t wat = at + code_piece(lane & 15, lane >> 4);
-        const uint32_t sat = at + S::CODES + static_cast<uint32_t>((lane >> 2) * S::WORDS * 4);
-        uint32_t xrow[TILES];
-#pragma unroll
-        for (int n = 0; n < TILES; ++n) xrow[n] = xat + x_piece(min(8 * n + (lane >> 2), tokens - 1), lane & 3);
-        const int pairs = min(S::CHUNK, p.kpad - chunk * S::CHUNK) / 64;
-#pragma unroll
-        for (int s = 0; s < S::CHUNK / 64; ++s) {  // 64 columns: two segments of 32
-          if (s >= pairs) break;
-          uint4 xb[2][TILES];
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int n = 0; n < TILES; ++n) {
-              uint4 v = lds128(xrow[n] ^ static_cast<uint32_t>((2 * s + j) * 64));
-              if (BF && !S::FEW) {
-                uint32_t f = factor[n];
-                if (part) {
-                  asm volatile("");  // a branch: the masks are not worth a test in every pass
-                  v = only(v, E[n] - down);
-                  f = factor_of(E[n] - down);
-                }
-                v = to_half2(v, f);
-              }
-              xb[j][n] = v;
-            }
-#pragma unroll
-          for (int i = 0; i < R; ++i) {
-            uint32_t w[4];
-            ldmatrix4((wat ^ static_cast<uint32_t>(s * 32)) + i * 16 * S::ROW, w);
-            const uint32_t word = sat + static_cast<uint32_t>(i * 16 * S::WORDS + (S::NV ? s : s >> 1)) * 4;
-            uint32_t sl = lds32(word), sh = lds32(word + 8 * S::WORDS * 4);
-            if (S::NV) {  // of a word's four blocks of 16 the lane's own: one in each segment
-              const uint32_t pick = lane & 2 ? 0x31u : 0x20u;
-              sl = e4m3_half2(__byte_perm(sl, 0, pick));
-              sh = e4m3_half2(__byte_perm(sh, 0, pick));
-            } else {
-              sl = e8m0_bf162(s & 1 ? sl >> 16 : sl);
-              sh = e8m0_bf162(s & 1 ? sh >> 16 : sh);
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              uint32_t lo[4], hi[4];
-              decode8(w[2 * j], lo);
-              decode8(w[2 * j + 1], hi);
-              if (S::NV) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                  lo[c] = j ? mul_half2<true>(lo[c], sl) : mul_half2<false>(lo[c], sl);
-                  hi[c] = j ? mul_half2<true>(hi[c], sh) : mul_half2<false>(hi[c], sh);
-                }
-#pragma unroll
-                for (int n = 0; n < TILES; ++n) {
-                  mma16816(acc[i][n], lo[0], hi[0], lo[1], hi[1], xb[j][n].x, xb[j][n].y);
-                  mma16816(acc[i][n], lo[2], hi[2], lo[3], hi[3], xb[j][n].z, xb[j][n].w);
-                }
-              } else {
-                const float fl = __uint_as_float(j ? sl & 0xFFFF0000u : sl << 16);
-                const float fh = __uint_as_float(j ? sh & 0xFFFF0000u : sh << 16);
-#pragma unroll
-                for (int n = 0; n < TILES; ++n) {
-                  float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                  mma16816(c, lo[0], hi[0], lo[1], hi[1], xb[j][n].x, xb[j][n].y);
-                  mma16816(c, lo[2], hi[2], lo[3], hi[3], xb[j][n].z, xb[j][n].w);
-                  acc[i][n][0] = fmaf(c[0], fl, acc[i][n][0]);
-                  acc[i][n][1] = fmaf(c[1], fl, acc[i][n][1]);
-                  acc[i][n][2] = fmaf(c[2], fh, acc[i][n][2]);
-                  acc[i][n][3] = fmaf(c[3], fh, acc[i][n][3]);
-                }
-              }
-            }
-          }
-        }
-      };
-      // FEW: this chunk's rows, converted, to shared memory.
-      auto stage_x = [&](bool part, int down) {
-        __syncwarp();
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          if (t >= tokens) break;
-          if (!BF) sts128(xat + x_piece(t, lane), xr[t]);
-          else if (!part) sts128(xat + x_piece(t, lane), to_half2(xr[t], factor[t]));
-          else sts128(xat + x_piece(t, lane), to_half2(only(xr[t], E[t] - down), factor_of(E[t] - down)));
-        }
-        __syncwarp();
-      };
 
       // ---- do this chunk's rows fit their scales?
       bool part = false;               // some do not, whatever the scale
@@ -583,15 +628,16 @@ __global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const
             if (n >= tokens) break;
             range[n].add(xr[n]);
           } else {
-            const uint32_t row = xat + x_piece(min(8 * n + (lane >> 2), tokens - 1), lane & 3);
+            const uint32_t row = xat + x_piece<S>(min(8 * n + (lane >> 2), tokens - 1), lane & 3);
 #pragma unroll
             for (int s = 0; s < S::CHUNK / 32; ++s) range[n].add(lds128(row ^ static_cast<uint32_t>(s * 64)));
           }
-          fits = fits && E[n] > 0 && range[n].within(E[n]);
+          fits = fits && range[n].inside(limit[n]);
         }
         if (!__all_sync(0xFFFFFFFFu, fits)) {
           if (chunk != warp) {
-            put_away(0, false);
+            put([&](int i, float v) { away[i] = v; });
+            kept = true;
             clear();
           }
           bool small = false;
@@ -609,30 +655,47 @@ __global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const
             E[n] = range[n].any() ? range[n].top() : 1;
             low[n] = range[n].any() ? range[n].bottom() : 256;
             factor[n] = factor_of(E[n]);
+            limit[n] = Range::within(E[n]);
             small = small || low[n] < E[n] - kBelow;
           }
           part = __any_sync(0xFFFFFFFFu, small);
         }
       }
-      for (int down = 0;; down += kBelow + 1) {
-        if (S::FEW) stage_x(part, down);
-        pass(part, down);
-        if (!BF || !part) break;
-        put_away(down, false);
-        clear();
-        bool left = false;
+      const int pairs = min(S::CHUNK, p.kpad - chunk * S::CHUNK) / 64;
+      if (S::FEW) {  // this chunk's rows, converted, to shared memory
+        __syncwarp();
 #pragma unroll
-        for (int n = 0; n < S::ROWS; ++n) left = left || low[n] < E[n] - down - kBelow;
-        if (!__any_sync(0xFFFFFFFFu, left)) break;
+        for (int t = 0; t < 2; ++t)
+          if (t < tokens) sts128(xat + x_piece<S>(t, lane), BF && !part ? to_half2(xr[t], factor[t]) : xr[t]);
+        __syncwarp();
+        if (chunk + W < chunks) fetch_x(chunk + W, 0);
       }
-      if (!S::FEW) __syncwarp();
-      if (chunk + W < chunks) fetch_x(chunk + W);
-      if (!S::FEW) copy_commit();
+      if (!BF || !part) {
+        multiply<S, R>(at, xat, tokens, pairs, acc, [&](uint4 v, int n) { return BF && !S::FEW ? to_half2(v, factor[n]) : v; });
+      } else {
+        if (!kept) {
+#pragma unroll
+          for (int i = 0; i < R * TILES * 4; ++i) away[i] = 0.0f;
+          kept = true;
+        }
+        int top[TILES], least[TILES];
+        row_values(E, top);
+        row_values(low, least);
+        multiply_wide<S, R>(at, xat, tokens, pairs, top, least, away);
+      }
+      if (S::XCHUNKS == 1 && !S::FEW) {
+        __syncwarp();
+        if (chunk + W < chunks) fetch_x(chunk + W, 0);
+        copy_commit();
+      }
       slot = slot + 1 == S::DEPTH ? 0 : slot + 1;
     }
     copy_wait<0>();
     __syncwarp();
-    put_away(0, true);
+    {
+      float* mine = reinterpret_cast<float*>(smem + static_cast<size_t>(warp) * part_bytes) + lane;
+      put([&](int i, float v) { mine[i * 32] = v; });
+    }
 
     // ---- the warps' sums, in order
     __syncthreads();
@@ -643,7 +706,7 @@ __global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const
         v += reinterpret_cast<const float*>(smem + static_cast<size_t>(w) * part_bytes)[((i * TILES + n) * 4 + c) * 32 + l];
       return v;
     };
-    constexpr int kRows = S::FEW ? 4 : 8;  // rows of x of a tile that can be there
+    constexpr int kRows = S::FEW ? 2 : 8;  // rows of x of a tile that can be there
     for (int o = tid; o < R * TILES * kRows * kOut; o += 32 * W) {
       // a value of lane l = 4 row + token / 2: c = token % 2, + 2 for the second eight rows of the tile
       const int col = o % kOut, t = o / kOut % kRows, n = o / (kOut * kRows) % TILES, i = o / (kOut * kRows * TILES);
@@ -685,6 +748,7 @@ cudaError_t launch(GemvParams p, cudaStream_t stream) {
   const int sub = GATED ? 4 : 2;  // blocks that share 32 R columns
   const dim3 grid((p.N + 32 * R - 1) / (32 * R) * sub, p.offsets ? std::min(p.groups, p.T) : 1);
   p.tokens = std::min(p.T, S::TOKENS);
+  p.side = !GATED || p.N % (32 * R) == 0;
   return launch_dependent(kernel, grid, dim3(32 * W), S::bytes(p.tokens), stream, p);
 }
 
@@ -693,13 +757,16 @@ cudaError_t choose(const GemvParams& p, int num_sms, cudaStream_t stream) {
   const int active = p.offsets ? std::min(p.groups, p.T) : 1;
   const int rows = (p.T + active - 1) / active;  // of a group, as their mean: the offsets are on the device
   const int64_t tiles = static_cast<int64_t>((p.N + (GATED ? 7 : 15)) / (GATED ? 8 : 16)) * active;
-  if (rows <= 4) {
-    if (tiles >= 8 * num_sms) return launch<FMT, 2, 0, 4, GATED, BF>(p, stream);
+  if (p.T <= 2) {  // no group has more
+    if (tiles >= 6 * num_sms) return launch<FMT, 2, 0, 4, GATED, BF>(p, stream);
     if (tiles >= 3 * num_sms) return launch<FMT, 2, 0, 8, GATED, BF>(p, stream);
+    if (tiles >= num_sms) return launch<FMT, 2, 0, 16, GATED, BF>(p, stream);
     return launch<FMT, 1, 0, 8, GATED, BF>(p, stream);
   }
   if (rows <= 8) {
-    if (tiles >= 4 * num_sms) return launch<FMT, 2, 1, 8, GATED, BF>(p, stream);
+    if (tiles >= 6 * num_sms) return launch<FMT, 4, 1, 8, GATED, BF>(p, stream);
+    if (tiles >= 3 * num_sms) return launch<FMT, 4, 1, 16, GATED, BF>(p, stream);
+    if (tiles >= num_sms) return launch<FMT, 2, 1, 16, GATED, BF>(p, stream);
     return launch<FMT, 1, 1, 8, GATED, BF>(p, stream);
   }
   if (rows <= 16)

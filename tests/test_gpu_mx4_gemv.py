@@ -21,7 +21,8 @@ from fp64_gemm_emulation_exponent_gb300 import ozk
 pytestmark = pytest.mark.gpu
 ROUND = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
 SIZES = [(1, 1, 1), (1, 16, 64), (2, 17, 100), (5, 1537, 2090), (8, 40, 4097), (9, 300, 1000), (16, 136, 640), (17, 70, 4500),
-         (31, 9, 130), (40, 33, 260), (1, 5000, 129), (3, 20000, 64), (12, 8200, 200), (33, 8200, 72)]
+         (31, 9, 130), (40, 33, 260), (1, 5000, 129), (3, 20000, 64), (12, 8200, 200), (33, 8200, 72),
+         (6, 4096, 320), (1, 4096, 256), (11, 4096, 192), (2, 1024, 96), (20, 2048, 128)]
 _erf = np.vectorize(math.erf)
 
 
