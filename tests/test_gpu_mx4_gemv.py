@@ -139,20 +139,27 @@ def test_bad_offsets_are_cut_and_reported(bad):
     assert ozk.ozk_stream_status() == 0
 
 
+@pytest.mark.parametrize("T,N", [(1, 33), (2, 2600), (2, 5000), (2, 16000), (5, 33), (7, 2600), (7, 8200), (7, 16000), (12, 33),
+                                 (12, 2600), (20, 8200)])
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
-def test_rows_of_any_range(fmt):
-    """Rows whose elements lie up to 2^250 apart, the large ones where the weights are zero: every element counts."""
-    T, N, K = 5, 33, 300
+def test_rows_of_any_range(fmt, T, N):
+    """Rows whose elements lie up to 2^226 apart, the large ones where the weights are zero: every element counts."""
+    K = 700
     wide = normal(N, K, seed=3)
     wide[:, ::7] = 0.0
     q = ozk.mx4_quantize(wide, fmt)
     w = ozk.mx4_dequantize(q, torch.float64).cpu().numpy()[None]
     x = normal(T, K, seed=4)
-    x[0, ::7] = 2.0 ** 60
-    x[1, ::7] = 2.0 ** 127
-    x[2] *= 2.0 ** -120
-    x[3] *= 2.0 ** -100
-    x[3, 7] = 2.0 ** 126
+    for t in range(T):
+        if t % 5 == 0:
+            x[t, ::7] = 2.0 ** 60
+        if t % 5 == 1:
+            x[t, 14::7] = 2.0 ** 127
+        if t % 5 == 2:
+            x[t] *= 2.0 ** -120
+        if t % 5 == 3:
+            x[t] *= 2.0 ** -100
+            x[t, 630] = 2.0 ** 126  # in a later chunk than the first
     x = x.bfloat16()
     check(x, q, w, None, [0, T], 1.0, None, torch.float32)
 
