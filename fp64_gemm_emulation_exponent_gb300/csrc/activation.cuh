@@ -28,7 +28,8 @@ __device__ __forceinline__ float act_value(float g, int act) { return g * act_p(
 // The derivative g P'(g) + P(g), given P(g).
 __device__ __forceinline__ float act_slope(float g, float p, int act) {
   if (act == OZK_SILU) return fmaf(g * p, 1.0f - p, p);
-  if (act == OZK_GELU_TANH) return fmaf(g * p * (1.0f - p), fmaf(3.0f * kGeluB, g * g, kGeluA), p);
+  // g^2 held finite: beside it 1 - p or p is 0
+  if (act == OZK_GELU_TANH) return fmaf(g * p * (1.0f - p), fmaf(3.0f * kGeluB, fminf(g * g, 1e30f), kGeluA), p);
   return fmaf(g * 0.39894228040143268f, __expf(-0.5f * g * g), p);
 }
 

@@ -155,7 +155,7 @@ cudaError_t launch_gated_grad(const GatedGrad& q, int num_sms, cudaStream_t stre
   auto aligned = [](const void* a) { return reinterpret_cast<uintptr_t>(a) % 16 == 0; };
   const bool vec = aligned(q.dh) && aligned(q.slopes) && aligned(q.out) && q.M % 8 == 0 && (q.T == 1 || q.lddh % 8 == 0) &&
                    (q.T == 1 || q.lds % 8 == 0) && q.slope_plane % 8 == 0 && (q.T == 1 || q.ldo % 8 == 0);
-  const int64_t units = q.T * p.runs;
+  const int64_t units = q.T * std::max(p.runs, 1);  // rows that are cleared want warps too
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>((units + kWarps - 1) / kWarps, 8 * num_sms)));
   const bool bf = q.dtype == OZK_BF16;
   auto kernel = bf ? (vec ? gated_grad_kernel<true, true> : gated_grad_kernel<true, false>)

@@ -641,25 +641,34 @@ def _activation(name):
 
 def _few_rows(name, x, w, offsets, per, act, alpha, out_dtype, out, stream):
     """mx4_gemv and mx4_gated_gemv: `per` rows of w to an output column, act the arguments of the gated one."""
-    index = _device_index(x)
-    if w._index != index:
-        raise ValueError(f"operands on cuda:{index} and cuda:{w._index}")
+    index, groups, at = w._index, w.groups, None
+    if x.get_device() != index:
+        raise ValueError(f"operands on {x.device} and cuda:{index}")
     if w.offsets is not None:
         raise ValueError("weights in equal groups are expected")
-    if offsets is None:
-        if w.groups != 1:
-            raise ValueError(f"offsets are needed for weights of {w.groups} groups")
-    elif _offsets(offsets, index) != w.groups:
-        raise ValueError(f"offsets of {offsets.shape[0] - 1} groups, weights of {w.groups}")
-    (T, K, ldx), N = _rows(x), w.rows // (w.groups * per)
-    if K != w.K or N * per * w.groups != w.rows:
-        raise ValueError(f"x is {tuple(x.shape)}, the weights {w.rows} x {w.K} in {w.groups} groups")
-    if out_dtype is None and out is None:
-        out_dtype = x.dtype
-    out, ld, kind = _result(out, T, N, out_dtype, x.device, stream)
-    rc = getattr(_lib, name)(T, N, K, w.groups, None if offsets is None else offsets.data_ptr(), x.data_ptr(), ldx,
-                             _dtype(x.dtype), w._codes, w._scales, _FORMATS[w.fmt], alpha, *act, out.data_ptr(), ld, kind,
-                             _stream_at(index, stream))
+    if offsets is not None:
+        if _offsets(offsets, index) != groups:
+            raise ValueError(f"offsets of {offsets.shape[0] - 1} groups, weights of {groups}")
+        at = offsets.data_ptr()
+    elif groups != 1:
+        raise ValueError(f"offsets are needed for weights of {groups} groups")
+    (T, K, ldx), N = _rows(x), w.rows // (groups * per)
+    if K != w.K or N * per * groups != w.rows:
+        raise ValueError(f"x is {tuple(x.shape)}, the weights {w.rows} x {w.K} in {groups} groups")
+    dtype = x.dtype
+    if out is None:
+        if out_dtype is None:
+            out_dtype = dtype
+        ld, kind = N or 1, _dtype(out_dtype)
+        if stream is None:
+            out = _torch.empty((T, N), dtype=out_dtype, device=w.device)
+        else:
+            out = _empty((T, N), out_dtype, w.device, stream)
+    else:
+        out, ld, kind = _result(out, T, N, out_dtype, w.device, stream)
+    rc = getattr(_lib, name)(T, N, K, groups, at, x.data_ptr(), ldx, _dtype(dtype), w._codes, w._scales, _FORMATS[w.fmt],
+                             alpha, *act, out.data_ptr(), ld, kind,
+                             _current_stream(index) if stream is None else _stream_at(index, stream))
     if rc:
         raise OzkError(name, rc)
     return out

@@ -282,3 +282,33 @@ def test_backward_pass_in_one_call(H, K):
     with pytest.raises(ValueError):
         ozk.grouped_gated_gemm_grad(dh, x, w, offsets, slopes[:, :, : H - 1])
     assert ozk.ozk_stream_status() == 0
+
+
+@pytest.mark.parametrize("act", ref.ACTS)
+def test_far_arguments(act):
+    """Far to the right the activation is g with slope 1, far to the left 0 with slope 0, also where g^2 leaves fp32."""
+    g = [1e3, 1e10, 3e19, 1e30, -1e3, -1e10, -3e19, -1e30]
+    x = torch.zeros(8, 8, dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = torch.tensor(g)
+    x[:, 1] = 1.0
+    w = torch.zeros(1, 2, 8, dtype=torch.bfloat16, device="cuda")
+    w[0, 0, 0] = w[0, 1, 1] = 1.0  # g is the first element, u is 1
+    offsets = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    slopes = torch.empty(2, 8, 1, dtype=x.dtype, device="cuda")
+    h = ozk.grouped_gated_gemm(x, w, offsets, activation=act, slopes=slopes)
+    want = torch.clamp(x[:, 0], min=0.0)
+    assert torch.equal(h[:, 0], want) and torch.equal(slopes[1, :, 0], want)
+    assert torch.equal(slopes[0, :, 0], (x[:, 0] > 0).to(x.dtype))
+
+
+@pytest.mark.parametrize("H,K,T", [(0, 16, 5), (8, 16, 0), (0, 16, 0)])
+def test_nothing_to_multiply(H, K, T):
+    """No columns or no rows: empty results, gradients of zeros."""
+    x = torch.ones(T, K, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    w = torch.ones(2, 2 * H, K, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    offsets = torch.tensor([0, T // 2, T], dtype=torch.int32, device="cuda")
+    h = ozk.grouped_gated_gemm(x, w, offsets)
+    assert h.shape == (T, H)
+    dx, dw = torch.autograd.grad(h, (x, w), torch.ones_like(h))
+    assert dx.shape == x.shape and not dx.any() and dw.shape == w.shape and not dw.any()
+    assert ozk.ozk_stream_status() == 0
