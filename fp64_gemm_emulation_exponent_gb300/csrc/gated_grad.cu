@@ -1,12 +1,12 @@
 // The gradient of a gated product with respect to its two projections:
 //   dpre[t, m] = dh[t, m] s0[t, m],   dpre[t, M + m] = dh[t, m] s1[t, m],
 // s0 = dh/dgate = u act'(g) and s1 = dh/dup = act(g) as the forward product
-// stored them, so no exponential is taken here and the activation is not
-// known.  Each product is rounded once (two 16-bit factors are exact in fp32).
+// stored them in fp32, so no exponential is taken here and the activation is not
+// known.  Each product is rounded to fp32 and to 16 bits.
 //
-// Five elements move for one of dh: bound by HBM, 10 T M bytes.  A warp takes a
-// row's run of up to 1024 columns with 16-byte accesses, all three loads of four
-// vectors ahead of the stores.  Where the gradient of x follows, the kernel also
+// 14 bytes move for an element of dh: bound by HBM.  A warp takes a row's run of
+// up to 512 columns with 16-byte accesses, the loads of two vectors ahead of
+// the stores.  Where the gradient of x follows, the kernel also
 // clears its rows in no group, which the product leaves as they are.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -23,7 +23,7 @@ __device__ int g_gated_status;  // bit 1: bad group offsets
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;
+constexpr int kUnroll = 2;
 constexpr int kRun = 32 * 8 * kUnroll;  // columns of a unit
 
 struct GradParams {
@@ -31,7 +31,8 @@ struct GradParams {
   int T, M, groups, runs;  // runs: units of a row
   FastDiv div_runs;
   const int32_t* offsets;
-  const uint16_t *dh, *slopes;
+  const uint16_t* dh;
+  const float* slopes;
   uint16_t* out;
   uint16_t* clear;   // T x K, or null: rows in no group are set to zero
   int64_t ldc;
@@ -54,18 +55,29 @@ __device__ __forceinline__ int2 rows_of(const GradParams& p) {
   return {min(max(p.offsets[0], 0), p.T), most};
 }
 
+// Both elements of a 16-bit pair times an fp32 factor each.
 template <bool BF>
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t mul2(uint32_t d, float lo, float hi) {
   uint32_t r;
-  if (BF) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  else asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  if (BF) {
+    lo *= __uint_as_float(d << 16);
+    hi *= __uint_as_float(d & 0xFFFF0000u);
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  } else {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&d));
+    lo *= v.x;
+    hi *= v.y;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  }
   return r;
 }
 template <bool BF>
-__device__ __forceinline__ uint4 mul8(uint4 a, uint4 b) {
-  return make_uint4(mul2<BF>(a.x, b.x), mul2<BF>(a.y, b.y), mul2<BF>(a.z, b.z), mul2<BF>(a.w, b.w));
+__device__ __forceinline__ uint4 mul8(const uint4& d, const uint4 (&s)[2]) {
+  auto f = [](uint32_t v) { return __uint_as_float(v); };
+  return make_uint4(mul2<BF>(d.x, f(s[0].x), f(s[0].y)), mul2<BF>(d.y, f(s[0].z), f(s[0].w)),
+                    mul2<BF>(d.z, f(s[1].x), f(s[1].y)), mul2<BF>(d.w, f(s[1].z), f(s[1].w)));
 }
-__device__ __forceinline__ uint4 load16(const uint16_t* p) {
+__device__ __forceinline__ uint4 load16(const void* p) {
   uint4 v;
   asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
   return v;
@@ -95,17 +107,21 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const GradParams p
     else row = u / p.runs;
     const int c0 = static_cast<int>(u - row * p.runs) * kRun;
     row += span.x;
-    const uint16_t *dh = p.dh + row * p.lddh, *s0 = p.slopes + row * p.lds, *s1 = s0 + p.plane;
+    const uint16_t* dh = p.dh + row * p.lddh;
+    const float *s0 = p.slopes + row * p.lds, *s1 = s0 + p.plane;
     uint16_t *o0 = p.out + row * p.ldo, *o1 = o0 + p.M;
     if (VEC) {
-      uint4 d[kUnroll], a[kUnroll], b[kUnroll];
+      uint4 d[kUnroll], a[kUnroll][2], b[kUnroll][2];
 #pragma unroll
       for (int i = 0; i < kUnroll; ++i) {
         const int c = c0 + (i * 32 + lane) * 8;
         if (c >= p.M) continue;
         d[i] = load16(dh + c);
-        a[i] = load16(s0 + c);
-        b[i] = load16(s1 + c);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          a[i][j] = load16(s0 + c + 4 * j);
+          b[i][j] = load16(s1 + c + 4 * j);
+        }
       }
 #pragma unroll
       for (int i = 0; i < kUnroll; ++i) {
@@ -118,8 +134,8 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const GradParams p
       const int end = min(c0 + kRun, p.M);
       for (int c = c0 + lane; c < end; c += 32) {
         const uint32_t d = dh[c];
-        o0[c] = static_cast<uint16_t>(mul2<BF>(d, s0[c]));
-        o1[c] = static_cast<uint16_t>(mul2<BF>(d, s1[c]));
+        o0[c] = static_cast<uint16_t>(mul2<BF>(d, s0[c], 0.0f));
+        o1[c] = static_cast<uint16_t>(mul2<BF>(d, s1[c], 0.0f));
       }
     }
   }
@@ -147,14 +163,14 @@ cudaError_t launch_gated_grad(const GatedGrad& q, int num_sms, cudaStream_t stre
   p.div_runs = fast_div(p.runs);
   p.offsets = q.offsets;
   p.dh = static_cast<const uint16_t*>(q.dh);
-  p.slopes = static_cast<const uint16_t*>(q.slopes);
+  p.slopes = q.slopes;
   p.out = static_cast<uint16_t*>(q.out);
   p.clear = static_cast<uint16_t*>(q.clear);
   p.ldc = q.ldc;
   p.K = static_cast<int>(q.K);
   auto aligned = [](const void* a) { return reinterpret_cast<uintptr_t>(a) % 16 == 0; };
   const bool vec = aligned(q.dh) && aligned(q.slopes) && aligned(q.out) && q.M % 8 == 0 && (q.T == 1 || q.lddh % 8 == 0) &&
-                   (q.T == 1 || q.lds % 8 == 0) && q.slope_plane % 8 == 0 && (q.T == 1 || q.ldo % 8 == 0);
+                   (q.T == 1 || q.lds % 4 == 0) && q.slope_plane % 4 == 0 && (q.T == 1 || q.ldo % 8 == 0);
   const int64_t units = q.T * std::max(p.runs, 1);  // rows that are cleared want warps too
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>((units + kWarps - 1) / kWarps, 8 * num_sms)));
   const bool bf = q.dtype == OZK_BF16;

@@ -55,7 +55,7 @@ struct Product {
   Mx4Matrix a, b;             // kMx4: rows and weights
   float alpha;
   int act;                    // kGated
-  void* slopes;               // [2][T][M], rows lds and the two slope_plane elements apart; or null
+  float* slopes;              // [2][T][M], rows lds and the two slope_plane elements apart; or null
   int64_t lds, slope_plane;
 };
 // dpre[t, m] = dh[t, m] slopes[0][t, m], dpre[t, M + m] = dh[t, m] slopes[1][t, m]
@@ -65,7 +65,8 @@ struct GatedGrad {
   int groups;
   const int32_t* offsets;
   int dtype;
-  const void *dh, *slopes;
+  const void* dh;
+  const float* slopes;
   int64_t lddh, lds, slope_plane;
   void* out;
   int64_t ldo;

@@ -80,8 +80,8 @@ int check_weights(const void* w, int64_t N, int64_t K, int64_t ldw, int groups, 
 bool known_activation(int a) { return a >= OZK_SILU && a <= OZK_GELU_TANH; }
 
 // The two slopes of a gated product: rows of N elements, lds apart, `plane` between the two.
-int check_slopes(const void* s, int64_t T, int64_t N, int64_t lds, int64_t plane) {
-  if (!s || reinterpret_cast<uintptr_t>(s) % 2 != 0 || lds < N || plane < (T - 1) * lds + N) return OZK_ERR_INVALID_ARG;
+int check_slopes(const float* s, int64_t T, int64_t N, int64_t lds, int64_t plane) {
+  if (!s || reinterpret_cast<uintptr_t>(s) % 4 != 0 || lds < N || plane < (T - 1) * lds + N) return OZK_ERR_INVALID_ARG;
   return OZK_OK;
 }
 
@@ -270,7 +270,7 @@ int ozk_grouped_gemm(int64_t T, int64_t N, int64_t K, int groups, const int32_t*
 
 int ozk_grouped_gated_gemm(int64_t T, int64_t N, int64_t K, int groups, const int32_t* offsets, const void* X,
                            int64_t ldx, const void* W, int64_t ldw, int64_t w_stride, int dtype, int activation,
-                           void* Y, int64_t ldy, void* slopes, int64_t lds, int64_t slope_stride,
+                           void* Y, int64_t ldy, float* slopes, int64_t lds, int64_t slope_stride,
                            ozk_stream_t stream) {
   int rc = check_grouped(T, N, K, groups, offsets, dtype, dtype);
   if (rc) return rc;
@@ -278,7 +278,7 @@ int ozk_grouped_gated_gemm(int64_t T, int64_t N, int64_t K, int groups, const in
   if (2 * N > kMaxFeatures) return OZK_ERR_UNSUPPORTED;
   if (T == 0 || N == 0) return OZK_OK;
   if (!Y || ldy < N || reinterpret_cast<uintptr_t>(Y) % 2 != 0) return OZK_ERR_INVALID_ARG;
-  const Span y = span(Y, T, N, ldy, 2), s = span(slopes, T, N, lds, 2, 2, slope_stride);
+  const Span y = span(Y, T, N, ldy, 2), s = span(slopes, T, N, lds, 4, 2, slope_stride);
   if (slopes) {
     if ((rc = check_slopes(slopes, T, N, lds, slope_stride))) return rc;
     if (overlap(y, s)) return OZK_ERR_INVALID_ARG;
@@ -315,7 +315,7 @@ int ozk_grouped_gated_gemm(int64_t T, int64_t N, int64_t K, int groups, const in
 }
 
 int ozk_gated_grad(int64_t T, int64_t N, int groups, const int32_t* offsets, const void* dH, int64_t lddh,
-                   const void* slopes, int64_t lds, int64_t slope_stride, int dtype, void* dpre, int64_t ldp,
+                   const float* slopes, int64_t lds, int64_t slope_stride, int dtype, void* dpre, int64_t ldp,
                    ozk_stream_t stream) {
   if (T < 0 || N < 0 || groups < 1 || (offsets == nullptr && groups != 1)) return OZK_ERR_INVALID_ARG;
   if (dtype != OZK_BF16 && dtype != OZK_F16) return OZK_ERR_UNSUPPORTED;
@@ -326,7 +326,7 @@ int ozk_gated_grad(int64_t T, int64_t N, int groups, const int32_t* offsets, con
   int rc = check_slopes(slopes, T, N, lds, slope_stride);
   if (rc) return rc;
   const Span d = span(dpre, T, 2 * N, ldp, 2);
-  if (overlap(d, span(dH, T, N, lddh, 2)) || overlap(d, span(slopes, T, N, lds, 2, 2, slope_stride)))
+  if (overlap(d, span(dH, T, N, lddh, 2)) || overlap(d, span(slopes, T, N, lds, 4, 2, slope_stride)))
     return OZK_ERR_INVALID_ARG;
   int sms = 0;
   if ((rc = current_device_supported(&sms))) return rc;
@@ -335,7 +335,7 @@ int ozk_gated_grad(int64_t T, int64_t N, int groups, const int32_t* offsets, con
 }
 
 int ozk_grouped_gated_gemm_grad(int64_t T, int64_t N, int64_t K, int groups, const int32_t* offsets, const void* dH,
-                                int64_t lddh, const void* slopes, int64_t lds, int64_t slope_stride, const void* X,
+                                int64_t lddh, const float* slopes, int64_t lds, int64_t slope_stride, const void* X,
                                 int64_t ldx, const void* W, int64_t ldw, int64_t w_stride, int dtype, void* dpre,
                                 int64_t ldp, void* dX, int64_t lddx, void* dW, int64_t lddw, int64_t dw_stride,
                                 ozk_stream_t stream) {
@@ -345,7 +345,7 @@ int ozk_grouped_gated_gemm_grad(int64_t T, int64_t N, int64_t K, int groups, con
   if (T > 0 && N > 0) {
     if (!dH || lddh < N || reinterpret_cast<uintptr_t>(dH) % 2 != 0) return OZK_ERR_INVALID_ARG;
     if ((rc = check_slopes(slopes, T, N, lds, slope_stride)) || (rc = check_operand(dpre, 2 * N, ldp))) return rc;
-    const Span d = span(dpre, T, 2 * N, ldp, 2), h = span(dH, T, N, lddh, 2), s = span(slopes, T, N, lds, 2, 2, slope_stride);
+    const Span d = span(dpre, T, 2 * N, ldp, 2), h = span(dH, T, N, lddh, 2), s = span(slopes, T, N, lds, 4, 2, slope_stride);
     if (overlap(d, h) || overlap(d, s) || overlap(d, span(X, T, K, ldx, 2)) ||
         overlap(d, span(W, 2 * N, K, ldw, 2, groups, w_stride)))
       return OZK_ERR_INVALID_ARG;

@@ -112,8 +112,8 @@ struct Config {
   // full, empty, tail and peer tail per stage (the tails: gradient of w);
   // accumulator full and empty; drain
   static constexpr int BARS = (OP == kGradWeights ? 4 : 2) * STAGES + 5;
-  // of each side of the epilogue: 32 rows of 128 16-bit columns; gated, of 64 and as many of both slopes
-  static constexpr uint32_t OUT_STAGE = GATED ? 12288 : 8192;
+  // of each side of the epilogue: 32 rows of 128 16-bit columns; gated, of 64 and as many fp32 ones of both slopes
+  static constexpr uint32_t OUT_STAGE = GATED ? 20480 : 8192;
   static constexpr uint32_t CTRL = 384;  // barriers, TMEM address, abort flag; from 256 on the loaders' last issues
   static constexpr uint32_t FIXED = 1024 + STAGES * STAGE + 2 * OUT_STAGE + CTRL;
   static_assert(8 * BARS + 8 <= 256 && 256 + 2 * 8 * STAGES <= CTRL, "control words");
@@ -132,7 +132,7 @@ struct ProductParams {
   int64_t ldo, out_group;
   float alpha;
   bool vec;        // 16-byte stores: a 16-bit output whose rows are 16-byte aligned
-  void* slopes;    // gated: the result's two slopes, [2][T][M], or null
+  float* slopes;   // gated: the result's two slopes, [2][T][M], or null
   int64_t lds, slope_plane;
   bool vec_slopes;
   int act;
@@ -532,8 +532,11 @@ __device__ __forceinline__ void store_edge(uint16_t* out, int64_t ldo, int rows,
 // the same rows of the other projection: read in the 16 x 256-bit form, a
 // thread has g and u of an output at the same place of two registers.  The
 // activation and the product are taken on the fp32 sums; what leaves is
-// rounded once.  Up to three blocks of 32 rows by 64 columns (the result, its
-// slopes by u and by g) go through shared memory as above.
+// rounded once.  A block of 32 rows by 64 columns of the result goes through
+// shared memory as above, and so do its slopes by g and by u where they are
+// asked for, in fp32, each as two halves of 32 columns: in 16 bits their
+// rounding was a third of the gradients' error (bf16: 0.29% of the norm, so
+// 0.24%, of which the results' own rounding is 0.17%).
 constexpr uint32_t kGatedBlock = 32 * 128;
 template <typename T>
 __device__ __forceinline__ void stage_gated(uint32_t block, int quad, int lane, const uint32_t (&v)[16]) {
@@ -547,7 +550,16 @@ __device__ __forceinline__ void stage_gated(uint32_t block, int quad, int lane, 
                  : "memory");
   }
 }
-// act(g) u over g, and where asked for the slopes u act'(g) and act(g).
+// This warp's 16 fp32 columns of 32 rows into a block of two halves.
+__device__ __forceinline__ void stage_slopes(uint32_t block, int quad, int lane, const uint32_t (&v)[16]) {
+  block += (quad >> 1) * kGatedBlock;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int c = 16 * (quad & 1) + (lane >> 2) + (i & 2 ? 8 : 0), n = 8 * (i >> 2) + 2 * (lane & 3) + (i & 1);
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(block + n * 128 + (((c >> 2) ^ (n & 7)) * 16) + (c & 3) * 4), "r"(v[i]) : "memory");
+  }
+}
+// act(g) u over g, and the slopes u act'(g) and act(g).
 template <int ACT>
 __device__ __forceinline__ void gate(uint32_t (&g)[16], uint32_t (&u)[16], bool slopes, uint32_t (&da)[16]) {
 #pragma unroll
@@ -568,31 +580,36 @@ __device__ __forceinline__ void stage_gate(uint32_t block, int quad, int lane, u
   else gate<OZK_GELU_TANH>(g, u, slopes, da);
   stage_gated<T>(block, quad, lane, g);
   if (slopes) {
-    stage_gated<T>(block + kGatedBlock, quad, lane, da);
-    stage_gated<T>(block + 2 * kGatedBlock, quad, lane, u);
+    stage_slopes(block + kGatedBlock, quad, lane, da);
+    stage_slopes(block + 3 * kGatedBlock, quad, lane, u);
   }
 }
-// `rows` rows and `cols` columns of such a block by ordinary stores: this warp's 8 rows.
-__device__ __forceinline__ void store_gated(uint16_t* out, int64_t ldo, int rows, int cols, uint32_t block, int quad, int lane,
-                                            bool vec) {
-  const int chunk = lane & 7;
+// `rows` rows and `cols` columns of such a block by ordinary stores: this
+// warp's 8 rows, of 64 columns of E in pieces of 16 bytes.
+template <typename E>
+__device__ __forceinline__ void store_gated(E* out, int64_t ldo, int rows, int cols, uint32_t block, int quad, int lane, bool vec) {
+  constexpr int kPer = 16 / sizeof(E), kPieces = 64 / kPer, kStep = 32 / kPieces;
+  const int chunk = lane % kPieces;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int n = 8 * quad + 4 * i + (lane >> 3);
-    if (n >= rows || 8 * chunk >= cols) continue;
+  for (int i = 0; i < 8; i += kStep) {
+    const int n = 8 * quad + i + lane / kPieces;
+    if (n >= rows || kPer * chunk >= cols) continue;
     uint4 w;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
                  : "r"(block + out_piece(n, chunk))
                  : "memory");
-    uint16_t* dst = out + n * ldo + 8 * chunk;
-    if (vec && 8 * chunk + 8 <= cols) {
+    E* dst = out + n * ldo + kPer * chunk;
+    if (vec && kPer * chunk + kPer <= cols) {
       *reinterpret_cast<uint4*>(dst) = w;
     } else {
       const uint32_t e[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (8 * chunk + j < cols) dst[j] = static_cast<uint16_t>(e[j / 2] >> (16 * (j & 1)));
+      for (int j = 0; j < kPer; ++j)
+        if (kPer * chunk + j < cols) {
+          if constexpr (sizeof(E) == 4) dst[j] = __uint_as_float(e[j]);
+          else dst[j] = static_cast<uint16_t>(e[j / 2] >> (16 * (j & 1)));
+        }
     }
   }
 }
@@ -1007,23 +1024,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           else stage_gate<__nv_bfloat16>(block, quad, lane, lo, hi, slopes, p.act);
           fence_proxy_async_smem();
           side_sync(side);
-          const bool whole = rows >= 32 && (cols >= C::COLS || (cols > 0 && cols % 8 == 0));  // see below
-          if (whole && p.vec) {
+          const bool inside = rows >= 32 && cols > 0;
+          if (inside && p.vec && (cols >= C::COLS || cols % 8 == 0)) {  // see below
             if (issuer) tma_store_3d(&tmO, block, m0, n, 0);
           } else if (cols > 0) {
             store_gated(static_cast<uint16_t*>(p.out) + static_cast<int64_t>(n) * p.ldo + m0, p.ldo, min(rows, 32), cols, block,
                         quad, lane, p.vec);
           }
           if (slopes) {
-            if (whole && p.vec_slopes) {
+            if (inside && p.vec_slopes && (cols >= C::COLS || cols % 4 == 0)) {
               if (issuer) {
-                tma_store_3d(&tmSW, block + kGatedBlock, m0, n, 0);
-                tma_store_3d(&tmSW, block + 2 * kGatedBlock, m0, n, 1);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  if (32 * (j & 1) < cols) tma_store_3d(&tmSW, block + (1 + j) * kGatedBlock, m0 + 32 * (j & 1), n, j >> 1);
               }
             } else if (cols > 0) {
-              uint16_t* s = static_cast<uint16_t*>(p.slopes) + static_cast<int64_t>(n) * p.lds + m0;
+              float* s = p.slopes + static_cast<int64_t>(n) * p.lds + m0;
               store_gated(s, p.lds, min(rows, 32), cols, block + kGatedBlock, quad, lane, p.vec_slopes);
-              store_gated(s + p.slope_plane, p.lds, min(rows, 32), cols, block + 2 * kGatedBlock, quad, lane, p.vec_slopes);
+              store_gated(s + p.slope_plane, p.lds, min(rows, 32), cols, block + 3 * kGatedBlock, quad, lane, p.vec_slopes);
             }
           }
           continue;
@@ -1197,7 +1215,7 @@ cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
     p.slopes = q.slopes;
     p.lds = q.lds;
     p.slope_plane = q.slope_plane;
-    p.vec_slopes = q.slopes && reinterpret_cast<uintptr_t>(q.slopes) % 16 == 0 && q.lds % 8 == 0 && q.slope_plane % 8 == 0;
+    p.vec_slopes = q.slopes && reinterpret_cast<uintptr_t>(q.slopes) % 16 == 0 && q.lds % 4 == 0 && q.slope_plane % 4 == 0;
   }
   const int64_t terms = OP == kGradWeights ? q.T : q.K;
   p.timeout_ns = kTimeoutNs + kStageNs * static_cast<uint64_t>(terms / C::BLOCK_K);
@@ -1275,11 +1293,9 @@ cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
       return cudaErrorInvalidValue;
   }
   if (p.vec_slopes) {
-    const int64_t dims[3] = {q.M, q.T, 2}, strides[2] = {2 * q.lds, 2 * q.slope_plane};
-    const uint32_t box[3] = {64, 32, 1};
-    if (!make_map(&tmSW, q.out_type == OZK_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                  q.slopes, dims, strides, box, true))
-      return cudaErrorInvalidValue;
+    const int64_t dims[3] = {q.M, q.T, 2}, strides[2] = {4 * q.lds, 4 * q.slope_plane};
+    const uint32_t box[3] = {32, 32, 1};
+    if (!make_map(&tmSW, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, q.slopes, dims, strides, box, true)) return cudaErrorInvalidValue;
   }
   auto kernel = product_kernel<OP, FMT, BN, PAIR>;
   const size_t table = (static_cast<size_t>(q.groups) + 1) * sizeof(Group);

@@ -837,8 +837,8 @@ def _load_gated():
         @staticmethod
         def forward(ctx, x, w, offsets, args):
             T, H = args[:2]
-            room = -(-H // 8) * 8
-            slopes = _torch.empty((2, T, room), dtype=x.dtype, device=x.device)
+            room = -(-H // 4) * 4
+            slopes = _torch.empty((2, T, room), dtype=_torch.float32, device=x.device)
             h = _torch.empty((T, H), dtype=x.dtype, device=x.device)
             _gated(args, h.data_ptr(), H or 1, slopes.data_ptr(), room, T * room)
             ctx.save_for_backward(x, w, offsets, slopes if room == H else slopes[:, :, :H])
@@ -859,8 +859,9 @@ def grouped_gated_gemm(x, w, offsets, activation: str = "silu", out=None, slopes
     """h[t] = act(x[t] @ w[g(t)][:H]^T) * (x[t] @ w[g(t)][H:]^T)
     (ozk_grouped_gated_gemm): x [T, K], w [groups, 2 H, K] of one 16-bit type,
     the gate's rows first; activation "silu", "gelu" or "gelu_tanh"; [T, H] of
-    their type.  Rows in no group are not written.  slopes, a [2, T, H] tensor,
-    takes dh/dgate and dh/dup, which gated_grad turns a gradient of h with.
+    their type.  Rows in no group are not written.  slopes, a [2, T, H] float32
+    tensor, takes dh/dgate and dh/dup, which gated_grad multiplies a gradient of
+    h by.
 
     Autograd records it where x or w asks for a gradient
     (grouped_gated_gemm_grad), once: there is no second derivative.  With out or
@@ -883,7 +884,7 @@ def grouped_gated_gemm(x, w, offsets, activation: str = "silu", out=None, slopes
         with _torch.cuda.stream(stream):
             return function.apply(x, w, offsets, args)
     out, ld, _ = _result(out, T, N // 2, x.dtype, x.device, stream)
-    at, lds, plane = (None, 0, 0) if slopes is None else _slopes(slopes, T, N // 2, x.dtype, index)
+    at, lds, plane = (None, 0, 0) if slopes is None else _slopes(slopes, T, N // 2, index)
     _gated(args, out.data_ptr(), ld, at, lds, plane)
     return out
 
@@ -894,12 +895,12 @@ def _gated(args, out, ld, slopes, lds, plane):
         raise OzkError("ozk_grouped_gated_gemm", rc)
 
 
-def _slopes(slopes, T, H, dtype, index):
+def _slopes(slopes, T, H, index):
     """(address, leading dimension, stride between the two) of a gated product's slopes."""
     if slopes.shape != (2, T, H):
         raise ValueError(f"slopes have shape {tuple(slopes.shape)}, (2, {T}, {H}) is expected")
-    if slopes.dtype != dtype:
-        raise TypeError(f"slopes are {slopes.dtype}, the operands {dtype}")
+    if slopes.dtype != _torch.float32:
+        raise TypeError(f"slopes are {slopes.dtype}, float32 is expected")
     _same_device(index, slopes)
     return (slopes.data_ptr(), *_groups(slopes)[3:])
 
@@ -915,10 +916,10 @@ def _plain_rows(t, dtype):
 
 def gated_grad(dh, slopes, offsets=None, out=None, stream=None):
     """The gradient with respect to a gated product's two projections
-    (ozk_gated_grad): dh [T, H] times each of slopes [2, T, H], side by side,
-    [T, 2 H] of the slopes' type (dh of another type is rounded to it).  With it
-    as dy, grouped_gemm_dx and grouped_gemm_dw give the gradients of x and w.
-    With offsets, rows in no group are not written."""
+    (ozk_gated_grad): dh [T, H], bf16 or fp16, times each of slopes [2, T, H],
+    side by side, [T, 2 H] of dh's type.  With it as dy, grouped_gemm_dx and
+    grouped_gemm_dw give the gradients of x and w.  With offsets, rows in no
+    group are not written."""
     if _torch is None:
         _load_torch()
     index = _device_index(slopes)
@@ -930,12 +931,12 @@ def gated_grad(dh, slopes, offsets=None, out=None, stream=None):
     if len(dh.shape) != 2:
         raise ValueError("expected a 2-D gradient")
     T, H = dh.shape
-    at, lds, plane = _slopes(slopes, T, H, slopes.dtype, index)
+    at, lds, plane = _slopes(slopes, T, H, index)
     if stream is not None:  # what is allocated belongs to the stream that writes it
         with _torch.cuda.stream(stream):
             return gated_grad(dh, slopes, offsets, out)
-    out, ld, kind = _result(out, T, 2 * H, slopes.dtype, slopes.device, None)
-    dh, lddh = _plain_rows(dh, slopes.dtype)
+    out, ld, kind = _result(out, T, 2 * H, dh.dtype, slopes.device, None)
+    dh, lddh = _plain_rows(dh, dh.dtype)
     rc = _lib.ozk_gated_grad(T, H, groups, None if offsets is None else offsets.data_ptr(), dh.data_ptr(), lddh, at, lds, plane,
                              kind, out.data_ptr(), ld, _current_stream(index))
     if rc:
@@ -959,7 +960,7 @@ def grouped_gated_gemm_grad(dh, x, w, offsets, slopes, need_dx: bool = True, nee
     if dh.shape != (T, N // 2):
         raise ValueError(f"the gradient has shape {tuple(dh.shape)}, the result ({T}, {N // 2})")
     _same_device(index, dh)
-    at, lds, plane = _slopes(slopes, T, N // 2, x.dtype, index)
+    at, lds, plane = _slopes(slopes, T, N // 2, index)
     if stream is not None:  # what is allocated belongs to the stream that writes it
         with _torch.cuda.stream(stream):
             return grouped_gated_gemm_grad(dh, x, w, offsets, slopes, need_dx, need_dw)

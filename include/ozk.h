@@ -486,23 +486,23 @@ int ozk_grouped_gemm_dw(int64_t T, int64_t N, int64_t K, int groups, const int32
  * gate's first, and Y[t, j] = act(g) u with g = sum_k x_tk w_g(t),j,k and u the
  * same with row N + j; g, u and the activation stay in fp32, Y (T x N, of
  * dtype) is rounded once.  slopes, where not NULL, takes what the gradients
- * need, both rounded to dtype: row t of the first matrix (rows lds elements
- * apart) is dY/dg = u act'(g), that of the second, slope_stride elements after
- * it, dY/du = act(g).  Operand requirements and groups as above, 2 N <= 2^22;
+ * need, in fp32: row t of the first matrix (rows lds elements apart) is dY/dg =
+ * u act'(g), that of the second, slope_stride elements after it, dY/du =
+ * act(g).  Operand requirements and groups as above, 2 N <= 2^22;
  * Y and slopes need the alignment of their type only. */
 int ozk_grouped_gated_gemm(int64_t T, int64_t N, int64_t K, int groups, const int32_t* offsets, const void* X,
                            int64_t ldx, const void* W, int64_t ldw, int64_t w_stride, int dtype, int activation,
-                           void* Y, int64_t ldy, void* slopes, int64_t lds, int64_t slope_stride,
+                           void* Y, int64_t ldy, float* slopes, int64_t lds, int64_t slope_stride,
                            ozk_stream_t stream);
 
 /* The gradient with respect to the two projections, from that of Y and the
  * slopes: dpre (T x 2 N) has dpre[t, j] = dh_tj dY/dg and dpre[t, N + j] =
- * dh_tj dY/du, each rounded once to dtype.  With it as dY, ozk_grouped_gemm_dx
+ * dh_tj dY/du, each rounded to fp32 and to dtype.  With it as dY, ozk_grouped_gemm_dx
  * and ozk_grouped_gemm_dw (of 2 N rows of w) give the gradients of x and w.
  * offsets as above, or NULL for all rows; rows in no group are not written.
  * Any alignment of the type. */
 int ozk_gated_grad(int64_t T, int64_t N, int groups, const int32_t* offsets, const void* dH, int64_t lddh,
-                   const void* slopes, int64_t lds, int64_t slope_stride, int dtype, void* dpre, int64_t ldp,
+                   const float* slopes, int64_t lds, int64_t slope_stride, int dtype, void* dpre, int64_t ldp,
                    ozk_stream_t stream);
 
 /* The whole backward pass in stream order: ozk_gated_grad, whose result is left
@@ -510,7 +510,7 @@ int ozk_gated_grad(int64_t T, int64_t N, int groups, const int32_t* offsets, con
  * the gradients of X (T x K; zeros in rows of no group) and of W (2 N x K per
  * group), each only where not NULL; both of dtype. */
 int ozk_grouped_gated_gemm_grad(int64_t T, int64_t N, int64_t K, int groups, const int32_t* offsets, const void* dH,
-                                int64_t lddh, const void* slopes, int64_t lds, int64_t slope_stride, const void* X,
+                                int64_t lddh, const float* slopes, int64_t lds, int64_t slope_stride, const void* X,
                                 int64_t ldx, const void* W, int64_t ldw, int64_t w_stride, int dtype, void* dpre,
                                 int64_t ldp, void* dX, int64_t lddx, void* dW, int64_t lddw, int64_t dw_stride,
                                 ozk_stream_t stream);

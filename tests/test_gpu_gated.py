@@ -10,8 +10,8 @@ import gated_reference as ref
 from fp64_gemm_emulation_exponent_gb300 import ozk
 
 pytestmark = pytest.mark.gpu
-HALF = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
-LEAST = {torch.bfloat16: 2.0 ** -126, torch.float16: 2.0 ** -24}
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
+LEAST = {torch.bfloat16: 2.0 ** -126, torch.float16: 2.0 ** -24, torch.float32: 2.0 ** -126}
 # rows of each group, H, K
 SHAPES = [([1], 1, 8), ([1], 8, 8), ([5, 0, 17], 64, 64), ([130, 3, 0, 64], 136, 264), ([300, 1], 36, 1032), ([1] * 24, 256, 512),
           ([16, 15, 0, 0, 49, 128, 129], 200, 136), ([700, 0, 260], 296, 520), ([61] * 30, 264, 520), ([2000], 513, 200),
@@ -46,15 +46,15 @@ def near(got, exact, bound, dtype, extra=0.0):
 @pytest.mark.parametrize("act", ref.ACTS)
 def test_product_and_slopes(counts, H, K, dtype, act):
     x, w, offsets, starts = setup(counts, H, K, dtype)
-    slopes = torch.empty(2, x.shape[0], H, dtype=dtype, device="cuda")
+    slopes = torch.empty(2, x.shape[0], H, device="cuda")
     h = ozk.grouped_gated_gemm(x, w, offsets, activation=act, slopes=slopes)
     assert torch.equal(h, ozk.grouped_gated_gemm(x, w, offsets, activation=act))  # the same with and without slopes
     X, W = wide(x), wide(w)
     for g, (a, b) in enumerate(zip(starts, starts[1:])):
         r = ref.Gated(X[a:b], W[g], act)
         near(h[a:b], r.h, r.dh, dtype)
-        near(slopes[0, a:b], r.by_gate, r.d_gate, dtype)
-        near(slopes[1, a:b], r.by_up, r.d_up, dtype)
+        near(slopes[0, a:b], r.by_gate, r.d_gate, torch.float32)
+        near(slopes[1, a:b], r.by_up, r.d_up, torch.float32)
     assert ozk.ozk_stream_status() == 0
 
 
@@ -62,8 +62,8 @@ def test_product_and_slopes(counts, H, K, dtype, act):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("act", ref.ACTS)
 def test_gradients(counts, H, K, dtype, act):
-    """The slopes are rounded to 16 bits, and so is the gradient of the projections; each rounding is off by at most half
-    a step of its value, and the products sum 2 H (rows of the group) terms in fp32."""
+    """The slopes are in fp32, the gradient of the projections is rounded to fp32 and to 16 bits; a rounding is off by at
+    most half a step of its value, and the products sum 2 H (rows of the group) terms in fp32."""
     x, w, offsets, starts = setup(counts, H, K, dtype)
     dh = normal(x.shape[0], H, seed=3, dtype=dtype)
     x.requires_grad_(), w.requires_grad_()
@@ -74,7 +74,7 @@ def test_gradients(counts, H, K, dtype, act):
     for g, (a, b) in enumerate(zip(starts, starts[1:])):
         r = ref.Gated(X[a:b], W[g], act)
         pre = np.concatenate((D[a:b] * r.by_gate, D[a:b] * r.by_up), axis=1)
-        err = np.concatenate([np.abs(D[a:b]) * ref.rounded(e, v, HALF[dtype], LEAST[dtype])
+        err = np.concatenate([np.abs(D[a:b]) * ref.rounded(e, v, 2.0 ** -23, 2.0 ** -126)
                               for v, e in ((r.by_gate, r.d_gate), (r.by_up, r.d_up))], axis=1)
         err = ref.rounded(err, pre, HALF[dtype], LEAST[dtype])
         mags = np.abs(pre) + err
@@ -89,7 +89,7 @@ def test_rows_in_no_group(H):
     x, w, offsets, starts = setup([9, 0, 40], H, 72, torch.bfloat16, before=3, after=6)
     T, inner = x.shape[0], slice(starts[0], starts[-1])
     out = torch.full((T, H), 7.0, dtype=x.dtype, device="cuda")
-    slopes = torch.full((2, T, H), 7.0, dtype=x.dtype, device="cuda")
+    slopes = torch.full((2, T, H), 7.0, device="cuda")
     ozk.grouped_gated_gemm(x, w, offsets, out=out, slopes=slopes)
     dpre = torch.full((T, 2 * H), 7.0, dtype=x.dtype, device="cuda")
     dh = normal(T, H, seed=3, dtype=x.dtype)
@@ -97,7 +97,7 @@ def test_rows_in_no_group(H):
     for t in (out, slopes[0], slopes[1], dpre):
         assert bool((t[: starts[0]] == 7).all()) and bool((t[starts[-1]:] == 7).all()) and not bool((t[inner] == 7).all())
     for half in range(2):
-        want = (dh[inner].double() * slopes[half, inner].double()).to(x.dtype)
+        want = (dh[inner].float() * slopes[half, inner]).to(x.dtype)  # rounded to fp32 and to 16 bits
         assert torch.equal(dpre[inner, half * H: half * H + H], want)
     x.requires_grad_()
     h = ozk.grouped_gated_gemm(x, w, offsets)
@@ -109,18 +109,17 @@ def test_rows_in_no_group(H):
 @pytest.mark.parametrize("T,H", [(1, 1), (3, 7), (5, 1024), (17, 1032), (300, 2056)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 def test_gated_grad_alone(T, H, dtype):
-    """Exact products, each rounded once; any alignment; a gradient of another type is rounded first."""
-    slopes, dh = normal(2, T, H, seed=4, dtype=dtype), normal(T, H, seed=5, dtype=torch.float32)
-    d16 = dh.to(dtype)
-    want = torch.cat((d16.double() * slopes[0].double(), d16.double() * slopes[1].double()), dim=1).to(dtype)
-    assert torch.equal(ozk.gated_grad(d16, slopes), want) and torch.equal(ozk.gated_grad(dh, slopes), want)
+    """Products rounded to fp32 and to 16 bits; any alignment."""
+    slopes, d16 = normal(2, T, H, seed=4, dtype=torch.float32), normal(T, H, seed=5, dtype=dtype)
+    want = torch.cat((d16.float() * slopes[0], d16.float() * slopes[1]), dim=1).to(dtype)
+    assert torch.equal(ozk.gated_grad(d16, slopes), want)
     room = torch.full((T, 2 * H + 3), 9.0, dtype=dtype, device="cuda")
-    odd = torch.empty(2, T, H + 5, dtype=dtype, device="cuda")[:, :, 3: H + 3]
+    odd = torch.empty(2, T, H + 5, device="cuda")[:, :, 3: H + 3]
     odd.copy_(slopes)
     ozk.gated_grad(d16, odd, out=room[:, 1: 2 * H + 1])
     assert torch.equal(room[:, 1: 2 * H + 1], want) and bool((room[:, 0] == 9).all()) and bool((room[:, 2 * H + 1:] == 9).all())
     one = torch.ones((), dtype=dtype, device="cuda").expand(T, H)
-    assert torch.equal(ozk.gated_grad(one, slopes), torch.cat((slopes[0], slopes[1]), dim=1))
+    assert torch.equal(ozk.gated_grad(one, slopes), torch.cat((slopes[0], slopes[1]), dim=1).to(dtype))
 
 
 def test_results_beside_others():
@@ -129,7 +128,7 @@ def test_results_beside_others():
     want = ozk.grouped_gated_gemm(x, w, offsets)
     for left in (0, 3, 8):
         room = torch.full((100, 40 + left + 5), 9.0, dtype=x.dtype, device="cuda")
-        sroom = torch.full((2, 100, 40 + left + 8), 9.0, dtype=x.dtype, device="cuda")
+        sroom = torch.full((2, 100, 40 + left + 8), 9.0, device="cuda")
         ozk.grouped_gated_gemm(x, w, offsets, out=room[:, left: left + 40], slopes=sroom[:, :, left: left + 40])
         assert torch.equal(room[:, left: left + 40], want)
         for t in (room, sroom[0], sroom[1]):
@@ -140,7 +139,7 @@ def test_no_terms():
     x = torch.empty(4, 0, dtype=torch.bfloat16, device="cuda")
     w = torch.empty(2, 16, 0, dtype=torch.bfloat16, device="cuda")
     offsets = torch.tensor([0, 3, 4], dtype=torch.int32, device="cuda")
-    slopes = torch.full((2, 4, 8), 9.0, dtype=x.dtype, device="cuda")
+    slopes = torch.full((2, 4, 8), 9.0, device="cuda")
     assert not ozk.grouped_gated_gemm(x, w, offsets, slopes=slopes).any() and not slopes.any()
 
 
@@ -165,7 +164,7 @@ def test_bad_offsets_are_cut_and_reported():
     got = ozk.grouped_gated_gemm(x, w, bad)
     assert ozk.ozk_stream_status() == ozk.OZK_ERR_INVALID_ARG
     assert torch.equal(got, ozk.grouped_gated_gemm(x, w, cut))
-    slopes, dh = normal(2, 30, 64, seed=1, dtype=x.dtype), normal(30, 64, seed=2, dtype=x.dtype)
+    slopes, dh = normal(2, 30, 64, seed=1, dtype=torch.float32), normal(30, 64, seed=2, dtype=x.dtype)
     assert torch.equal(ozk.gated_grad(dh, slopes, bad), ozk.gated_grad(dh, slopes))
     assert ozk.ozk_stream_status() == ozk.OZK_ERR_INVALID_ARG
     assert ozk.ozk_stream_status() == 0
@@ -202,7 +201,7 @@ def test_replayed_with_other_rows():
     """A captured graph of the product and its gradients, replayed with other values and offsets."""
     x, w, offsets, _ = setup([50, 14], 72, 136, torch.bfloat16)
     dh = normal(64, 72, seed=3, dtype=x.dtype)
-    slopes = torch.empty(2, 64, 72, dtype=x.dtype, device="cuda")
+    slopes = torch.empty(2, 64, 72, device="cuda")
 
     def step():
         h = ozk.grouped_gated_gemm(x, w, offsets, slopes=slopes)
@@ -245,18 +244,20 @@ def test_refusals():
     with pytest.raises(TypeError):
         ozk.grouped_gated_gemm(x.half(), w, offsets)
     with pytest.raises(TypeError):
-        ozk.grouped_gated_gemm(x, w, offsets, slopes=torch.empty(2, 16, 32, device="cuda"))
+        ozk.grouped_gated_gemm(x, w, offsets, slopes=torch.empty(2, 16, 32, dtype=x.dtype, device="cuda"))
     with pytest.raises(ValueError):
-        ozk.grouped_gated_gemm(x, w, offsets, slopes=torch.empty(2, 16, 31, dtype=x.dtype, device="cuda"))
+        ozk.grouped_gated_gemm(x, w, offsets, slopes=torch.empty(2, 16, 31, device="cuda"))
     with pytest.raises(ValueError):
         ozk.grouped_gated_gemm(x, w, offsets[:2].contiguous())
-    slopes = torch.empty(2, 16, 32, dtype=x.dtype, device="cuda")
+    slopes = torch.empty(2, 16, 32, device="cuda")
     with pytest.raises(ValueError):
         ozk.gated_grad(torch.empty(16, 31, dtype=x.dtype, device="cuda"), slopes)
     with pytest.raises(ValueError):
         ozk.gated_grad(torch.empty(16, 32, dtype=x.dtype), slopes)
     with pytest.raises(ozk.OzkError):
-        ozk.gated_grad(slopes[0], slopes, out=torch.empty(0, dtype=x.dtype, device="cuda").set_(slopes.untyped_storage(), 0, (16, 64)))
+        ozk.gated_grad(slopes[0], slopes)  # a gradient in fp32
+    with pytest.raises(ozk.OzkError):  # a result over the slopes
+        ozk.gated_grad(x[:, :32], slopes, out=slopes.view(x.dtype)[0, :, :].view(16, 64))
 
 
 @pytest.mark.parametrize("H,K", [(61, 72), (64, 40)])
@@ -265,14 +266,14 @@ def test_backward_pass_in_one_call(H, K):
     for is not computed."""
     x, w, offsets, starts = setup([9, 0, 40], H, K, torch.bfloat16, before=3, after=6)
     T = x.shape[0]
-    slopes = normal(2, T, H, seed=4, dtype=x.dtype)
-    dh = normal(T, H, seed=3, dtype=torch.float32)
+    slopes = normal(2, T, H, seed=4, dtype=torch.float32)
+    dh = normal(T, H, seed=3, dtype=x.dtype)
     torch.full((1 << 18,), float("nan"), device="cuda", dtype=torch.bfloat16)  # what unwritten memory would hold
     room = torch.zeros(T, -(-2 * H // 8) * 8, dtype=x.dtype, device="cuda")
     dpre = ozk.gated_grad(dh, slopes, offsets, out=room[:, : 2 * H])
     want_x = ozk.grouped_gemm_dx(dpre, w, offsets, out=torch.zeros(T, K, dtype=x.dtype, device="cuda"))
     want_w = ozk.grouped_gemm_dw(dpre, x, offsets)
-    dx, dw = ozk.grouped_gated_gemm_grad(dh, x, w, offsets, slopes)
+    dx, dw = ozk.grouped_gated_gemm_grad(dh.float(), x, w, offsets, slopes)  # rounded to bf16 again
     assert torch.equal(dx, want_x) and torch.equal(dw, want_w) and not dw[1].any()
     assert ozk.grouped_gated_gemm_grad(dh, x, w, offsets, slopes, need_dw=False)[1] is None
     dx, dw = ozk.grouped_gated_gemm_grad(dh, x, w, offsets, slopes, need_dx=False)
@@ -294,11 +295,11 @@ def test_far_arguments(act):
     w = torch.zeros(1, 2, 8, dtype=torch.bfloat16, device="cuda")
     w[0, 0, 0] = w[0, 1, 1] = 1.0  # g is the first element, u is 1
     offsets = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
-    slopes = torch.empty(2, 8, 1, dtype=x.dtype, device="cuda")
+    slopes = torch.empty(2, 8, 1, device="cuda")
     h = ozk.grouped_gated_gemm(x, w, offsets, activation=act, slopes=slopes)
     want = torch.clamp(x[:, 0], min=0.0)
-    assert torch.equal(h[:, 0], want) and torch.equal(slopes[1, :, 0], want)
-    assert torch.equal(slopes[0, :, 0], (x[:, 0] > 0).to(x.dtype))
+    assert torch.equal(h[:, 0], want) and torch.equal(slopes[1, :, 0], want.float())
+    assert torch.equal(slopes[0, :, 0], (x[:, 0] > 0).float())
 
 
 @pytest.mark.parametrize("H,K,T", [(0, 16, 5), (8, 16, 0), (0, 16, 0)])
