@@ -2,9 +2,10 @@
 //   y[t, n] = alpha sum_k x[t, k] w[g(t)][n, k], and its gated form
 //   h[t, n] = act(alpha sum_k x[t, k] w[g][n, k]) (alpha sum_k x[t, k] w[g][H + n, k]).
 //
-// What bounds them is reading the weights once: N K (1/2 + 1/block) bytes,
-// 42 weights a cycle and SM at the measured 6.8 TB/s, so the work on a weight
-// between memory and its product is kept below 4 x 512 weights in 48 cycles:
+// The floor is reading the weights once: N K (1/2 + 1/block) bytes, 42 weights
+// a cycle and SM at the measured 6.8 TB/s, or a quarter of an SM's 512 weights
+// (a unit: 32 columns of 16 rows) in 48 cycles.  The work on a weight between
+// memory and its product decides how near the kernel comes:
 //   - E2M1 codes become fp16 pairs by one conversion a byte (64 lanes a cycle
 //     and SM); as fp16 they are exact, and so are NVFP4 codes times their
 //     E4M3 scale (6 significant bits).  MXFP4 scales reach past fp16, and
@@ -25,10 +26,28 @@
 // so take part in further passes over the chunk, 27 binades at a time.
 //
 // A block owns 16 R output rows of w (gated: 8 R of each projection) and all
-// of K; its warps take the chunks of 128 columns in turn, each through a ring
-// of its own in shared memory (codes, scales and x) filled by asynchronous
+// of K; its warps take the chunks of 128 or 256 columns in turn, each through a
+// ring of its own in shared memory (codes, scales and x) filled by asynchronous
 // copies, no barrier between them, and the warps' sums are added at the end in
 // a fixed order.
+//
+// Measured on a GB300 (us in replayed graphs, weights from HBM; floor at 6.79
+// TB/s): 8192 x 4096 NVFP4, 1 row 6.8, 8 rows 7.7, 16 rows 9.5 (2.8, and some 2
+// of a launch); 8192 x 8192 11.0, 11.8, 15.7 (5.6); 1024 x 4096 3.3, 4.0, 5.5;
+// 32 rows over 32 experts, 4096 -> 2048 MXFP4, 20.7 (10.6).  With one row the
+// schedulers issue 54% of the time (36 instructions a unit, 18.5 of them the
+// conversions, scales and products themselves, on 3.3 warps a scheduler); two
+// blocks on some SMs and one on others cost another sixth.  Without the products
+// the loop runs at 82% of HBM's rate.
+// The steps (16 x 8192 x 8192 / 1 x 8192 x 4096, us): x staged as fp16 for the
+// whole block, panel by panel 58.8 / 10.7; rings and conversion per warp 24.3 /
+// 11.9; chunks of 256 columns, blocks of two tiles 21.3 / 7.8; copies without
+// tests 18.3 / 7.6; the rare wide chunk out of line, scale words of all tiles in
+// one copy 17.9 / 7.8; 8 warps of 255 registers 16.6; the first chunk's prefetch
+// 15.7 / 6.8.
+// What did not help: more warps a block at the price of registers (30% slower
+// with 16 rows), three blocks an SM, prefetching further ahead, whole ranges of
+// columns to L2 for grouped rows (13% slower).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -428,7 +447,9 @@ __device__ __noinline__ void multiply_wide(uint32_t at, uint32_t xat, int tokens
   }
 }
 
-// Blocks of an SM that registers are kept for.
+// Blocks of an SM that registers are kept for: 16 warps of 128 registers, but for
+// 16 rows on four tiles 8 warps of 255 (16 x 8192 x 4096 NVFP4 11.7 us with 16
+// warps a block, 10.9 with two blocks of 8, 10.3 so).
 constexpr int blocks_of(int R, int NT, int W) { return (NT == 0 && R == 1 ? 24 : R == 4 && NT == 2 ? 8 : 16) / W; }
 
 template <int FMT, int R, int NT, int W, bool GATED, bool BF>
@@ -762,6 +783,18 @@ cudaError_t launch(GemvParams p, cudaStream_t stream) {
   return launch_dependent(kernel, grid, dim3(32 * W), S::bytes(p.tokens), stream, p);
 }
 
+// The block's form by the rows of x and the tiles of 16 rows of w.  More tiles
+// a block (R) spread the conversion of x over more weights, more warps (W) the
+// columns over more of the SM; what serves best is some 2048 warps in all with
+// up to two rows, and blocks for nearly every SM with more.  NVFP4, us, the form
+// taken and the next best: 1 x 16384 x 4096 11.8 and 13.6 (8 warps); 1 x 8192 x
+// 8192 12.1 and 12.9 (4 warps); 1 x 4096 x 16384 12.0 and 13.3 (8 warps); 1 x 1024
+// x 4096 3.6 and 4.2 (two tiles).  8 x 16384 x 4096 12.9 and 14.1 (two tiles); 8 x
+// 8192 x 8192 13.1 and 13.9 (8 warps); 8 x 4096 x 16384 14.6 and 18.1 (8 warps); 8 x
+// 1024 x 4096 4.1 and 5.3 (two tiles).  32 rows over 32 experts 21.0 and 22.6 (8
+// warps).  16 x 8192 x 8192 16.7 and 17.9 (16 warps); 16 x 4096 x 16384 19.1 and 21.9
+// (8 warps); 16 x 1024 x 4096 5.5 and 6.7 (two tiles).  Tiles of 32 rows of x took
+// longer than two runs of 16 (45 and 33 us at 8192 x 8192).
 template <int FMT, bool GATED, bool BF>
 cudaError_t choose(const GemvParams& p, int num_sms, cudaStream_t stream) {
   const int active = p.offsets ? std::min(p.groups, p.T) : 1;

@@ -36,7 +36,11 @@
 //     weights are read for two tiles of rows only, HBM and MMAs about even
 //   1 x 8192 x 4096 NVFP4: 5.9 us, 2.1 of them a launch with nothing to do; one
 //     SM takes in 64-74 bytes a cycle, and the 64 tiles are on 64 SMs
-// What did not help: prefetching the next tile's operands into L2 by TMA (10-20%
+//   gated, 8192 rows over 16 groups, 4096 -> 2048, bf16: 183 us, 1.50 PFLOP/s; 8
+//     groups of 2048 rows, 4096 x 4096 with both slopes in fp32 666 us, 1.65
+//     PFLOP/s (power limit; the gradients' products of the same size 631-679)
+// What did not help: one copy of five dimensions for the gated product's 64 + 64
+// rows of w in place of four of 16 + 16 (no change); prefetching the next tile's operands into L2 by TMA (10-20%
 // slower: the copies' requests are what is short) or the weights' lines by an
 // idle warp 16 stages ahead (no change; 40 ahead 18% slower), scale tiles multicast in
 // the pair, a cluster of two or four CTAs along the terms of a small call (the

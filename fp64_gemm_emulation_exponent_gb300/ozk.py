@@ -905,11 +905,12 @@ def _slopes(slopes, T, H, index):
     return (slopes.data_ptr(), *_groups(slopes)[3:])
 
 
-def _plain_rows(t, dtype):
+def _plain_rows(t, dtype, stream):
     """(t, leading dimension), t rounded to dtype and laid out in rows where it is not (an expanded gradient)."""
     (rows, cols), (sr, sc) = t.shape, t.stride()
     if t.dtype != dtype or sc != 1 and cols > 1 or sr < cols and rows > 1:
-        t = t.to(dtype).contiguous()
+        with _torch.cuda.stream(stream):
+            t = t.to(dtype).contiguous()
         return t, cols or 1
     return t, sr if rows > 1 else _one_row(cols)
 
@@ -932,13 +933,11 @@ def gated_grad(dh, slopes, offsets=None, out=None, stream=None):
         raise ValueError("expected a 2-D gradient")
     T, H = dh.shape
     at, lds, plane = _slopes(slopes, T, H, index)
-    if stream is not None:  # what is allocated belongs to the stream that writes it
-        with _torch.cuda.stream(stream):
-            return gated_grad(dh, slopes, offsets, out)
-    out, ld, kind = _result(out, T, 2 * H, dh.dtype, slopes.device, None)
-    dh, lddh = _plain_rows(dh, dh.dtype)
+    handle = _stream_at(index, stream)
+    out, ld, kind = _result(out, T, 2 * H, dh.dtype, slopes.device, stream)
+    dh, lddh = _plain_rows(dh, dh.dtype, stream)
     rc = _lib.ozk_gated_grad(T, H, groups, None if offsets is None else offsets.data_ptr(), dh.data_ptr(), lddh, at, lds, plane,
-                             kind, out.data_ptr(), ld, _current_stream(index))
+                             kind, out.data_ptr(), ld, handle)
     if rc:
         raise OzkError("ozk_gated_grad", rc)
     return out
@@ -961,19 +960,16 @@ def grouped_gated_gemm_grad(dh, x, w, offsets, slopes, need_dx: bool = True, nee
         raise ValueError(f"the gradient has shape {tuple(dh.shape)}, the result ({T}, {N // 2})")
     _same_device(index, dh)
     at, lds, plane = _slopes(slopes, T, N // 2, index)
-    if stream is not None:  # what is allocated belongs to the stream that writes it
-        with _torch.cuda.stream(stream):
-            return grouped_gated_gemm_grad(dh, x, w, offsets, slopes, need_dx, need_dw)
-    empty, dtype, device = _torch.empty, x.dtype, x.device
-    dh, lddh = _plain_rows(dh, dtype)
+    handle, dtype, device = _stream_at(index, stream), x.dtype, x.device
+    dh, lddh = _plain_rows(dh, dtype, stream)
     ldp = -(-N // 8) * 8  # rows that bulk copies can read
-    dpre = empty((T, ldp), dtype=dtype, device=device)
-    dx = empty((T, K), dtype=dtype, device=device) if need_dx else None
-    dw = empty((groups, N, K), dtype=dtype, device=device) if need_dw else None
+    dpre = _empty((T, ldp), dtype, device, stream)
+    dx = _empty((T, K), dtype, device, stream) if need_dx else None
+    dw = _empty((groups, N, K), dtype, device, stream) if need_dw else None
     rc = _lib.ozk_grouped_gated_gemm_grad(
         T, N // 2, K, groups, offsets.data_ptr(), dh.data_ptr(), lddh, at, lds, plane, x.data_ptr(), ldx, w.data_ptr(), ldw,
         stride, kind, dpre.data_ptr(), ldp, dx.data_ptr() if need_dx else None, K or 1, dw.data_ptr() if need_dw else None,
-        K or 1, N * (K or 1), _current_stream(index))
+        K or 1, N * (K or 1), handle)
     if rc:
         raise OzkError("ozk_grouped_gated_gemm_grad", rc)
     return dx, dw

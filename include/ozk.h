@@ -444,8 +444,9 @@ typedef enum { OZK_SILU = 0, OZK_GELU = 1, OZK_GELU_TANH = 2 } ozk_activation;
 /* Y[t, j] = alpha * sum_k x_tk w_g(t),j,k for a few rows: X is T x K of dtype
  * OZK_BF16 or OZK_F16, as it is (not quantised), any alignment of its type; w
  * as in ozk_mx4_grouped_gemm.  offsets as there, or NULL for one group.  Any T
- * is taken; the weights are read once for every 8 to 32 rows of a group, so
- * that past some 32 quantised rows and ozk_mx4_grouped_gemm are faster.  Y: T x
+ * is taken; the weights are read once for every 2, 8 or 16 rows of a group, and
+ * past some 8 rows (with many columns) to 16 quantised rows and
+ * ozk_mx4_grouped_gemm are faster.  Y: T x
  * N of OZK_BF16, OZK_F16 or OZK_F32, ldy >= N, any alignment of its own type;
  * it must overlap nothing.  x is used exactly, whatever its range; sums are
  * formed in fp32 (with MXFP4 scales above 2^96 one may overflow where its

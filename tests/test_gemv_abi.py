@@ -48,9 +48,10 @@ def test_activations():
         assert gated(act=bad) == INVALID
 
 
-def test_loads_stay_behind_the_wait_for_the_kernel_before():
+@pytest.mark.parametrize("name", ["gemv.cu", "gated_grad.cu", "activation.cuh"])
+def test_loads_stay_behind_the_wait_for_the_kernel_before(name):
     """As for the other kernels: no read through the non-coherent path, none that may move over the wait."""
-    text = open(os.path.join(ozk_build.CSRC, "gemv.cu")).read()
+    text = open(os.path.join(ozk_build.CSRC, name)).read()
     text = re.sub(r"//[^\n]*", "", text)
     assert "__ldg" not in text and "__restrict__" not in text
     assert not re.search(r"\bld\.global[.\w:]*\.nc\b", text)
