@@ -18,10 +18,31 @@ __device__ __forceinline__ float act_logistic(float z) { return __fdividef(1.0f,
 constexpr float kGeluA = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f * kGeluA;
 
+// The normal distribution's tail beyond |g|, e^(-g^2/2) t p(t) with t = 1 / (1 +
+// 0.3 |g|): what the exponential leaves is smooth in t, and p, of degree 7, is
+// fitted to it for 0 <= |g| <= 14 by least squares at Chebyshev's points,
+// reweighted towards the largest relative error (1.5e-7; 5e-7 in fp32, the
+// exponential aside).  With erfcf in its place the epilogue of a product with
+// gelu cost 3.5 us more on 1999 rows, 1032 -> 520, and 30 of 180 on 8192 rows,
+// 4096 -> 2048: its instructions slow the warps that issue copies and MMAs.
+__device__ __forceinline__ float normal_tail(float g) {
+  const float t = __fdividef(1.0f, fmaf(0.3f, fabsf(g), 1.0f));
+  float p = 0.03567477688193321f;
+  p = fmaf(p, t, -0.15720310807228088f);
+  p = fmaf(p, t, 0.20635353028774261f);
+  p = fmaf(p, t, -0.05368367210030556f);
+  p = fmaf(p, t, 0.12856164574623108f);
+  p = fmaf(p, t, 0.09991348534822464f);
+  p = fmaf(p, t, 0.12075395882129669f);
+  p = fmaf(p, t, 0.11962930113077164f);
+  return __expf(-0.5f * g * g) * (t * p);
+}
+
 __device__ __forceinline__ float act_p(float g, int act) {
   if (act == OZK_SILU) return act_logistic(g);
   if (act == OZK_GELU_TANH) return act_logistic(g * fmaf(kGeluB, g * g, kGeluA));
-  return 0.5f * erfcf(g * -0.70710678118654752f);
+  const float tail = normal_tail(g);
+  return g < 0.0f ? tail : 1.0f - tail;
 }
 __device__ __forceinline__ float act_value(float g, int act) { return g * act_p(g, act); }
 

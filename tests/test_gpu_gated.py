@@ -313,3 +313,26 @@ def test_nothing_to_multiply(H, K, T):
     dx, dw = torch.autograd.grad(h, (x, w), torch.ones_like(h))
     assert dx.shape == x.shape and not dx.any() and dw.shape == w.shape and not dw.any()
     assert ozk.ozk_stream_status() == 0
+
+
+@pytest.mark.parametrize("act", ref.ACTS)
+def test_the_activation_itself(act):
+    """The second slope is act(g) in fp32, the first act'(g) where u is 1: at every fp16 value of g from -8 to 8.  Off by
+    off(g) of act(g) (gated_reference).  act' = P + g P' has terms of at most 1 and 1.2, in silu's and gelu_tanh's case
+    g P (1 - P) z', where 1 - P may be off by all of P's error: off(g) P (1 + 2 |g| z') together, below 64 units times 8
+    where P is not tiny (|z| <= 19), and nothing elsewhere."""
+    g = torch.arange(1 << 16, dtype=torch.int32, device="cuda").to(torch.int16).view(torch.float16)
+    g = g[torch.isfinite(g) & (g.abs() <= 8)]
+    x = torch.zeros(g.numel(), 8, dtype=torch.float16, device="cuda")
+    x[:, 0], x[:, 1] = g, 1.0
+    w = torch.zeros(1, 2, 8, dtype=torch.float16, device="cuda")
+    w[0, 0, 0] = w[0, 1, 1] = 1.0
+    offsets = torch.tensor([0, g.numel()], dtype=torch.int32, device="cuda")
+    slopes = torch.empty(2, g.numel(), 1, device="cuda")
+    ozk.grouped_gated_gemm(x, w, offsets, activation=act, slopes=slopes)
+    value, slope = ref.act(wide(g), act)
+    tail = np.array([math.erfc(-v * math.sqrt(0.5)) / 2 for v in wide(g)]) if act == "gelu" else None
+    if tail is not None:  # 1 + erf loses the tail's digits to 64 bits
+        value = wide(g) * tail
+    assert np.all(np.abs(wide(slopes[1, :, 0]) - value) <= ref.off(wide(g), act) * np.abs(value) + 2.0 ** -140)
+    assert np.all(np.abs(wide(slopes[0, :, 0]) - slope) <= 64 * 2.0 ** -23 * 8)
