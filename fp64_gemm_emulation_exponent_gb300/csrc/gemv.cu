@@ -45,7 +45,9 @@
 // tests 18.3 / 7.6; the rare wide chunk out of line, scale words of all tiles in
 // one copy 17.9 / 7.8; 8 warps of 255 registers 16.6; the first chunk's prefetch
 // 15.7 / 6.8.
-// What did not help: more warps a block at the price of registers (30% slower
+// What did not help: rows of x converted by all lanes together where a tile has
+// three or fewer (a fifth fewer instructions, 5% slower: a longer way from the
+// copy to the products), more warps a block at the price of registers (30% slower
 // with 16 rows), three blocks an SM, prefetching further ahead, whole ranges of
 // columns to L2 for grouped rows (13% slower).
 #include <cuda_bf16.h>

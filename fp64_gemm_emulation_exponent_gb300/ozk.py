@@ -678,7 +678,7 @@ def mx4_gemv(x, w: Mx4, offsets=None, alpha: float = 1.0, out_dtype=None, out=No
     """alpha * x_t @ w_g(t)^T for a few rows of 16-bit x, not quantised
     (ozk_mx4_gemv): x [T, K] bf16 or fp16, w a matrix of one group, or from a
     [groups, N, K] tensor with offsets for the rows of x; [T, N] of out_dtype
-    (default x's).  Rows in no group are not written."""
+    (default x's).  Rows in no group are not written.  No graph is recorded."""
     if w._index != _current_device():
         with _torch.cuda.device(w._index):
             return mx4_gemv(x, w, offsets, alpha, out_dtype, out, stream)
@@ -689,7 +689,8 @@ def mx4_gated_gemv(x, w: Mx4, offsets=None, activation: str = "silu", alpha: flo
                    stream=None):
     """act(g) * u for a few rows of 16-bit x (ozk_mx4_gated_gemv): w holds 2 H
     rows per group, the gate's first, g = alpha * x_t @ w_g(t)[:H]^T and u the
-    same with w_g(t)[H:]; activation "silu", "gelu" or "gelu_tanh"; [T, H]."""
+    same with w_g(t)[H:]; activation "silu", "gelu" or "gelu_tanh"; [T, H].
+    Otherwise as mx4_gemv."""
     if w._index != _current_device():
         with _torch.cuda.device(w._index):
             return mx4_gated_gemv(x, w, offsets, activation, alpha, out_dtype, out, stream)

@@ -336,3 +336,89 @@ def test_the_activation_itself(act):
         value = wide(g) * tail
     assert np.all(np.abs(wide(slopes[1, :, 0]) - value) <= ref.off(wide(g), act) * np.abs(value) + 2.0 ** -140)
     assert np.all(np.abs(wide(slopes[0, :, 0]) - slope) <= 64 * 2.0 ** -23 * 8)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_operands_in_padded_buffers(dtype):
+    """Rows of 60 columns in buffers of 72, groups apart: the same bits as tight ones of 64 with zeros, gradients too."""
+    x, w, offsets, _ = setup([33, 0, 100], 40, 60, dtype)
+    T = x.shape[0]
+    xs, ws = torch.full((T, 72), 9.0, dtype=dtype, device="cuda"), torch.full((3, 85, 72), 9.0, dtype=dtype, device="cuda")
+    xs[:, :60], ws[:, :80, :60] = x, w
+    xz, wz = torch.zeros(T, 64, dtype=dtype, device="cuda"), torch.zeros(3, 80, 64, dtype=dtype, device="cuda")
+    xz[:, :60], wz[..., :60] = x, w
+    dh = normal(T, 40, seed=3, dtype=dtype)
+    results = []
+    for a, b in ((xs[:, :60], ws[:, :80, :60]), (xz, wz)):
+        a, b = a.detach().requires_grad_(), b.detach().requires_grad_()
+        h = ozk.grouped_gated_gemm(a, b, offsets, activation="gelu")
+        dx, dw = torch.autograd.grad(h, (a, b), dh)
+        results.append((h.detach(), dx[:, :60], dw[..., :60]))
+    for got, want in zip(*results):
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("how", ["expanded", "transposed", "double"])
+def test_gradients_that_come_in_other_forms(how):
+    x, w, offsets, _ = setup([20, 13], 24, 40, torch.bfloat16)
+    x.requires_grad_(), w.requires_grad_()
+    if how == "expanded":
+        dh = torch.ones((), dtype=x.dtype, device="cuda").expand(33, 24)
+    elif how == "transposed":
+        dh = normal(24, 33, seed=3, dtype=x.dtype).t()
+    else:
+        dh = normal(33, 24, seed=3, dtype=x.dtype)
+    h = ozk.grouped_gated_gemm(x, w, offsets)
+    want = torch.autograd.grad(h, (x, w), dh.contiguous(), retain_graph=True)
+    if how == "double":
+        got = torch.autograd.grad(h.double(), (x, w), dh.double())
+    else:
+        got = torch.autograd.grad(h, (x, w), dh)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_training_step_in_a_graph():
+    """Forward and backward through autograd, captured and replayed with other values.  (With an eager graph of the same
+    leaves alive autograd refuses the capture, whatever the function.)"""
+    x, w, offsets, _ = setup([50, 14], 72, 136, torch.bfloat16)
+    dh = normal(64, 72, seed=3, dtype=x.dtype)
+    x.requires_grad_(), w.requires_grad_()
+
+    def step():
+        h = ozk.grouped_gated_gemm(x, w, offsets)
+        return (h, *torch.autograd.grad(h, (x, w), dh))
+
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        step()
+    torch.cuda.current_stream().wait_stream(stream)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        outs = step()
+    with torch.no_grad():
+        dh.copy_(normal(64, 72, seed=4, dtype=x.dtype))
+        offsets.copy_(torch.tensor([0, 7, 64], dtype=torch.int32))
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(outs, step()):
+        assert torch.equal(a.detach(), b.detach())
+    assert ozk.ozk_stream_status() == 0
+
+
+def test_more_than_2_to_31_elements():
+    """Results, slopes and gradients past 2^31 elements, where the last rows are those of a call of their own."""
+    T, H, K = 270400, 8000, 8
+    x = normal(T, K, seed=1, dtype=torch.bfloat16)
+    w = normal(1, 2 * H, K, seed=2, dtype=torch.bfloat16)
+    last = slice(T - 40, T)
+    slopes = torch.empty(2, T, H, device="cuda")
+    h = ozk.grouped_gated_gemm(x, w, torch.tensor([0, T], dtype=torch.int32, device="cuda"), slopes=slopes)
+    few = torch.empty(2, 40, H, device="cuda")
+    want = ozk.grouped_gated_gemm(x[last].clone(), w, torch.tensor([0, 40], dtype=torch.int32, device="cuda"), slopes=few)
+    assert torch.equal(h[last], want) and torch.equal(slopes[:, last], few)
+    dpre = ozk.gated_grad(h, slopes)
+    assert torch.equal(dpre[last], ozk.gated_grad(want, few))
+    assert ozk.ozk_stream_status() == 0

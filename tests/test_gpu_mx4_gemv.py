@@ -249,3 +249,26 @@ def test_refusals():
     with pytest.raises(TypeError):
         ozk.mx4_gemv(x, q, out_dtype=torch.int32)
     ozk.mx4_gemv(x, grouped, offsets)
+
+
+def test_more_than_2_to_31_elements():
+    """The last rows of a result past 2^31 elements are those of a call of their own."""
+    T, N, K = 270400, 8000, 64
+    q, _ = weights(N, K, "nvfp4", 1, seed=1)
+    x = normal(T, K, seed=2, dtype=torch.bfloat16)
+    y = ozk.mx4_gemv(x, q)
+    assert torch.equal(y[-48:], ozk.mx4_gemv(x[-48:].clone(), q))
+    assert ozk.ozk_stream_status() == 0
+
+
+def test_calls_on_two_streams_at_once():
+    q, _ = weights(3000, 2000, "mxfp4", 1, seed=3)
+    xs = [normal(t, 2000, seed=t, dtype=torch.bfloat16) for t in (1, 2, 5, 12)]
+    want = [ozk.mx4_gemv(x, q) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [[ozk.mx4_gemv(x, q, stream=s) for x, s in zip(xs, streams)] for _ in range(10)]
+    torch.cuda.synchronize()
+    for row in got:
+        for a, b in zip(row, want):
+            assert torch.equal(a, b)
