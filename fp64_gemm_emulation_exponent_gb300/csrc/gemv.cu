@@ -253,7 +253,7 @@ __device__ __forceinline__ float pow2f(int e) {  // 2^e, -126 <= e <= 127
 }
 // v 2^e for e beyond the exponents of one factor.
 __device__ __forceinline__ float scaled(float v, int e) {
-  const int half = e / 2;
+  const int half = e >> 1;
   return v * pow2f(half) * pow2f(e - half);
 }
 // ---- bf16 pairs as fp16 pairs
@@ -464,21 +464,23 @@ __global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const
   // This block's output columns: tile i has kOut of them, 32 from the next
   // tile's, so that the scale words of all tiles lie side by side.
   constexpr int kOut = GATED ? 8 : 16, kSub = 32 / kOut;
-  const int n0 = static_cast<int>(blockIdx.x) / kSub * (32 * R) + static_cast<int>(blockIdx.x) % kSub * kOut;
-  if (n0 >= p.N) return;
-  auto w_row = [&](int r) {  // of row r of the tiles
-    const int n = n0 + r / 16 * 32 + (GATED ? r & 7 : r & 15);
-    return GATED && (r & 8) ? p.N + n : n;
+  const uint32_t N = static_cast<uint32_t>(p.N), n0 = blockIdx.x / kSub * (32 * R) + blockIdx.x % kSub * kOut;
+  if (n0 >= N) return;
+  auto w_row = [&](uint32_t r) {  // of row r of the tiles
+    const uint32_t n = n0 + r / 16 * 32 + (GATED ? r & 7 : r & 15);
+    return GATED && (r & 8) ? N + n : n;
   };
-  auto in_range = [&](int r) { return n0 + r / 16 * 32 + (GATED ? r & 7 : r & 15) < p.N; };
+  auto in_range = [&](uint32_t r) { return n0 + r / 16 * 32 + (GATED ? r & 7 : r & 15) < N; };
+  const uint32_t pitch = static_cast<uint32_t>(p.kpad) / 2;  // bytes of a row of codes
 
   // Every warp's first chunk is on its way to L2 while the kernel before still
   // runs: a hint that reads nothing, so what that kernel writes is not missed
   // (1 x 8192 x 4096 NVFP4 7.8 us without, 6.9 so, 7.4 with two chunks).
-  if (!p.offsets && warp * S::ROW < p.kpad / 2) {
-    for (int r = lane; r < 16 * R; r += 32)
+  if (!p.offsets && warp * S::ROW < static_cast<int>(pitch)) {
+#pragma unroll
+    for (uint32_t r = lane; r < 16 * R; r += 32)
       if (in_range(r))
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.codes + static_cast<int64_t>(w_row(r)) * (p.kpad / 2) + warp * S::ROW));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.codes + static_cast<uint64_t>(w_row(r)) * pitch + warp * S::ROW));
   }
   grid_dependency_sync();
 
@@ -492,9 +494,13 @@ __global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const
     if (rows == 0) return;
   }
 
-  const int64_t group_row = static_cast<int64_t>(e) * p.w_rows;
-  const uint8_t* codes = p.codes + group_row * (p.kpad / 2);
-  const uint8_t* scales = p.scales + (group_row / 128 + e) * p.words * 512;
+  const uint8_t *codes = p.codes, *scales = p.scales;
+  const uint32_t block_bytes = static_cast<uint32_t>(p.words) * 512;  // of the scales of 128 rows
+  if (e) {
+    const uint32_t group_row = static_cast<uint32_t>(e) * static_cast<uint32_t>(p.w_rows);  // below 2^30
+    codes += static_cast<uint64_t>(group_row) * pitch;
+    scales += static_cast<uint64_t>(group_row / 128 + e) * block_bytes;
+  }
 
   // A warp's ring of codes and scale words, and one or two chunks' rows of x (FEW:
   // as fp16; else as they came).  16-byte pieces are swapped within a row so that
@@ -509,25 +515,24 @@ __global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const
   // written.
   constexpr int kCopies = R * 16 * S::PIECES / 32, kStep = 32 / S::PIECES;
   const int r0 = lane / S::PIECES;
-  const uint32_t pitch = static_cast<uint32_t>(p.kpad / 2);
-  const uint8_t* src = codes + static_cast<int64_t>(n0 + r0) * pitch + lane % S::PIECES * 16;
-  const int64_t up = GATED ? static_cast<int64_t>(p.N) * pitch : 0;  // from a row to that of the other projection
-  const bool all_rows = n0 + 32 * (R - 1) + kOut <= p.N;
+  const uint8_t* src = codes + static_cast<uint64_t>(n0 + r0) * pitch + lane % S::PIECES * 16;
+  const uint64_t up = GATED ? static_cast<uint64_t>(N) * pitch : 0;  // from a row to that of the other projection
+  const bool all_rows = n0 + 32 * (R - 1) + kOut <= N;
   const uint32_t dst = code_piece<S>(r0, lane % S::PIECES);
   // Scale words (lane + 32 j) of a chunk, each of all tiles: [word][row of a tile][tile]
   constexpr int kScaleCopies = (16 * S::WORDS + 31) / 32;
-  auto scale_at = [&](int row) { return static_cast<int64_t>(row / 128) * p.words * 512 + row % 32 * 16 + row / 32 % 4 * 4; };
-  const uint8_t* ssrc[kScaleCopies];
-#pragma unroll
-  for (int j = 0; j < kScaleCopies; ++j) ssrc[j] = scales + scale_at(w_row(lane & 15)) + (lane / 16 + 2 * j) * 512;
+  auto scale_at = [&](uint32_t row) {
+    return scales + static_cast<uint64_t>(row / 128) * block_bytes + (row % 32 * 16 + row / 32 % 4 * 4 + lane / 16 * 512);
+  };
+  const uint8_t* ssrc = scale_at(w_row(lane & 15));
 
   for (int t0 = 0; t0 < rows; t0 += S::TOKENS) {
     const int tokens = min(S::TOKENS, rows - t0);
     const uint16_t* x = p.x + (static_cast<int64_t>(row0) + t0) * p.ldx;
     auto fetch = [&](int chunk, int slot) {
       const uint32_t at = ring + static_cast<uint32_t>(slot * S::STAGE);
-      const uint8_t* from = src + static_cast<int64_t>(chunk) * S::ROW;
-      const int64_t sfrom = static_cast<int64_t>(chunk) * (S::WORDS * 512);
+      const uint8_t* from = src + static_cast<uint32_t>(chunk) * S::ROW;
+      const uint32_t sfrom = static_cast<uint32_t>(chunk) * (S::WORDS * 512);  // below the 2^25 bytes of a row block
       auto code = [&](int j) {
         // rows 8 apart (where FEW, 4: pieces differ by one bit) have their pieces in the same places
         const uint32_t to = S::FEW && (j & 1) ? dst ^ 64u : dst;
@@ -538,12 +543,12 @@ __global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const
       auto scale = [&](int j) {
         const uint32_t to = at + S::CODES + (lane + 32 * j) * (4 * R);
         if (p.side) {
-          copy<4 * R>(to, ssrc[j] + sfrom);
+          copy<4 * R>(to, ssrc + sfrom + j * 1024);
         } else {
 #pragma unroll 1
           for (int i = 0; i < R; ++i)
             if (in_range(16 * i + (lane & 15)))
-              copy<4>(to + 4 * i, scales + scale_at(w_row(16 * i + (lane & 15))) + (lane / 16 + 2 * j) * 512 + sfrom);
+              copy<4>(to + 4 * i, scale_at(w_row(16 * i + (lane & 15))) + sfrom + j * 1024);
         }
       };
       if (all_rows && (chunk + 1) * S::CHUNK <= p.kpad) {
@@ -744,7 +749,7 @@ __global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const
       // a value of lane l = 4 row + token / 2: c = token % 2, + 2 for the second eight rows of the tile
       const int col = o % kOut, t = o / kOut % kRows, n = o / (kOut * kRows) % TILES, i = o / (kOut * kRows * TILES);
       const int l = (col & 7) * 4 + (t >> 1), c = t & 1;
-      const int token = 8 * n + t, out = n0 + 32 * i + col;
+      const int token = 8 * n + t, out = static_cast<int>(n0) + 32 * i + col;
       if (token >= tokens || out >= p.N) continue;
       float v = p.alpha * sum(i, n, GATED ? c : c + 2 * (col >> 3), l);
       if (GATED) v = act_value(v, p.act) * (p.alpha * sum(i, n, c + 2, l));
