@@ -639,9 +639,9 @@ def _activation(name):
         raise ValueError(f"unknown activation {name!r} (silu, gelu, gelu_tanh)") from None
 
 
-def _few_rows(name, x, w, offsets, per, act, alpha, out_dtype, out, stream):
-    """mx4_gemv and mx4_gated_gemv: `per` rows of w to an output column, act the arguments of the gated one."""
-    index, groups, at = w._index, w.groups, None
+def _few_rows(x, w, offsets, act, alpha, out_dtype, out, stream):
+    """mx4_gemv and, where act is given, mx4_gated_gemv, which has two rows of w to an output column."""
+    index, groups, at, per = w._index, w.groups, None, 1 if act is None else 2
     if x.get_device() != index:
         raise ValueError(f"operands on {x.device} and cuda:{index}")
     if w.offsets is not None:
@@ -652,25 +652,39 @@ def _few_rows(name, x, w, offsets, per, act, alpha, out_dtype, out, stream):
         at = offsets.data_ptr()
     elif groups != 1:
         raise ValueError(f"offsets are needed for weights of {groups} groups")
-    (T, K, ldx), N = _rows(x), w.rows // (groups * per)
-    if K != w.K or N * per * groups != w.rows:
-        raise ValueError(f"x is {tuple(x.shape)}, the weights {w.rows} x {w.K} in {groups} groups")
-    dtype = x.dtype
+    if x.is_contiguous() and len(x.shape) == 2:
+        T, K = x.shape
+        ldx = K or 1
+    else:
+        T, K, ldx = _rows(x)
+    rows, dtype = w.rows, x.dtype
+    N = rows // (groups * per)
+    if K != w.K or N * per * groups != rows:
+        raise ValueError(f"x is {tuple(x.shape)}, the weights {rows} x {w.K} in {groups} groups")
+    kind_x = _DTYPES.get(dtype)
+    if kind_x is None:
+        _dtype(dtype)  # raises
     if out is None:
+        ld, kind = N or 1, kind_x
         if out_dtype is None:
             out_dtype = dtype
-        ld, kind = N or 1, _dtype(out_dtype)
+        elif out_dtype is not dtype:
+            kind = _dtype(out_dtype)
         if stream is None:
             out = _torch.empty((T, N), dtype=out_dtype, device=w.device)
         else:
             out = _empty((T, N), out_dtype, w.device, stream)
     else:
         out, ld, kind = _result(out, T, N, out_dtype, w.device, stream)
-    rc = getattr(_lib, name)(T, N, K, groups, at, x.data_ptr(), ldx, _dtype(dtype), w._codes, w._scales, _FORMATS[w.fmt],
-                             alpha, *act, out.data_ptr(), ld, kind,
-                             _current_stream(index) if stream is None else _stream_at(index, stream))
+    handle = _current_stream(index) if stream is None else _stream_at(index, stream)
+    if act is None:
+        rc = _lib.ozk_mx4_gemv(T, N, K, groups, at, x.data_ptr(), ldx, kind_x, w._codes, w._scales, _FORMATS[w.fmt], alpha,
+                               out.data_ptr(), ld, kind, handle)
+    else:
+        rc = _lib.ozk_mx4_gated_gemv(T, N, K, groups, at, x.data_ptr(), ldx, kind_x, w._codes, w._scales, _FORMATS[w.fmt],
+                                     alpha, act, out.data_ptr(), ld, kind, handle)
     if rc:
-        raise OzkError(name, rc)
+        raise OzkError("ozk_mx4_gemv" if act is None else "ozk_mx4_gated_gemv", rc)
     return out
 
 
@@ -682,7 +696,7 @@ def mx4_gemv(x, w: Mx4, offsets=None, alpha: float = 1.0, out_dtype=None, out=No
     if w._index != _current_device():
         with _torch.cuda.device(w._index):
             return mx4_gemv(x, w, offsets, alpha, out_dtype, out, stream)
-    return _few_rows("ozk_mx4_gemv", x, w, offsets, 1, (), alpha, out_dtype, out, stream)
+    return _few_rows(x, w, offsets, None, alpha, out_dtype, out, stream)
 
 
 def mx4_gated_gemv(x, w: Mx4, offsets=None, activation: str = "silu", alpha: float = 1.0, out_dtype=None, out=None,
@@ -694,7 +708,7 @@ def mx4_gated_gemv(x, w: Mx4, offsets=None, activation: str = "silu", alpha: flo
     if w._index != _current_device():
         with _torch.cuda.device(w._index):
             return mx4_gated_gemv(x, w, offsets, activation, alpha, out_dtype, out, stream)
-    return _few_rows("ozk_mx4_gated_gemv", x, w, offsets, 2, (_activation(activation),), alpha, out_dtype, out, stream)
+    return _few_rows(x, w, offsets, _activation(activation), alpha, out_dtype, out, stream)
 
 
 def _grouped(first, second, offsets, groups):
