@@ -349,12 +349,14 @@ int ozk_grouped_gated_gemm_grad(int64_t T, int64_t N, int64_t K, int groups, con
     if (overlap(d, h) || overlap(d, s) || overlap(d, span(X, T, K, ldx, 2)) ||
         overlap(d, span(W, 2 * N, K, ldw, 2, groups, w_stride)))
       return OZK_ERR_INVALID_ARG;
-    if (dX && K > 0) {
-      const Span x = span(dX, T, K, lddx, 2);
-      if (overlap(x, h) || overlap(x, s)) return OZK_ERR_INVALID_ARG;  // cleared while they are read
-      if ((rc = check_weights(W, 2 * N, K, ldw, groups, w_stride))) return rc;
-    }
+    if (dX && K > 0 && (rc = check_weights(W, 2 * N, K, ldw, groups, w_stride))) return rc;
     if (dW && K > 0 && (rc = check_operand(X, K, ldx))) return rc;
+    // all three results are written before the last operand has been read
+    const Span in[5] = {h, s, span(X, T, K, ldx, 2), span(W, 2 * N, K, ldw, 2, groups, w_stride), d};
+    const Span dx = span(dX, dX ? T : 0, K, lddx, 2), dw = span(dW, dW ? 2 * N : 0, K, lddw, 2, groups, dw_stride);
+    for (const Span& i : in)
+      if (overlap(dx, i) || overlap(dw, i)) return OZK_ERR_INVALID_ARG;
+    if (overlap(dx, dw)) return OZK_ERR_INVALID_ARG;
   }
   if (dX && T > 0 && K > 0 && (lddx < K || reinterpret_cast<uintptr_t>(dX) % 2 != 0)) return OZK_ERR_INVALID_ARG;
   if (dW && N > 0 && K > 0 && (lddw < K || (groups > 1 && dw_stride < (2 * N - 1) * lddw + K))) return OZK_ERR_INVALID_ARG;

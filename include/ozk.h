@@ -509,7 +509,8 @@ int ozk_gated_grad(int64_t T, int64_t N, int groups, const int32_t* offsets, con
 /* The whole backward pass in stream order: ozk_gated_grad, whose result is left
  * in dpre (its requirements those of an operand of ozk_grouped_gemm_dx), then
  * the gradients of X (T x K; zeros in rows of no group) and of W (2 N x K per
- * group), each only where not NULL; both of dtype. */
+ * group), each only where not NULL; both of dtype.  What is written overlaps
+ * nothing. */
 int ozk_grouped_gated_gemm_grad(int64_t T, int64_t N, int64_t K, int groups, const int32_t* offsets, const void* dH,
                                 int64_t lddh, const float* slopes, int64_t lds, int64_t slope_stride, const void* X,
                                 int64_t ldx, const void* W, int64_t ldw, int64_t w_stride, int dtype, void* dpre,

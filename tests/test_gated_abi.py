@@ -69,7 +69,8 @@ def test_backward_refusals():
     for bad in (dict(T=-1), dict(N=-1), dict(K=-1), dict(groups=0), dict(off=None), dict(dh=None), dict(s=None), dict(p=None),
                 dict(lddh=7), dict(lds=7), dict(plane=31), dict(ldp=15), dict(x=None), dict(w=None), dict(ldx=56), dict(ldw=56),
                 dict(lddx=63), dict(lddw=63), dict(dwstride=15 * 64), dict(dx=DX + 1), dict(p=DH), dict(p=S), dict(p=X), dict(p=W),
-                dict(dx=DH), dict(dx=S)):
+                dict(dx=DH), dict(dx=S), dict(dx=X), dict(dx=W), dict(dx=P), dict(dw=DH), dict(dw=S), dict(dw=X), dict(dw=W),
+                dict(dw=P), dict(dw=DX)):
         assert backward(**bad) == INVALID, bad
     for bad in (dict(dtype=2), dict(T=1 << 31), dict(N=(1 << 21) + 1), dict(K=(1 << 22) + 1), dict(groups=1025), dict(ldx=68),
                 dict(ldw=68), dict(ldp=20), dict(p=P + 8), dict(x=X + 8), dict(w=W + 2)):
