@@ -55,6 +55,7 @@
 #include <cstring>
 #include <map>
 #include <mutex>
+#include <type_traits>
 
 #include "activation.cuh"
 #include "lowp.h"
@@ -136,14 +137,21 @@ struct ProductParams {
   int64_t ldo, out_group;
   float alpha;
   bool vec;        // 16-byte stores: a 16-bit output whose rows are 16-byte aligned
-  float* slopes;   // gated: the result's two slopes, [2][T][M], or null
-  int64_t lds, slope_plane;
-  bool vec_slopes;
-  int act;
   uint64_t timeout_ns;  // limit of a pipeline wait: what a whole tile's stages may take, and 2 s
   int withhold_kb, withhold_cta;  // the stage that test runs withhold (of that CTA's first tile), or -1
   uint32_t idesc;  // types, majorness, M; N is filled in per tile
 };
+
+// Apart from the others': in every product's parameters they cost each kernel
+// up to 8 registers, and one row of 8192 x 4096 NVFP4 0.5 us (7.3 -> 7.8).
+struct GatedParams : ProductParams {
+  float* slopes;  // the result's two slopes, [2][T][M], or null
+  int64_t lds, slope_plane;
+  bool vec_slopes;
+  int act;
+};
+template <ProductOp OP>
+using Params = std::conditional_t<OP == kGated, GatedParams, ProductParams>;
 
 // One lane of a converged warp.  The compiler then knows that a single thread
 // runs the branch, and takes tcgen05's warp-uniform operands from it directly.
@@ -693,7 +701,7 @@ template <ProductOp OP, int FMT, int BN, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmR,
                    const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmSR,
-                   const __grid_constant__ CUtensorMap tmO, const ProductParams p) {
+                   const __grid_constant__ CUtensorMap tmO, const Params<OP> p) {
   using C = Config<OP, FMT, BN, PAIR>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -1108,7 +1116,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // the stores in flight finish before the CTA's shared memory goes
-    if ((p.vec || p.vec_slopes) && quad == 0) {
+    bool stores = p.vec;
+    if constexpr (OP == kGated) stores |= p.vec_slopes;
+    if (stores && quad == 0) {
       if (elect_one()) bulk_wait_all();
       __syncwarp();
     }
@@ -1200,7 +1210,7 @@ thread_local Withhold g_withhold = {};
 template <ProductOp OP, int FMT, int BN, bool PAIR>
 cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
   using C = Config<OP, FMT, BN, PAIR>;
-  ProductParams p = {};
+  Params<OP> p = {};
   p.T = static_cast<int>(q.T);
   p.M = static_cast<int>(q.M);
   p.N = static_cast<int>(q.N);
@@ -1214,7 +1224,7 @@ cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
   p.alpha = q.K ? q.alpha : 1.0f;  // a sum of no terms is zero, whatever alpha
   p.vec = q.out_type != OZK_F32 && reinterpret_cast<uintptr_t>(q.out) % 16 == 0 && q.ldo % 8 == 0 &&
           (OP != kGradWeights || q.groups == 1 || q.out_group % 8 == 0);
-  if (C::GATED) {
+  if constexpr (C::GATED) {
     p.act = q.act;
     p.slopes = q.slopes;
     p.lds = q.lds;
@@ -1296,10 +1306,11 @@ cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
                   dims, strides, box, true))
       return cudaErrorInvalidValue;
   }
-  if (p.vec_slopes) {
+  if constexpr (C::GATED) {
     const int64_t dims[3] = {q.M, q.T, 2}, strides[2] = {4 * q.lds, 4 * q.slope_plane};
     const uint32_t box[3] = {32, 32, 1};
-    if (!make_map(&tmSW, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, q.slopes, dims, strides, box, true)) return cudaErrorInvalidValue;
+    if (p.vec_slopes && !make_map(&tmSW, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, q.slopes, dims, strides, box, true))
+      return cudaErrorInvalidValue;
   }
   auto kernel = product_kernel<OP, FMT, BN, PAIR>;
   const size_t table = (static_cast<size_t>(q.groups) + 1) * sizeof(Group);
