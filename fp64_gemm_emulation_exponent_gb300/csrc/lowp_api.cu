@@ -42,10 +42,12 @@ Mx4Matrix matrix(int64_t rows, int64_t K, int format, const int32_t* offsets, in
   return {rows, K, format, groups, offsets, const_cast<uint8_t*>(codes), const_cast<uint8_t*>(scales)};
 }
 
+bool countable(int64_t tiles_m, int64_t tiles_n) { return tiles_m == 0 || tiles_n <= kMaxTiles / tiles_m; }
+int64_t tiles_of(int64_t n) { return (n + 127) / 128; }
+
 int run(const Product& q, cudaStream_t stream, int sms) {
-  const int64_t tiles_m = ((q.op == kGated ? 2 * q.M : q.M) + 127) / 128;
-  const int64_t tiles_n = q.op == kGradWeights ? ((q.N + 127) / 128) * q.groups : q.T / 128 + q.groups;
-  if (tiles_m > 0 && tiles_n > kMaxTiles / tiles_m) return OZK_ERR_UNSUPPORTED;
+  const int64_t tiles_n = q.op == kGradWeights ? tiles_of(q.N) * q.groups : q.T / 128 + q.groups;
+  if (!countable(tiles_of(q.op == kGated ? 2 * q.M : q.M), tiles_n)) return OZK_ERR_UNSUPPORTED;
   try {  // the launcher's tables may allocate; nothing is thrown across the C boundary
     return launch_product(q, sms, stream) == cudaSuccess ? OZK_OK : OZK_ERR_CUDA;
   } catch (...) {
@@ -358,8 +360,13 @@ int ozk_grouped_gated_gemm_grad(int64_t T, int64_t N, int64_t K, int groups, con
       if (overlap(dx, i) || overlap(dw, i)) return OZK_ERR_INVALID_ARG;
     if (overlap(dx, dw)) return OZK_ERR_INVALID_ARG;
   }
+  // whatever the calls below would refuse is refused here, before the first of them has written
   if (dX && T > 0 && K > 0 && (lddx < K || reinterpret_cast<uintptr_t>(dX) % 2 != 0)) return OZK_ERR_INVALID_ARG;
-  if (dW && N > 0 && K > 0 && (lddw < K || (groups > 1 && dw_stride < (2 * N - 1) * lddw + K))) return OZK_ERR_INVALID_ARG;
+  if (dW && N > 0 && K > 0 &&
+      (lddw < K || reinterpret_cast<uintptr_t>(dW) % 2 != 0 || (groups > 1 && dw_stride < (2 * N - 1) * lddw + K)))
+    return OZK_ERR_INVALID_ARG;
+  if (dX && T > 0 && !countable(tiles_of(K), T / 128 + groups)) return OZK_ERR_UNSUPPORTED;
+  if (dW && !countable(tiles_of(K), tiles_of(2 * N) * groups)) return OZK_ERR_UNSUPPORTED;
   int sms = 0;
   if ((rc = current_device_supported(&sms))) return rc;
   if (T > 0 && (N > 0 || (dX && K > 0))) {
