@@ -25,7 +25,10 @@ Span span(const void* p, int64_t rows, int64_t cols, int64_t ld, size_t esize, i
   if (rows <= 0 || cols <= 0 || groups <= 0) return {a, a};
   return {a, a + esize * static_cast<size_t>((groups - 1) * group + (rows - 1) * ld + cols)};
 }
-bool overlap(const Span& x, const Span& y) { return x.lo < y.hi && y.lo < x.hi; }
+// Memory of no bytes overlaps nothing, whatever its address.
+bool overlap(const Span& x, const Span& y) {
+  return x.lo < x.hi && y.lo < y.hi && x.lo < y.hi && y.lo < x.hi;
+}
 
 bool known_format(int f) { return f == OZK_NVFP4 || f == OZK_MXFP4; }
 bool known_dtype(int t) { return t >= OZK_BF16 && t <= OZK_F64; }
@@ -347,18 +350,18 @@ int ozk_grouped_gated_gemm_grad(int64_t T, int64_t N, int64_t K, int groups, con
   if (T > 0 && N > 0) {
     if (!dH || lddh < N || reinterpret_cast<uintptr_t>(dH) % 2 != 0) return OZK_ERR_INVALID_ARG;
     if ((rc = check_slopes(slopes, T, N, lds, slope_stride)) || (rc = check_operand(dpre, 2 * N, ldp))) return rc;
-    const Span d = span(dpre, T, 2 * N, ldp, 2), h = span(dH, T, N, lddh, 2), s = span(slopes, T, N, lds, 4, 2, slope_stride);
-    if (overlap(d, h) || overlap(d, s) || overlap(d, span(X, T, K, ldx, 2)) ||
-        overlap(d, span(W, 2 * N, K, ldw, 2, groups, w_stride)))
-      return OZK_ERR_INVALID_ARG;
     if (dX && K > 0 && (rc = check_weights(W, 2 * N, K, ldw, groups, w_stride))) return rc;
     if (dW && K > 0 && (rc = check_operand(X, K, ldx))) return rc;
-    // all three results are written before the last operand has been read
-    const Span in[5] = {h, s, span(X, T, K, ldx, 2), span(W, 2 * N, K, ldw, 2, groups, w_stride), d};
-    const Span dx = span(dX, dX ? T : 0, K, lddx, 2), dw = span(dW, dW ? 2 * N : 0, K, lddw, 2, groups, dw_stride);
-    for (const Span& i : in)
-      if (overlap(dx, i) || overlap(dw, i)) return OZK_ERR_INVALID_ARG;
-    if (overlap(dx, dw)) return OZK_ERR_INVALID_ARG;
+  }
+  // all three results are written before the last operand has been read; dX without columns and dW without rows too
+  const Span out[3] = {span(dpre, T, 2 * N, ldp, 2), span(dX, dX ? T : 0, K, lddx, 2),
+                       span(dW, dW ? 2 * N : 0, K, lddw, 2, groups, dw_stride)};
+  const Span in[4] = {span(dH, T, N, lddh, 2), span(slopes, T, N, lds, 4, 2, slope_stride), span(X, T, K, ldx, 2),
+                      span(W, 2 * N, K, ldw, 2, groups, w_stride)};
+  for (int i = 0; i < 3; ++i) {
+    for (const Span& s : in)
+      if (overlap(out[i], s)) return OZK_ERR_INVALID_ARG;
+    if (overlap(out[i], out[(i + 1) % 3])) return OZK_ERR_INVALID_ARG;
   }
   // whatever the calls below would refuse is refused here, before the first of them has written
   if (dX && T > 0 && K > 0 && (lddx < K || reinterpret_cast<uintptr_t>(dX) % 2 != 0)) return OZK_ERR_INVALID_ARG;

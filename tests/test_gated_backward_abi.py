@@ -32,3 +32,15 @@ def test_more_tiles_than_the_products_count():
     assert backward(**many, dw=None) == UNSUPPORTED
     assert backward(T=4, N=1 << 18, K=1 << 16, groups=1024) == UNSUPPORTED  # dW: 2^12 by 2^10 by 2^9
     assert backward(T=4, N=1 << 18, K=1 << 16, groups=1024, dx=None) == UNSUPPORTED
+
+
+def test_results_over_operands_of_empty_products():
+    """Without columns dX is cleared all the same, and without rows dW: neither may lie on what is read elsewhere."""
+    for bad in (dict(N=0, dx=X), dict(N=0, dx=X + 64), dict(T=0, dw=W), dict(T=0, dw=W + 2)):
+        assert backward(**bad) == INVALID, bad
+
+
+def test_empty_operands_lie_over_nothing():
+    """Memory of no bytes may have any address, one inside a result too: no refusal (the call ends at the device)."""
+    for fine in (dict(T=0, x=DW + 64, dx=DW + 64), dict(N=0, dw=DX + 64, w=DX + 64, p=DX + 64), dict(K=0, x=P + 2, w=P + 4)):
+        assert backward(**fine) not in (INVALID, UNSUPPORTED), fine
