@@ -13,7 +13,13 @@
 namespace ozk {
 namespace {
 
-__device__ __forceinline__ float act_logistic(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+// From e^-|z|, which never leaves fp32's range on the large side: 1 / (1 + e^-z)
+// is 0 from z = -87.3 on, where __fdividef's divisor passes 2^126, though the
+// function is 2^-126 there and act(g) u need not be small.
+__device__ __forceinline__ float act_logistic(float z) {
+  const float t = __expf(-fabsf(z)), r = __fdividef(1.0f, 1.0f + t);
+  return z < 0.0f ? t * r : r;
+}
 
 constexpr float kGeluA = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f * kGeluA;
