@@ -50,7 +50,16 @@ __device__ __forceinline__ float act_p(float g, int act) {
   const float tail = normal_tail(g);
   return g < 0.0f ? tail : 1.0f - tail;
 }
-__device__ __forceinline__ float act_value(float g, int act) { return g * act_p(g, act); }
+// act(g) within a few units of 2^-23, for results in fp32: silu 4, gelu 5.5,
+// gelu_tanh 4 + 2 |z|, where the forms above are off by up to 12 + 2.7 |z| with z
+// the exponential's argument.  An epilogue of a few rows takes few values, and the
+// functions in full cost it 0.1 us (1 x 2 x 8192 x 4096 NVFP4 10.7 -> 10.8).
+__device__ __forceinline__ float act_value(float g, int act) {
+  if (act == OZK_GELU) return g * normcdff(g);
+  const float z = act == OZK_SILU ? g : g * fmaf(kGeluB, g * g, kGeluA);
+  const float t = expf(-fabsf(z)), r = __frcp_rn(1.0f + t);
+  return g * (z < 0.0f ? t * r : r);
+}
 
 // The derivative g P'(g) + P(g), given P(g).
 __device__ __forceinline__ float act_slope(float g, float p, int act) {

@@ -1,5 +1,6 @@
 """The activations far to the left, where their distribution P is tiny: values
-that fp32 holds are not lost, whatever multiplies them.
+that fp32 holds are not lost, whatever multiplies them; and how exact they are
+in the products of a few rows.
 
 P = e^z / (1 + e^z) or a polynomial times e^(-g^2/2) is off by off(z) units of
 gated_reference, and by at most 3 of fp32's least steps 2^-149 where e^z is
@@ -58,3 +59,32 @@ def test_products_keep_the_tail(name, power):
     assert np.all(np.abs(got[1] - u * (p + q)) <= u * ((off + 6 * 2.0 ** -23) * (p + np.abs(q)) + 2.0 ** -139) + 2.0 ** -149)
     assert np.all(np.abs(got[2] - u * a) <= ref.rounded(u * bound, u * a, 2.0 ** -8, 2.0 ** -126 * 2.0 ** -8))
     assert ozk.ozk_stream_status() == 0
+
+
+# In units of 2^-23: expf is off by up to 2 steps, a rounding by half a unit.  silu: e^-|g|, 1 +, the quotient, times
+# e^-|g|, times g: 2 + 4 / 2.  gelu: normcdff, up to 5 steps, times g.  gelu_tanh: as silu, and z by 2 units of itself
+# (its two constants, g^2, the sum and the product, half a unit each, of terms of one sign).
+UNITS = {"silu": lambda z: 4.0, "gelu": lambda z: 5.5, "gelu_tanh": lambda z: 4.0 + 2 * np.abs(z)}
+
+
+@pytest.mark.parametrize("name", ref.ACTS)
+@pytest.mark.parametrize("rows", [2, 4000])
+def test_rows_with_4_bit_weights(name, rows):
+    """act(g) in fp32 at every bf16 value of g from the span's left end to 30 (two rows: eleven of them)."""
+    g = bf16_between(SPAN[name][0], 30.0)
+    g = g[g.abs() >= 2.0 ** -20]
+    if rows == 2:
+        g = g[:: g.numel() // 10]
+    w = torch.zeros(2, 64, device="cuda")
+    w[0, 0] = w[1, 1] = 1.0  # MXFP4 holds a one exactly
+    q = ozk.mx4_quantize(w, "mxfp4")
+    x = torch.zeros(g.numel(), 64, dtype=torch.bfloat16)
+    x[:, 0], x[:, 1] = g, 1.0
+    x = x.cuda()
+    got = torch.cat([ozk.mx4_gated_gemv(x[i: i + rows], q, activation=name, out_dtype=torch.float32)
+                     for i in range(0, g.numel(), rows)])
+    got, g = got.double().cpu().numpy().ravel(), g.double().numpy()
+    a = exact(g, name)[0]
+    z = C * (g + 0.044715 * g ** 3)
+    worst = np.max((np.abs(got - a) - 2.0 ** -140) / np.abs(a)) * 2.0 ** 23
+    assert np.all(np.abs(got - a) <= UNITS[name](z) * 2.0 ** -23 * np.abs(a) + 2.0 ** -140), worst
