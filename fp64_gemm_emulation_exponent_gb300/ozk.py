@@ -163,18 +163,19 @@ def ozk_workspace_size(M: int, N: int, K: int, n_moduli: int) -> int:
 
 # ---------------------------------------------------------------- torch helpers
 _DTYPES = {}
-_torch = _current_device = _current_stream = None
+_torch = _current_device = _current_stream = _forward_ad = None
 
 
 def _load_torch():
-    global _torch, _current_device, _current_stream
+    global _torch, _current_device, _current_stream, _forward_ad
     import torch
+    from torch.autograd import forward_ad
 
     _DTYPES.update({torch.bfloat16: OZK_BF16, torch.float16: OZK_F16, torch.float32: OZK_F32,
                     torch.float64: OZK_F64})
     lib()
     _current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-    _torch = torch
+    _torch, _forward_ad = torch, forward_ad
     return torch
 
 
@@ -581,6 +582,16 @@ def mx4_dequantize(q: Mx4, dtype=None, out=None, stream=None):
     return out
 
 
+def _no_tangents(name, *tensors):
+    """Refuses forward-mode tangents, which would be dropped (with gradients off too: no_grad is for reverse mode alone)."""
+    if _forward_ad is None or _forward_ad._current_level < 0:
+        return
+    for t in tensors:
+        if _forward_ad.unpack_dual(t)[1] is not None:
+            raise NotImplementedError(f"{name} has no forward-mode derivative, and an operand carries a tangent "
+                                      "(forward_ad.unpack_dual(x).primal is without it)")
+
+
 def _pair_of(a, b):
     if a.fmt != b.fmt or a.K != b.K:
         raise ValueError(f"operands differ: {a.fmt}, K = {a.K} and {b.fmt}, K = {b.K}")
@@ -641,6 +652,7 @@ def _activation(name):
 
 def _few_rows(x, w, offsets, act, alpha, out_dtype, out, stream):
     """mx4_gemv and, where act is given, mx4_gated_gemv, which has two rows of w to an output column."""
+    _no_tangents("a product with 4-bit weights", x)
     index, groups, at, per = w._index, w.groups, None, 1 if act is None else 2
     if x.get_device() != index:
         raise ValueError(f"operands on {x.device} and cuda:{index}")
@@ -692,7 +704,8 @@ def mx4_gemv(x, w: Mx4, offsets=None, alpha: float = 1.0, out_dtype=None, out=No
     """alpha * x_t @ w_g(t)^T for a few rows of 16-bit x, not quantised
     (ozk_mx4_gemv): x [T, K] bf16 or fp16, w a matrix of one group, or from a
     [groups, N, K] tensor with offsets for the rows of x; [T, N] of out_dtype
-    (default x's).  Rows in no group are not written.  No graph is recorded."""
+    (default x's).  Rows in no group are not written.  No graph is
+    recorded, and forward-mode tangents are refused."""
     if w._index != _current_device():
         with _torch.cuda.device(w._index):
             return mx4_gemv(x, w, offsets, alpha, out_dtype, out, stream)
@@ -735,13 +748,14 @@ def grouped_gemm(x, w, offsets, out_dtype=None, out=None, stream=None):
     Autograd records it where x or w asks for a gradient (grouped_gemm_dx and
     grouped_gemm_dw, each only where asked for; zeros for rows in no group; a
     float32 result's gradient is rounded to the operands' type), once: there is
-    no second derivative.  With out given, and in every other call here, no
-    graph is recorded."""
+    no second derivative, and forward-mode tangents are refused.  With out
+    given, and in every other call here, no graph is recorded."""
     groups, N, K, ldw, stride = _groups(w)
     _, kind, index = _grouped(x, w, offsets, groups)
     if index != _current_device():
         with _torch.cuda.device(index):
             return grouped_gemm(x, w, offsets, out_dtype, out, stream)
+    _no_tangents("grouped_gemm", x, w)
     if out is None and (x.requires_grad or w.requires_grad) and _torch.is_grad_enabled():
         with _torch.cuda.stream(stream):
             return (_GroupedGemm or _load_function()).apply(x, w, offsets, out_dtype)
@@ -879,17 +893,19 @@ def grouped_gated_gemm(x, w, offsets, activation: str = "silu", out=None, slopes
     h by.
 
     Autograd records it where x or w asks for a gradient
-    (grouped_gated_gemm_grad), once: there is no second derivative.  With out or
-    slopes given no graph is recorded.  Both passes can be captured into a CUDA
-    graph, together, and only while no result of an eager pass from the same
-    leaves is alive: autograd would take their gradients to that pass's stream,
-    which ends the capture with an error, whatever the function."""
+    (grouped_gated_gemm_grad), once: there is no second derivative, and
+    forward-mode tangents are refused.  With out or slopes given no graph is
+    recorded.  Both passes can be captured into a CUDA graph, together, and only
+    while no result of an eager pass from the same leaves is alive: autograd
+    would take their gradients to that pass's stream, which ends the capture with
+    an error, whatever the function."""
     groups, N, K, ldw, stride = _groups(w)
     _, kind, index = _grouped(x, w, offsets, groups)
     act = _activation(activation)
     if index != _current_device():
         with _torch.cuda.device(index):
             return grouped_gated_gemm(x, w, offsets, activation, out, slopes, stream)
+    _no_tangents("grouped_gated_gemm", x, w)
     T, k, ldx = _rows(x)
     if k != K or N % 2:
         raise ValueError(f"x is {tuple(x.shape)}, the weights {tuple(w.shape)}")
