@@ -652,6 +652,9 @@ def _activation(name):
 
 def _few_rows(x, w, offsets, act, alpha, out_dtype, out, stream):
     """mx4_gemv and, where act is given, mx4_gated_gemv, which has two rows of w to an output column."""
+    if x.requires_grad and out is None and _torch.is_grad_enabled():
+        raise NotImplementedError("products with 4-bit weights record no gradient, and x asks for one: "
+                                  "x.detach(), no_grad or out says that none is wanted")
     _no_tangents("a product with 4-bit weights", x)
     index, groups, at, per = w._index, w.groups, None, 1 if act is None else 2
     if x.get_device() != index:
@@ -705,7 +708,8 @@ def mx4_gemv(x, w: Mx4, offsets=None, alpha: float = 1.0, out_dtype=None, out=No
     (ozk_mx4_gemv): x [T, K] bf16 or fp16, w a matrix of one group, or from a
     [groups, N, K] tensor with offsets for the rows of x; [T, N] of out_dtype
     (default x's).  Rows in no group are not written.  No graph is
-    recorded, and forward-mode tangents are refused."""
+    recorded: where x asks for a gradient the call is refused, unless under
+    no_grad or with out given; so are forward-mode tangents."""
     if w._index != _current_device():
         with _torch.cuda.device(w._index):
             return mx4_gemv(x, w, offsets, alpha, out_dtype, out, stream)

@@ -1,11 +1,36 @@
-"""Calls that have no forward-mode derivative say so instead of dropping a
-tangent (the host side, with the stand-ins of test_operand_device)."""
+"""Calls that record no gradient, or no forward-mode tangent, say so instead of
+dropping it (the host side, with the stand-ins of test_operand_device)."""
 import pytest
 import torch
 from torch.autograd import forward_ad
 
 from fp64_gemm_emulation_exponent_gb300 import ozk
 from test_operand_device import FakeTensor, machine, matrix, offsets, tensor  # noqa: F401
+
+
+def asking(*shape):
+    t = tensor(*shape)
+    t.requires_grad = True
+    return t
+
+
+ROWS = {
+    "mx4_gemv": lambda x, **k: ozk.mx4_gemv(x, matrix(groups=2), offsets(), **k),
+    "mx4_gated_gemv": lambda x, **k: ozk.mx4_gated_gemv(x, matrix(), **k),
+}
+
+
+@pytest.mark.parametrize("name", ROWS)
+@pytest.mark.parametrize("device", [0, 1])
+def test_rows_that_ask_for_a_gradient(machine, name, device):  # noqa: F811
+    machine.fake.current = device  # the rows' own device, or another one
+    with pytest.raises(NotImplementedError, match="gradient"):
+        ROWS[name](asking(4, 64))
+    assert machine.calls == [] and machine.fake.allocated_on == []
+    ROWS[name](asking(4, 64), out=tensor(4, 8))  # into memory given
+    machine.fake.is_grad_enabled = lambda: False
+    ROWS[name](asking(4, 64))
+    assert [c[0] for c in machine.calls] == ["ozk_" + name] * 2
 
 
 CALLS = {
@@ -75,4 +100,13 @@ def test_on_the_gpu():
                 call(dual)
             assert torch.equal(call(x), want)
             assert torch.equal(call(forward_ad.unpack_dual(dual).primal), want)
+    asking = x.clone().requires_grad_()
+    for call, want in zip(calls[:2], wanted):
+        assert call(asking).requires_grad
+    for call, want in zip(calls[2:], wanted[2:]):
+        with pytest.raises(NotImplementedError):
+            call(asking)
+        with torch.no_grad():
+            assert torch.equal(call(asking), want)
+    assert torch.equal(ozk.mx4_gemv(asking, q, out=torch.empty_like(wanted[2])), wanted[2])
     assert ozk.ozk_stream_status() == 0
