@@ -448,13 +448,19 @@ typedef enum { OZK_SILU = 0, OZK_GELU = 1, OZK_GELU_TANH = 2 } ozk_activation;
 /* Y[t, j] = alpha * sum_k x_tk w_g(t),j,k for a few rows: X is T x K of dtype
  * OZK_BF16 or OZK_F16, as it is (not quantised), any alignment of its type; w
  * as in ozk_mx4_grouped_gemm.  offsets as there, or NULL for one group.  Any T
- * is taken; the weights are read once for every 2, 8 or 16 rows of a group, and
- * past some 8 rows (with many columns) to 16 quantised rows and
- * ozk_mx4_grouped_gemm are faster.  Y: T x
- * N of OZK_BF16, OZK_F16 or OZK_F32, ldy >= N, any alignment of its own type;
- * it must overlap nothing.  x is used exactly, whatever its range; sums are
- * formed in fp32 (with MXFP4 scales above 2^96 one may overflow where its
- * result would not).  K = 0 gives zeros. */
+ * is taken.  The weights are read once for every 2, 8 or 16 rows of a group:
+ * from 17 rows on (from 9 with 8192 rows of w or more), where x need not stay in
+ * 16 bits, quantising it (ozk_mx4_quantize) for ozk_mx4_gemm is faster, the
+ * quantisation included.  Y: T x N of OZK_BF16, OZK_F16 or OZK_F32, ldy >= N, any alignment of its own type;
+ * it must overlap nothing.  K = 0 gives zeros.
+ * x is used exactly, whatever its range; sums are formed in fp32.  bf16 rows
+ * whose non-zero elements lie more than 2^26 apart within 128 columns (256 for
+ * one or two rows) are multiplied once for every 27 binades: outputs of a gelu,
+ * with gates of a standard deviation of 2 to 4, take two to four times as long
+ * as normal ones.  No sum overflows on the way while the largest scale is at most
+ * 2^109 / K (NVFP4's always are).  At the other end a result is off by up to
+ * 2^-146, and with MXFP4 weights by up to K / 32 times 2^-158 of its row's largest
+ * element, beside the roundings of the sums. */
 int ozk_mx4_gemv(int64_t T, int64_t N, int64_t K, int groups, const int32_t* offsets, const void* X, int64_t ldx,
                  int dtype, const uint8_t* w_codes, const uint8_t* w_scales, int format, float alpha, void* Y,
                  int64_t ldy, int out_dtype, ozk_stream_t stream);
