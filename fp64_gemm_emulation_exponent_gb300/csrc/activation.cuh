@@ -27,7 +27,7 @@ constexpr float kGeluB = 0.044715f * kGeluA;
 // The normal distribution's tail beyond |g|, e^(-g^2/2) t p(t) with t = 1 / (1 +
 // 0.3 |g|): what the exponential leaves is smooth in t, and p, of degree 7, is
 // fitted to it for 0 <= |g| <= 14 by least squares at Chebyshev's points,
-// reweighted towards the largest relative error (1.5e-7; 5e-7 in fp32, the
+// reweighted towards the largest relative error (1.7e-7; 5e-7 in fp32, the
 // exponential aside).  With erfcf in its place the epilogue of a product with
 // gelu cost 3.5 us more on 1999 rows, 1032 -> 520, and 30 of 180 on 8192 rows,
 // 4096 -> 2048: its instructions slow the warps that issue copies and MMAs.

@@ -23,7 +23,13 @@
 // 2^10): exact as fp16 for every element from 2^-26 to 2^6 of that one.  Every
 // chunk is checked for it; where one does not fit, the sums are put away and
 // the scale starts again from that chunk, and elements that are too small even
-// so take part in further passes over the chunk, 27 binades at a time.
+// so take part in further passes over the chunk, 27 binades at a time.  Those
+// passes cost what they compute.  Rows that are gelu(g) u take no longer than
+// normal ones with g of a standard deviation of 1, but with 2 or 4 (gelu(-6) is
+// 2^-27, and a chunk has such) two to four times as long; us, normal / 2 / 4: 1 x
+// 8192 x 4096 6.8 / 13.1 / 21.4, 8 x 8192 x 8192 12.1 / 26.2 / 34.4, 16 x 8192 x
+// 8192 15.9 / 49.1 / 63.2.  After silu at most a half longer.  fp16 rows need
+// neither check nor passes: 5.7, 10.0 and 12.6.
 //
 // A block owns 16 R output rows of w (gated: 8 R of each projection) and all
 // of K; its warps take the chunks of 128 or 256 columns in turn, each through a
@@ -32,17 +38,19 @@
 // a fixed order.
 //
 // Measured on a GB300 (us in replayed graphs, weights from HBM; floor at 6.79
-// TB/s): 8192 x 4096 NVFP4, 1 row 6.8, 8 rows 7.7, 16 rows 9.5 (2.8, and some 2
-// of a launch); 8192 x 8192 11.0, 11.8, 15.7 (5.6); 1024 x 4096 3.3, 4.0, 5.5;
-// 32 rows over 32 experts, 4096 -> 2048 MXFP4, 20.7 (10.6).  With one row the
-// schedulers issue 54% of the time (36 instructions a unit, 18.5 of them the
-// conversions, scales and products themselves, on 3.3 warps a scheduler); two
-// blocks on some SMs and one on others cost another sixth.  Without the products
-// the loop runs at 82% of HBM's rate.
+// TB/s): 8192 x 4096 NVFP4, 1 row 6.8, 8 rows 7.6, 16 rows 9.6 (2.8, and some 2
+// of a launch); 8192 x 8192 10.8, 11.9, 15.8 (5.6); 1024 x 4096 3.2, 4.0, 5.4;
+// 32 rows over 32 experts, 4096 -> 2048 MXFP4, 20.7 (10.6).  No unit is full: HBM
+// 24-42%, issue slots 38-51% (36 instructions a unit with one row and many
+// columns, 18.5 of them the conversions, scales and products themselves), tensor
+// pipe 13-24%.  What is left is latency on 2 to 3.3 warps a scheduler, the start
+// (2 of 5.4 us pass before a warp's first chunk is in), and blocks that are two on
+// some SMs and one on others (a sixth).  Without the products the loop runs at
+// 82% of HBM's rate.
 // The steps (16 x 8192 x 8192 / 1 x 8192 x 4096, us): x staged as fp16 for the
 // whole block, panel by panel 58.8 / 10.7; rings and conversion per warp 24.3 /
 // 11.9; chunks of 256 columns, blocks of two tiles 21.3 / 7.8; copies without
-// tests 18.3 / 7.6; the rare wide chunk out of line, scale words of all tiles in
+// tests 18.3 / 7.6; the path of wide chunks out of line, scale words of all tiles in
 // one copy 17.9 / 7.8; 8 warps of 255 registers 16.6; the first chunk's prefetch
 // 15.7 / 6.8.
 // What did not help: rows of x converted by all lanes together where a tile has
@@ -426,8 +434,8 @@ __device__ __forceinline__ void unscaled(const int (&E)[TILES], F f) {
 // A chunk whose rows of x (as they came, at `xat`) hold elements too small for
 // their largest one's scale: one run over its weights for every kBelow + 1
 // binades, added to `away`.  E and low: exponents of the largest and the
-// smallest element of this lane's row of every tile.  Out of line: hardly ever
-// called, and the loop that calls it keeps its registers.
+// smallest element of this lane's row of every tile.  Out of line, so that the
+// loop that calls it keeps its registers: what it costs is said above.
 template <typename S, int R>
 __device__ __noinline__ void multiply_wide(uint32_t at, uint32_t xat, int tokens, int pairs, const int (&E)[S::TILES],
                                            const int (&low)[S::TILES], float* away) {
@@ -451,7 +459,7 @@ __device__ __noinline__ void multiply_wide(uint32_t at, uint32_t xat, int tokens
 
 // Blocks of an SM that registers are kept for: 16 warps of 128 registers, but for
 // 16 rows on four tiles 8 warps of 255 (16 x 8192 x 4096 NVFP4 11.7 us with 16
-// warps a block, 10.9 with two blocks of 8, 10.3 so).
+// warps a block, 9.6 so; before the prefetch 10.3, and 10.9 with two blocks of 8).
 constexpr int blocks_of(int R, int NT, int W) { return (NT == 0 && R == 1 ? 24 : R == 4 && NT == 2 ? 8 : 16) / W; }
 
 template <int FMT, int R, int NT, int W, bool GATED, bool BF>
@@ -616,7 +624,7 @@ __global__ void __launch_bounds__(32 * W, blocks_of(R, NT, W)) gemv_kernel(const
       for (int n = 0; n < TILES; ++n) own[n] = S::FEW ? of[(lane >> 2) ? S::ROWS - 1 : 0] : of[n];
     };
     bool kept = false;          // sums of an earlier scale have been put away
-    float away[R * TILES * 4];  // in local memory: hardly ever used
+    float away[R * TILES * 4];  // in local memory: used where a scale starts again
     // The sums without their scale to `to`, with what was put away.
     auto put = [&](auto&& to) {
       int own[TILES];
@@ -793,15 +801,16 @@ cudaError_t launch(GemvParams p, cudaStream_t stream) {
 // The block's form by the rows of x and the tiles of 16 rows of w.  More tiles
 // a block (R) spread the conversion of x over more weights, more warps (W) the
 // columns over more of the SM; what serves best is some 2048 warps in all with
-// up to two rows, and blocks for nearly every SM with more.  NVFP4, us, the form
-// taken and the next best: 1 x 16384 x 4096 11.8 and 13.6 (8 warps); 1 x 8192 x
-// 8192 12.1 and 12.9 (4 warps); 1 x 4096 x 16384 12.0 and 13.3 (8 warps); 1 x 1024
-// x 4096 3.6 and 4.2 (two tiles).  8 x 16384 x 4096 12.9 and 14.1 (two tiles); 8 x
-// 8192 x 8192 13.1 and 13.9 (8 warps); 8 x 4096 x 16384 14.6 and 18.1 (8 warps); 8 x
-// 1024 x 4096 4.1 and 5.3 (two tiles).  32 rows over 32 experts 21.0 and 22.6 (8
-// warps).  16 x 8192 x 8192 16.7 and 17.9 (16 warps); 16 x 4096 x 16384 19.1 and 21.9
-// (8 warps); 16 x 1024 x 4096 5.5 and 6.7 (two tiles).  Tiles of 32 rows of x took
-// longer than two runs of 16 (45 and 33 us at 8192 x 8192).
+// up to two rows, and blocks for nearly every SM with more.  Of all forms at 20
+// sizes of 1 to 16 rows the one taken was the best or within 2% of it.  NVFP4, us,
+// the form taken and the best other: 1 x 16384 x 4096 10.8 and 12.3 (8 warps); 1 x 8192 x
+// 8192 10.8 and 11.8 (4 warps); 1 x 4096 x 16384 10.7 and 12.3 (8 warps); 1 x 1024
+// x 4096 3.2 and 3.8 (two tiles).  8 x 16384 x 4096 11.9 and 11.8 (8 warps); 8 x
+// 8192 x 8192 11.9 and 12.3 (8 warps); 8 x 4096 x 16384 13.3 and 15.2 (8 warps); 8 x
+// 1024 x 4096 4.0 and 4.7 (two tiles).  32 rows over 32 experts 21.0 and 22.2 (8
+// warps).  16 x 8192 x 8192 15.8 and 18.9 (two tiles); 16 x 4096 x 16384 18.4 and 20.8
+// (8 warps); 16 x 1024 x 4096 5.4 and 6.5 (two tiles).  Tiles of 32 rows of x took
+// longer than two runs of 16 (45 and 33 us at 8192 x 8192, in an earlier form).
 template <int FMT, bool GATED, bool BF>
 cudaError_t choose(const GemvParams& p, int num_sms, cudaStream_t stream) {
   const int active = p.offsets ? std::min(p.groups, p.T) : 1;

@@ -34,8 +34,8 @@
 //     of 38 KB an SM takes 525 cycles to arrive, its MMAs 512
 //   8192 rows over 16 groups, 4096 -> 2048, bf16: 97 us, 1.42 PFLOP/s; the
 //     weights are read for two tiles of rows only, HBM and MMAs about even
-//   1 x 8192 x 4096 NVFP4: 5.9 us, 2.1 of them a launch with nothing to do; one
-//     SM takes in 64-74 bytes a cycle, and the 64 tiles are on 64 SMs
+//   1 x 8192 x 4096 NVFP4: 5.8 us with the weights in L2, 6.8-7.6 from HBM, 2.1
+//     of them a launch with nothing to do; one SM takes in 64-74 bytes a cycle, and the 64 tiles are on 64 SMs
 //   gated, 8192 rows over 16 groups, 4096 -> 2048, bf16: 183 us, 1.50 PFLOP/s; 8
 //     groups of 2048 rows, 4096 x 4096 with both slopes in fp32 666 us, 1.65
 //     PFLOP/s (power limit; the gradients' products of the same size 631-679)
@@ -143,7 +143,8 @@ struct ProductParams {
 };
 
 // Apart from the others': in every product's parameters they cost each kernel
-// up to 8 registers, and one row of 8192 x 4096 NVFP4 0.5 us (7.3 -> 7.8).
+// up to 8 registers, and one row of 8192 x 4096 NVFP4 (weights from HBM) 0.5 us
+// (7.3 -> 7.8).
 struct GatedParams : ProductParams {
   float* slopes;  // the result's two slopes, [2][T][M], or null
   int64_t lds, slope_plane;
@@ -1357,7 +1358,11 @@ cudaError_t launch(const Product& q, int num_sms, cudaStream_t stream) {
 // single CTAs alone 5%, and more where it counts (pairs and single): 8192^3
 // NVFP4 154 and 234 us; 16 groups of 512 rows, 4096 -> 2048 bf16, 92 and 108;
 // but 1000 x 1537 x 2090 MXFP4 to fp32 8.2 and 6.2, and 32 rows in 32 groups,
-// 4096 -> 2048 NVFP4, 30.0 and 28.5.
+// 4096 -> 2048 NVFP4, 30.0 and 28.5.  The gated product takes the plain one's
+// constants, and ragged groups count too few tiles: over 264 of its sizes, 4 to
+// 8192 rows in 1 to 32 uneven groups, the choice takes 1.0% longer than the better
+// form (pairs alone 8.4%, single CTAs 5.0%), and at 20 of them 6 to 29%: 2000 rows in
+// 4 groups, 1032 -> 520, 18.5 (pairs 14.4); 1000 in 4, 2048 -> 1024, 19.5 (16.4).
 template <ProductOp OP, int FMT>
 cudaError_t choose(const Product& q, int num_sms, cudaStream_t stream) {
   const bool mx = OP == kMx4, sum_rows = OP == kGradWeights;

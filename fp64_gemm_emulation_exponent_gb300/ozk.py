@@ -899,7 +899,8 @@ def grouped_gated_gemm(x, w, offsets, activation: str = "silu", out=None, slopes
     Autograd records it where x or w asks for a gradient
     (grouped_gated_gemm_grad), once: there is no second derivative, and
     forward-mode tangents are refused.  With out or slopes given no graph is
-    recorded.  Both passes can be captured into a CUDA graph, together, and only
+    recorded.  Between the passes the slopes are kept, 8 bytes for an element of
+    h.  Both passes can be captured into a CUDA graph, together, and only
     while no result of an eager pass from the same leaves is alive: autograd
     would take their gradients to that pass's stream, which ends the capture with
     an error, whatever the function."""

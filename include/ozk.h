@@ -508,8 +508,10 @@ int ozk_grouped_gated_gemm(int64_t T, int64_t N, int64_t K, int groups, const in
 
 /* The gradient with respect to the two projections, from that of Y and the
  * slopes: dpre (T x 2 N) has dpre[t, j] = dh_tj dY/dg and dpre[t, N + j] =
- * dh_tj dY/du, each rounded to fp32 and to dtype.  With it as dY, ozk_grouped_gemm_dx
- * and ozk_grouped_gemm_dw (of 2 N rows of w) give the gradients of x and w.
+ * dh_tj dY/du, each rounded to fp32 and to dtype (past its range to Inf, in fp16
+ * also where the gradients of x and w would not be).  With it as dY,
+ * ozk_grouped_gemm_dx and ozk_grouped_gemm_dw (of 2 N rows of w) give the
+ * gradients of x and w.
  * offsets as above, or NULL for all rows; rows in no group are not written.
  * Any alignment of the type. */
 int ozk_gated_grad(int64_t T, int64_t N, int groups, const int32_t* offsets, const void* dH, int64_t lddh,
