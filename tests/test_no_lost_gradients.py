@@ -85,6 +85,26 @@ def test_what_counts_as_a_tangent(monkeypatch):
     assert not refused(x)
 
 
+def test_a_function_with_a_derivative_of_its_own_may_call_them(monkeypatch):
+    """Inside a custom function's forward there are no tangents, and no gradients are recorded."""
+    monkeypatch.setattr(ozk, "_forward_ad", forward_ad)
+
+    class Double(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            ozk._no_tangents("a call", x)
+            assert not torch.is_grad_enabled()
+            return 2 * x
+
+        @staticmethod
+        def jvp(ctx, tangent):
+            return 2 * tangent
+
+    x = torch.ones(3)
+    with forward_ad.dual_level():
+        assert torch.equal(forward_ad.unpack_dual(Double.apply(forward_ad.make_dual(x, x))).tangent, 2 * x)
+
+
 @pytest.mark.gpu
 def test_on_the_gpu():
     """The same calls on real tensors."""
